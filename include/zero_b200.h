@@ -70,7 +70,8 @@ typedef enum {
                             incomplete; steps are refused until a load succeeds */
 } zero_status_t;
 
-typedef enum { ZERO_FP16 = 0, ZERO_BF16 = 1 } zero_dtype_t;
+/* ZERO_FP32 is accepted only where an entry point says so. */
+typedef enum { ZERO_FP16 = 0, ZERO_BF16 = 1, ZERO_FP32 = 2 } zero_dtype_t;
 
 /* Optimizer and mixed-precision settings ([L32] 3.2 and 4.2 DeepSpeed config:
  * optimizer lr, fp16 loss scaling, gradient_clipping).
@@ -481,6 +482,164 @@ zero_status_t zero_offload_step(zero_plan_t plan, const void* grads, float* mast
 zero_status_t zero_cpu_adam(const void* grads16, zero_dtype_t dtype, uint64_t n, float loss_scale,
                             float clip_coef, float bc1, float bc2, const zero_hparams_t* hp,
                             float* master, float* m, float* v, void* params16, int nthreads);
+
+/* ---- 8-bit activation checkpoints -------------------------------------------- */
+
+/* [L18] part 4 and [PZ] part 6 name the activations kept for the backward pass as
+ * the next memory after the sharded model state (checkpointing them, and
+ * partitioning the checkpoints over ranks).  These calls keep an activation
+ * matrix in 8 bits per element and use it in the backward pass without first
+ * expanding it; the gradients they produce go straight into a rank's row of
+ * zero_step's gradients.  The pages fix no format; this is the library's own:
+ *
+ *   A matrix of `cols` columns is stored row by row, zero_act_row_bytes(cols)
+ *   bytes apart: with C = cols rounded up to 32, C code bytes (two's complement,
+ *   |code| <= 127, 0 past cols), then C/32 exponent bytes, then zeros up to a
+ *   multiple of 32 bytes.  Codes and exponent E of a block of 32 consecutive
+ *   columns stand for code * 2^(E - 127).  E is the smallest exponent with
+ *   max|x| <= 127 * 2^(E - 127), kept in [103, 136] for fp16 and [1, 248] for
+ *   bf16 and fp32 inputs; code = round_half_even(x * 2^(127 - E)), clamped to
+ *   +-127.  A block that holds an inf or a NaN has E = 255 and zero codes and
+ *   reads back as NaN in all its columns (so the overflow flag of the step that
+ *   receives the gradients is raised).
+ * The scale is a power of two so that the value of a code is exact in the 16-bit
+ * type: what a tensor core multiplies is the checkpoint's value itself.
+ * Rows are independent: a range of rows of a checkpoint is a checkpoint. */
+
+/* Most columns of a checkpointed matrix. */
+#define ZERO_ACT_MAX_COLS (1ll << 24)
+
+/* Bytes from one row of a checkpoint to the next (a matrix takes rows times
+ * that); 0 if cols < 1 or cols > ZERO_ACT_MAX_COLS. */
+uint64_t zero_act_row_bytes(int64_t cols);
+
+/* Checkpoint x (dtype fp16, bf16 or fp32; rows ld elements apart, aligned to its
+ * element; 16-byte aligned rows are read fastest).  Asynchronous.  rows = 0 is
+ * accepted.  Errors: ZERO_EINVAL (dtype, sizes: rows in [0, 2^31), ld >= cols;
+ * null or misaligned pointer), ZERO_ECUDA. */
+zero_status_t zero_act_save(zero_dtype_t dtype, const void* x, int64_t rows, int64_t cols,
+                            int64_t ld, void* ckpt, void* stream);
+
+/* The values of a checkpoint, rounded to dtype (exact when dtype is the type that
+ * was saved, or fp32), into out (rows ld elements apart, aligned to its element).
+ * Asynchronous.  Errors: as zero_act_save. */
+zero_status_t zero_act_load(zero_dtype_t dtype, const void* ckpt, int64_t rows, int64_t cols,
+                            void* out, int64_t ld, void* stream);
+
+/* The gradient of a linear layer's weight from the gradient of its output and
+ * the checkpoint of its input.  With xh the checkpoint's values [tokens][k],
+ *   dw[i][j] = sum_t dy[t][i] * (xh[t][j] * col_scale[j] + col_shift[j])
+ *   db[i]    = sum_t dy[t][i]
+ * summed in fp32.  col_scale and col_shift (dtype, [k]; NULL: 1 and 0) are the
+ * weight and bias of a norm whose normalised rows were checkpointed, so one
+ * checkpoint serves the norm's backward pass and every layer it feeds.
+ *   dtype       fp16 or bf16: dy, col_scale, col_shift.  An fp16 dy needs a
+ *               checkpoint saved as fp16 (block exponents outside fp16's range
+ *               read as NaN).
+ *   dy          [tokens] rows of n elements, ldy apart.
+ *   grad_dtype  of dw and db: dtype, or fp32.
+ *   dw          [n] rows of k elements, ldw apart (e.g. a tensor's place in a
+ *               rank's gradient row); db [n], NULL: not wanted.
+ *   accumulate  1: the sums are added to what dw and db hold (one rounding);
+ *               0: overwritten.
+ *   work        zero_act_wgrad_workspace(tokens, n, k) bytes, 16-byte aligned.
+ *               The caller zeroes it once, before the first use (with any sizes);
+ *               every call leaves it ready for the next.  Calls whose executions
+ *               overlap need a workspace each.
+ * Matrices need the alignment of their element; 16-byte aligned dy rows are read
+ * by TMA and 16-byte aligned dw rows are written in vectors, others element by
+ * element.  tokens = 0 is accepted (the sums are zero).  Sums are taken in a
+ * fixed order: equal inputs give equal bits.  Asynchronous.  A bounded device
+ * wait that gives up (none should) sets the first int32 of `work` to
+ * ZERO_ETIMEOUT and writes NaN where the sums are missing.
+ * Errors: ZERO_EINVAL (types, sizes: tokens in [0, 2^31), n in [1, 2^24], k in
+ * [1, ZERO_ACT_MAX_COLS], ldy >= n, ldw >= k; null or misaligned pointer),
+ * ZERO_ECUDA. */
+zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int64_t tokens, int64_t n,
+                             int64_t ldy, const void* ckpt, int64_t k, const void* col_scale,
+                             const void* col_shift, zero_dtype_t grad_dtype, void* dw, int64_t ldw,
+                             void* db, int accumulate, void* work, void* stream);
+
+/* Workspace bytes of zero_act_wgrad; 0 on invalid sizes. */
+uint64_t zero_act_wgrad_workspace(int64_t tokens, int64_t n, int64_t k);
+
+/* ---- norms around a block, with its gate and residual scale ------------------- */
+
+typedef enum { ZERO_NORM_NONE = 0, ZERO_NORM_RMS = 1, ZERO_NORM_LAYER = 2 } zero_norm_kind_t;
+
+/* Most columns of a norm's rows. */
+#define ZERO_NORM_MAX_COLS 16384
+
+/* What stands between one block's output y and the next block's input x, on a
+ * residual stream h (each row of `cols` elements on its own):
+ *   yh = post-norm of y without weights        (ZERO_NORM_NONE: yh = y)
+ *   z  = post_w yh + post_b
+ *   h' = h + alpha * gate * z
+ *   xh = pre-norm of h' without weights
+ *   x  = pre_w xh + pre_b
+ * where ZERO_NORM_RMS divides a row by sqrt(mean(v^2) + eps) and
+ * ZERO_NORM_LAYER first subtracts the row's mean.  All in fp32, each output
+ * rounded once; xh is taken of the unrounded h'.
+ *   dtype       fp16 or bf16: y, x, weights, gate and their gradients' inputs.
+ *   res_dtype   of the residual stream (h, h', their gradients): dtype or fp32.
+ *   post, pre   zero_norm_kind_t; pre = ZERO_NORM_NONE: no x.
+ *   alpha       residual scale (finite).  eps >= 0.
+ *   group_rows  rows that share a row of the gate (e.g. a sequence's length): row
+ *               i uses gate row i / group_rows; 0: one gate row for all.
+ *   post_w, post_b, pre_w, pre_b   [cols]; NULL: 1 (weights), 0 (biases).  They
+ *               belong to a norm: with ZERO_NORM_NONE they have to be NULL.
+ *   gate        [ceil(rows / group_rows)][cols], contiguous; NULL: 1.
+ * Pointers need the alignment of their element (16-byte aligned rows are
+ * fastest); checkpoints and statistics 16 bytes. */
+typedef struct {
+    int32_t dtype, res_dtype, post, pre;
+    int64_t rows, cols, group_rows;
+    float   eps, alpha;
+    const void *post_w, *post_b, *gate, *pre_w, *pre_b;
+} zero_norm_t;
+
+/* The forward pass.  h [rows] rows ldh apart, and y; y = NULL: no block yet, h' = h
+ * (h_out may then be NULL, and post, gate, ckpt_y have to be none).  h_out may be
+ * h itself.  x: NULL iff pre is ZERO_NORM_NONE.
+ * For the backward pass (all may be NULL when there is none):
+ *   ckpt_y   8-bit checkpoint of yh, ckpt_x of xh (the format above; the limits of
+ *            dtype's exponents apply);
+ *   stats    [rows][4] fp32: mean and 1/deviation of the post-norm, then of the
+ *            pre-norm (0 and 1 where there is none).
+ * Asynchronous.  rows = 0 is accepted.  Errors: ZERO_EINVAL (description, sizes:
+ * rows in [0, 2^31), cols in [1, ZERO_NORM_MAX_COLS]; strides below cols; null or
+ * misaligned pointer), ZERO_ECUDA. */
+zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* h, int64_t ldh, const void* y,
+                                int64_t ldy, void* h_out, int64_t ldho, void* x, int64_t ldx,
+                                void* ckpt_y, void* ckpt_x, float* stats, void* stream);
+
+/* The backward pass, with yh and xh read from the checkpoints.  dh_out is the
+ * gradient of h' from later use of the residual stream (NULL: zero), dx that of x
+ * (NULL iff pre is none).  With r and the means from stats,
+ *   D  = dh_out + r1 (pre_w dx - [mean(pre_w dx)] - xh mean(pre_w dx xh))
+ *   dh = D
+ *   dz = alpha gate D
+ *   dy = r2 (post_w dz - [mean(post_w dz)] - yh mean(post_w dz yh))  (dz if none)
+ * ([] for ZERO_NORM_LAYER), and summed over rows
+ *   dpre_w = sum dx xh, dpre_b = sum dx, dpost_w = sum dz yh, dpost_b = sum dz,
+ *   dgate[group] = sum over the group's rows of alpha D z.
+ * dh may be dh_out itself, dy may be NULL (a stream without a block yet: ckpt_y,
+ * post, gate none).  ckpt_y is needed if post is a norm or dgate is wanted.
+ * dpost_w ... dpre_b [cols], dgate [groups][cols]: grad_dtype (dtype or fp32),
+ * NULL where not wanted; accumulate as in zero_act_wgrad.  The gradients of a NULL
+ * weight may be asked for too.  work: zero_norm_workspace(norm) bytes, 16-byte
+ * aligned, contents ignored; calls whose executions overlap need one each.
+ * Sums are taken in a fixed order: equal inputs give equal bits.  Asynchronous.
+ * Errors: as zero_norm_forward. */
+zero_status_t zero_norm_backward(const zero_norm_t* norm, const void* dh_out, int64_t lddho,
+                                 const void* dx, int64_t lddx, const void* ckpt_y,
+                                 const void* ckpt_x, const float* stats, void* dh, int64_t lddh,
+                                 void* dy, int64_t lddy, zero_dtype_t grad_dtype, void* dpost_w,
+                                 void* dpost_b, void* dgate, void* dpre_w, void* dpre_b,
+                                 int accumulate, void* work, void* stream);
+
+/* Workspace bytes of zero_norm_backward; 0 on an invalid description. */
+uint64_t zero_norm_workspace(const zero_norm_t* norm);
 
 /* ---- memory ledger and communication volume ------------------------------- */
 

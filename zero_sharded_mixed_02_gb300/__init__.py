@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(_DIR, "libzero_b200.so")
 (ZERO_OK, ZERO_EINVAL, ZERO_ENOMEM, ZERO_ECUDA, ZERO_ETIMEOUT, ZERO_ENOENT, ZERO_ECORRUPT,
  ZERO_EIO, ZERO_ESTATE) = range(9)
 ZERO_CKPT_FSYNC, ZERO_CKPT_DROP_CACHE = 1, 2
-ZERO_FP16, ZERO_BF16 = 0, 1
+ZERO_FP16, ZERO_BF16, ZERO_FP32 = 0, 1, 2
+ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_NORM_LAYER = 0, 1, 2
 PATH_FUSED, PATH_G32, PATH_RECOMPUTE = 0, 1, 2
 
 # every entry point declared in include/zero_b200.h
@@ -38,6 +39,8 @@ ENTRY_POINTS = (
     "zero_grad_norm_noalloc", "zero_plan_set_reduce_kernel", "zero_quantize_shard",
     "zero_gather_layer_q", "zero_plan_set_bucket", "zero_step_bucket", "zero_step_apply",
     "zero_checkpoint_save", "zero_checkpoint_load", "zero_offload_step", "zero_cpu_adam",
+    "zero_act_row_bytes", "zero_act_save", "zero_act_load", "zero_act_wgrad",
+    "zero_act_wgrad_workspace", "zero_norm_forward", "zero_norm_backward", "zero_norm_workspace",
 )
 
 
@@ -62,6 +65,25 @@ def hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, decoupl
     return zero_hparams_t(lr, beta1, beta2, eps, weight_decay, decoupled_wd, clip_norm,
                           loss_scale, dynamic_scale, backoff, growth_interval,
                           skip_on_overflow)
+
+
+class zero_norm_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group_rows", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("post_w", ctypes.c_void_p), ("post_b", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("pre_w", ctypes.c_void_p), ("pre_b", ctypes.c_void_p)]
+
+
+def norm(dtype, rows, cols, res_dtype=None, post=ZERO_NORM_NONE, pre=ZERO_NORM_RMS, eps=1e-5,
+         alpha=1.0, group_rows=0, post_w=None, post_b=None, gate=None, pre_w=None,
+         pre_b=None) -> zero_norm_t:
+    """Description of a block boundary for zero_norm_forward/backward.  It holds raw device
+    pointers: the caller keeps the weights alive."""
+    return zero_norm_t(dtype, dtype if res_dtype is None else res_dtype, post, pre, rows, cols,
+                       group_rows, eps, alpha, _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(pre_w),
+                       _ptr(pre_b))
 
 
 _lock = threading.Lock()
@@ -122,6 +144,18 @@ def lib():
                 "zero_cpu_adam": (st, [_P, ctypes.c_int, _U64, ctypes.c_float, ctypes.c_float,
                                        ctypes.c_float, ctypes.c_float, _P, _P, _P, _P, _P,
                                        ctypes.c_int]),
+                "zero_act_row_bytes": (_U64, [_I64]),
+                "zero_act_save": (st, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P]),
+                "zero_act_load": (st, [ctypes.c_int, _P, _I64, _I64, _P, _I64, _P]),
+                "zero_act_wgrad": (st, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _I64, _P, _P,
+                                        ctypes.c_int, _P, _I64, _P, ctypes.c_int, _P, _P]),
+                "zero_act_wgrad_workspace": (_U64, [_I64, _I64, _I64]),
+                "zero_norm_forward": (st, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P,
+                                           _P]),
+                "zero_norm_backward": (st, [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64,
+                                            ctypes.c_int, _P, _P, _P, _P, _P, ctypes.c_int, _P,
+                                            _P]),
+                "zero_norm_workspace": (_U64, [_P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -326,6 +360,54 @@ def zero_gather_layer_q(plan: int, unit: int, bits: int, code_ptrs: Sequence,
     s = (ctypes.c_void_p * max(1, len(scale_ptrs)))(*[_ptr(p) for p in scale_ptrs])
     _check(lib().zero_gather_layer_q(plan, unit, bits, ctypes.addressof(c), ctypes.addressof(s),
                                      _ptr(out), _ptr(stream)), "zero_gather_layer_q")
+
+
+def zero_act_row_bytes(cols: int) -> int:
+    return lib().zero_act_row_bytes(cols)
+
+
+def zero_act_save(dtype: int, x, rows: int, cols: int, ld: int, ckpt, stream=0) -> None:
+    _check(lib().zero_act_save(dtype, _ptr(x), rows, cols, ld, _ptr(ckpt), _ptr(stream)),
+           "zero_act_save")
+
+
+def zero_act_load(dtype: int, ckpt, rows: int, cols: int, out, ld: int, stream=0) -> None:
+    _check(lib().zero_act_load(dtype, _ptr(ckpt), rows, cols, _ptr(out), ld, _ptr(stream)),
+           "zero_act_load")
+
+
+def zero_act_wgrad(dtype: int, dy, tokens: int, n: int, ldy: int, ckpt, k: int, col_scale, col_shift,
+                   grad_dtype: int, dw, ldw: int, db, accumulate: int, work, stream=0) -> None:
+    """work: zero_act_wgrad_workspace(tokens, n, k) bytes, zeroed once by the caller."""
+    _check(lib().zero_act_wgrad(dtype, _ptr(dy), tokens, n, ldy, _ptr(ckpt), k, _ptr(col_scale),
+                                _ptr(col_shift), grad_dtype, _ptr(dw), ldw, _ptr(db), accumulate,
+                                _ptr(work), _ptr(stream)), "zero_act_wgrad")
+
+
+def zero_act_wgrad_workspace(tokens: int, n: int, k: int) -> int:
+    return lib().zero_act_wgrad_workspace(tokens, n, k)
+
+
+def zero_norm_forward(norm: zero_norm_t, h, ldh: int, y, ldy: int, h_out, ldho: int, x, ldx: int,
+                      ckpt_y=None, ckpt_x=None, stats=None, stream=0) -> None:
+    _check(lib().zero_norm_forward(ctypes.byref(norm), _ptr(h), ldh, _ptr(y), ldy, _ptr(h_out), ldho,
+                                   _ptr(x), ldx, _ptr(ckpt_y), _ptr(ckpt_x), _ptr(stats),
+                                   _ptr(stream)), "zero_norm_forward")
+
+
+def zero_norm_backward(norm: zero_norm_t, dh_out, lddho: int, dx, lddx: int, ckpt_y, ckpt_x, stats,
+                       dh, lddh: int, dy, lddy: int, grad_dtype: int, dpost_w=None, dpost_b=None,
+                       dgate=None, dpre_w=None, dpre_b=None, accumulate: int = 0, work=None,
+                       stream=0) -> None:
+    _check(lib().zero_norm_backward(ctypes.byref(norm), _ptr(dh_out), lddho, _ptr(dx), lddx,
+                                    _ptr(ckpt_y), _ptr(ckpt_x), _ptr(stats), _ptr(dh), lddh,
+                                    _ptr(dy), lddy, grad_dtype, _ptr(dpost_w), _ptr(dpost_b),
+                                    _ptr(dgate), _ptr(dpre_w), _ptr(dpre_b), accumulate, _ptr(work),
+                                    _ptr(stream)), "zero_norm_backward")
+
+
+def zero_norm_workspace(norm: zero_norm_t) -> int:
+    return lib().zero_norm_workspace(ctypes.byref(norm))
 
 
 def zero_state_bytes(psi: int, nd: int, stage: int, K: int = 12) -> int:

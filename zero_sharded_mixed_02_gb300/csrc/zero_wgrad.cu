@@ -2,38 +2,564 @@
 // output and the 8-bit checkpoint of its input: dw = dy^T xh, db = the column sums
 // of dy (include/zero_b200.h).
 //
-// First form: a 64 x 64 tile of dw per block on the fp32 pipes, 16 tokens at a time
-// through shared memory.
+// dw is a matrix product whose contraction runs over tokens, bound by the 16-bit
+// tensor cores (2 tokens n k operations) once there are more than a few hundred
+// tokens.  The checkpoint's values are exact in the 16-bit type, so they are widened
+// into the tensor cores' shared-memory operand and multiplied as they are.
+//
+// A pair of SMs (a cluster of two) computes a 256 x 256 tile of dw, 64 tokens at a
+// time: each SM's 128 rows of dy^T come by TMA in the layout the tensor cores read
+// (both operands have the non-contracted axis contiguous, so nothing is transposed),
+// its 128 columns of codes and their exponents come by TMA as bytes, eight warps
+// widen the codes into the second operand, and one thread of the pair issues the
+// products, which accumulate in tensor memory.  With two accumulators, four other
+// warps write one tile out while the next is summed.
+//
+// Tiles are dealt to the pairs in whole waves, where all pairs work on the same
+// tokens at the same time and share their panels in L2; the tiles of an incomplete
+// last wave are cut along the token axis into equal parts, one for each pair.  Parts
+// go to the workspace and a second kernel adds them in token order, so the sums do
+// not depend on timing.
+#include <cuda.h>
+
+#include <mutex>
+
 #include "zero_act.cuh"
 #include "zero_b200.h"
+#include "zero_tma.cuh"
 #include "zero_trace.h"
 
 namespace zero {
+
+#define ZERO_WG_TILE 256                    // rows and columns of a pair's tile
+#define ZERO_WG_TOK 64                      // tokens of a stage
+#define ZERO_WG_STAGES 5
+#define ZERO_WG_THREADS 512                 // warps 0 TMA, 1 products, 4-7 output, 8-15 widening
+#define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
+#define ZERO_WG_PART 8                      // least stages of a part of a cut tile
+#define ZERO_WG_SUMS 16                     // token ranges of the column sums
+
+// bytes of a stage in one SM: dy rows, codes, exponents, widened codes
+#define ZERO_WG_A 16384
+#define ZERO_WG_C 8192
+#define ZERO_WG_E 1024
+#define ZERO_WG_STAGE (2 * ZERO_WG_A + ZERO_WG_C + ZERO_WG_E)
+#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + 1024)
+#define ZERO_WG_SLOT (ZERO_WG_TILE * ZERO_WG_TILE)     // floats of a part
 
 struct WgradArgs {
     const uint16_t* dy;
     const uint8_t* ckpt;
     const uint16_t *scale, *shift;
     void *dw, *db;
+    int32_t* err;
+    float *sums, *slots;                    // column sums [ZERO_WG_SUMS][n]; parts
     int64_t tokens, n, k, ldy, ldw;
-    int64_t wide, stride;
-    int grad_dtype, accumulate;
+    int64_t wide;
+    int64_t tiles, steps;                   // steps: stages of a tile
+    int tiles_n, tiles_k, pairs, waves, rest, rest_pairs;
+    int grad_dtype, accumulate, vec;
 };
 
+// ---- the division of the work ------------------------------------------------------
+struct WgradSegment {
+    int64_t tile, s0, s1;                   // stages [s0, s1) of a tile
+    int slot;                               // -1: the whole tile, else its part's place
+};
+
+// Segment i of a pair; false past its last.
+static __host__ __device__ __forceinline__ bool wgrad_segment(const WgradArgs& a, int pair, int i, WgradSegment& g)
+{
+    if (i < a.waves) {
+        g.tile = (int64_t)i * a.pairs + pair;
+        g.s0 = 0;
+        g.s1 = a.steps;
+        g.slot = -1;
+        return true;
+    }
+    if (pair >= a.rest_pairs) return false;
+    const int64_t units = (int64_t)a.rest * a.steps;
+    const int64_t u0 = pair * units / a.rest_pairs, u1 = (pair + 1) * units / a.rest_pairs;
+    const int64_t t = u0 / a.steps + (i - a.waves);
+    int64_t b = t * a.steps, e = b + a.steps;
+    if (b >= u1) return false;
+    b = b > u0 ? b : u0;
+    e = e < u1 ? e : u1;
+    g.tile = (int64_t)a.waves * a.pairs + t;
+    g.s0 = b - t * a.steps;
+    g.s1 = e - t * a.steps;
+    g.slot = g.s1 - g.s0 == a.steps ? -1 : 2 * pair + (i - a.waves);
+    return true;
+}
+
+// Tiles in an order that keeps a wave's panels few: bands of eight tiles along n.
+static __device__ __forceinline__ void wgrad_place(const WgradArgs& a, int64_t tile, int64_t& i0, int64_t& j0)
+{
+    const int64_t band = tile / (8ll * a.tiles_k), in = tile - band * 8 * a.tiles_k;
+    const int64_t high = a.tiles_n - band * 8 < 8 ? a.tiles_n - band * 8 : 8;
+    j0 = in / high * ZERO_WG_TILE;
+    i0 = (band * 8 + in % high) * ZERO_WG_TILE;
+}
+
+// ---- output ------------------------------------------------------------------------
+static __device__ __forceinline__ float grad_in(const void* p, int64_t i, int grad_dtype)
+{
+    if (grad_dtype == 2) return static_cast<const float*>(p)[i];
+    const uint16_t u = static_cast<const uint16_t*>(p)[i];
+    return grad_dtype == 0 ? widen1<0>(u) : widen1<1>(u);
+}
 static __device__ __forceinline__ void put_grad(void* p, int64_t i, float v, int grad_dtype, int accumulate)
 {
-    if (grad_dtype == 2) {
-        float* o = static_cast<float*>(p) + i;
-        *o = accumulate ? *o + v : v;
-    } else {
-        uint16_t* o = static_cast<uint16_t*>(p) + i;
-        if (accumulate) v += grad_dtype == 0 ? widen1<0>(*o) : widen1<1>(*o);
-        *o = grad_dtype == 0 ? narrow1<0>(v) : narrow1<1>(v);
+    if (accumulate) v += grad_in(p, i, grad_dtype);
+    if (grad_dtype == 2) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = grad_dtype == 0 ? narrow1<0>(v) : narrow1<1>(v);
+}
+
+// 32 columns from j of row i; s the row's column sum of dy.
+template <int DT>
+static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, int64_t j, float (&v)[32], float s)
+{
+    if (i >= a.n || j >= a.k) return;
+    const int m = a.k - j < 32 ? (int)(a.k - j) : 32;
+    if (a.scale || a.shift)
+#pragma unroll
+        for (int c = 0; c < 32; c++)
+            if (c < m) {
+                if (a.scale) v[c] *= widen1<DT>(__ldg(a.scale + j + c));
+                if (a.shift) v[c] = __fmaf_rn(s, widen1<DT>(__ldg(a.shift + j + c)), v[c]);
+            }
+    const int64_t at = i * a.ldw + j;
+    if (a.vec && m == 32) {
+        if (a.grad_dtype == 2) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                float4 q = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                if (a.accumulate) {
+                    const float4 p = o[c / 4];
+                    q = make_float4(q.x + p.x, q.y + p.y, q.z + p.z, q.w + p.w);
+                }
+                o[c / 4] = q;
+            }
+        } else {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dw) + at);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                if (a.accumulate) {
+                    const uint4 p = o[c / 8];
+                    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        float lo, hi;
+                        widen2<DT>(w[e], lo, hi);
+                        v[c + 2 * e] += lo;
+                        v[c + 2 * e + 1] += hi;
+                    }
+                }
+                o[c / 8] = make_uint4(narrow2<DT>(v[c], v[c + 1]), narrow2<DT>(v[c + 2], v[c + 3]),
+                                      narrow2<DT>(v[c + 4], v[c + 5]), narrow2<DT>(v[c + 6], v[c + 7]));
+            }
+        }
+        return;
     }
+#pragma unroll
+    for (int c = 0; c < 32; c++)
+        if (c < m) put_grad(a.dw, at + c, v[c], a.grad_dtype, a.accumulate);
+}
+
+static __device__ __forceinline__ float column_sum(const WgradArgs& a, int64_t i)
+{
+    float s = 0.0f;
+    if ((a.shift || a.db) && i < a.n)
+        for (int p = 0; p < ZERO_WG_SUMS; p++) s += __ldg(a.sums + p * a.n + i);
+    return s;
+}
+
+// ---- the pair's machinery ------------------------------------------------------------
+static __device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+static __device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrive on the barrier of the pair's first SM that lies at this SM's address `bar`.
+static __device__ __forceinline__ void arrive_first(uint32_t bar)
+{
+    asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
+                 " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
+}
+static __device__ __forceinline__ uint32_t try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok;
+}
+// Bounded wait: false when it gave up (here or in another warp of this SM).
+static __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
+{
+    for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT; it++) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if (*dead) return false;
+    }
+    *dead = 1;
+    atomicExch(err, ZERO_ETIMEOUT);
+    return false;
+}
+static __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// Completion of every product issued so far arrives on `bar` in both SMs.
+static __device__ __forceinline__ void commit_both(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+// Operand in shared memory with the non-contracted axis contiguous, 128-byte swizzle:
+// groups of 64 columns are 8192 bytes apart, groups of 8 tokens 1024.
+static __device__ __forceinline__ uint64_t operand(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+static __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(what), "r"((uint32_t)add) : "memory");
+}
+static __device__ __forceinline__ void read_accumulator(uint32_t at, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+
+// Two codes (bytes 0 and 1, or 2 and 3, of w) times their block's 2^e, as a 16-bit pair.
+// bf16: with l the code's low seven bits, 0x4300 | l is 128 + l, and 0x4300 with the
+// code's sign bit in place 7 is 128 or 256; the difference is the code.  fp16: 1024 plus
+// the code XOR 128 in the mantissa, less 1152.  Difference and product are exact.
+template <int DT>
+static __device__ __forceinline__ uint32_t widen_codes(uint32_t w, uint32_t select, uint32_t scale)
+{
+    if (DT == 1) {
+        const uint32_t x = __byte_perm(w, 0x43434343u, select);
+        const uint32_t t = x & 0xFF7FFF7Fu, u = x & 0xFF80FF80u;
+        const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&u));
+        const __nv_bfloat162 r = __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&scale));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const uint32_t x = __byte_perm(w, 0x64646464u, select), bias = 0x64806480u;     // 1152
+    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
+    const __half2 r = __hmul2(c, *reinterpret_cast<const __half2*>(&scale));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 2^(E - 127) twice in the 16-bit type.  E = 0 is no block's (a row past the last token):
+// 0.  255 gives inf, and 0 * inf = NaN; exponents that fp16 does not have give NaN.
+template <int DT>
+static __device__ __forceinline__ uint32_t code_scale(uint32_t e)
+{
+    uint32_t s;
+    if (DT == 1) {
+        s = e << 7;
+    } else {
+        s = __half_as_ushort(__float2half_rn(__uint_as_float(e << 23)));
+        if (e != 0 && e != ZERO_ACT_BAD && (e < 103 || e > 136)) s = 0x7FFF;
+    }
+    return s | s << 16;
+}
+
+struct WgradShared {
+    uint64_t full[ZERO_WG_STAGES];          // a stage's bytes have come
+    uint64_t ready[ZERO_WG_STAGES];         // both SMs' operands are in place (first SM's)
+    uint64_t empty[ZERO_WG_STAGES];         // the stage's products are done
+    uint64_t sum_full[2], sum_empty[2];     // accumulators
+    uint64_t drain;                         // products in flight after a wait gave up
+    uint32_t tmem;
+    int dead;
+};
+
+template <int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
+    k_wgrad(const __grid_constant__ WgradArgs a, const __grid_constant__ CUtensorMap map_y,
+            const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_e)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ WgradShared sh;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    volatile int* dead = &sh.dead;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ZERO_WG_STAGES; s++) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.ready[s]), 16);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(smem_u32(&sh.sum_full[s]), 1);
+            mbar_init(smem_u32(&sh.sum_empty[s]), 8);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
+                     "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+    WgradSegment g;
+
+    if (warp == 0) {
+        // ---- loads ----
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
+                int64_t i0, j0;
+                wgrad_place(a, g.tile, i0, j0);
+                const int x = (int)(i0 + rank * 128), c = (int)(j0 + rank * 128);
+                const int e = (int)a.wide + (c / 32 & ~15);
+                for (int64_t t = g.s0; t < g.s1; t++) {
+                    if (issued >= ZERO_WG_STAGES && !pair_wait(smem_u32(&sh.empty[s]), ph ^ 1u, dead, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = base + s * ZERO_WG_STAGE, bar = smem_u32(&sh.full[s]);
+                    const int y = (int)(t * ZERO_WG_TOK);
+                    mbar_expect_tx(bar, ZERO_WG_A + ZERO_WG_C + ZERO_WG_E);
+                    tma_box(at, &map_y, x, y, bar);
+                    tma_box(at + 8192, &map_y, x + 64, y, bar);
+                    tma_box(at + 2 * ZERO_WG_A, &map_c, c, y, bar);
+                    tma_box(at + 2 * ZERO_WG_A + ZERO_WG_C, &map_e, e, y, bar);
+                    issued++;
+                    if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            // the last stages: their copies have landed and their products are done before
+            // this SM's shared memory is given back
+            for (int64_t q = issued > ZERO_WG_STAGES ? issued - ZERO_WG_STAGES : 0; q < issued; q++) {
+                const int k = (int)(q % ZERO_WG_STAGES);
+                const uint32_t parity = (uint32_t)(q / ZERO_WG_STAGES & 1);
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !try_wait_cluster(smem_u32(&sh.full[k]), parity); it++) {
+                }
+                if (!*dead) pair_wait(smem_u32(&sh.empty[k]), parity, dead, a.err);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products (the first SM's thread, for both) ----
+        if (lane == 0 && rank == 0) {
+            // fp32 sums of fp16/bf16 operands, both with the contracted axis strided, 256 x 256
+            const uint32_t what = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | 1u << 15 | 1u << 16 |
+                                  (uint32_t)(ZERO_WG_TILE >> 3) << 17 | (uint32_t)(ZERO_WG_TILE >> 4) << 24;
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
+                const int acc = i & 1;
+                if (i >= 2 && !pair_wait(smem_u32(&sh.sum_empty[acc]), (uint32_t)((i >> 1) - 1) & 1u, dead, a.err)) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int64_t t = g.s0; t < g.s1; t++) {
+                    if (!pair_wait(smem_u32(&sh.ready[s]), ph, dead, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t at = base + s * ZERO_WG_STAGE;
+                    const uint64_t da = operand(at), db = operand(at + ZERO_WG_A);
+#pragma unroll
+                    for (int q = 0; q < ZERO_WG_TOK / 16; q++)
+                        product(tmem + acc * ZERO_WG_TILE, da + q * (2048 >> 4), db + q * (2048 >> 4), what,
+                                t > g.s0 || q > 0);
+                    commit_both(smem_u32(&sh.empty[s]));
+                    if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (ok) commit_both(smem_u32(&sh.sum_full[acc]));
+            }
+            if (*dead) {                                     // let the products in flight finish
+                commit_both(smem_u32(&sh.drain));
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !try_wait_cluster(smem_u32(&sh.drain), 0); it++) {
+                }
+            }
+        }
+    } else if (warp >= 8) {
+        // ---- codes to 16-bit values: a thread takes one token's block of 32 columns ----
+        // The order in which a thread takes its block's halves (h) makes the eight lanes of
+        // each shared-memory access fall on different 16-byte columns, reading and writing.
+        const int w = threadIdx.x - 256, blk = w & 3, tok = w >> 2;
+        const int h = (blk >> 1) ^ (tok & 1);
+        const uint32_t from = tok * 128 + blk * 32, row = (blk >> 1) * 8192 + tok * 128;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
+            int64_t i0, j0;
+            wgrad_place(a, g.tile, i0, j0);
+            const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * 128) / 32 & 15) + blk;
+            for (int64_t t = g.s0; t < g.s1; t++) {
+                if (!pair_wait(smem_u32(&sh.full[s]), ph, dead, a.err)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = base + s * ZERO_WG_STAGE, codes = at + 2 * ZERO_WG_A;
+                uint32_t e, q[2][4];
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(codes + ZERO_WG_C + eat));
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(q[c][0]), "=r"(q[c][1]), "=r"(q[c][2]), "=r"(q[c][3])
+                                 : "r"(codes + from + 16 * (c ^ h)));
+                const uint32_t sc = code_scale<DT>(e);
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+#pragma unroll
+                    for (int p = 0; p < 2; p++) {              // eight codes -> 16 bytes
+                        uint32_t r[4];
+#pragma unroll
+                        for (int d = 0; d < 4; d++) {
+                            const uint32_t x = DT == 1 ? q[c][2 * p + d / 2] : q[c][2 * p + d / 2] ^ 0x80808080u;
+                            r[d] = widen_codes<DT>(x, d & 1 ? 0x4342 : 0x4140, sc);
+                        }
+                        const uint32_t col = ((blk & 1) * 4 + 2 * (c ^ h) + p) ^ (tok & 7);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(at + ZERO_WG_A + row + 16 * col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                                     : "memory");
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_first(smem_u32(&sh.ready[s]));
+                if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- output: warp w has rows 32 (w - 4) + lane of this SM's half ----
+        for (int i = 0; wgrad_segment(a, pair, i, g); i++) {
+            const int acc = i & 1;
+            int64_t i0, j0;
+            wgrad_place(a, g.tile, i0, j0);
+            const int64_t r = i0 + rank * 128 + (warp - 4) * 32 + lane;
+            // a wait that gave up in any lane leaves the whole warp without the sums
+            const bool have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, a.err));
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const float sum = g.slot < 0 ? column_sum(a, r) : 0.0f;
+            if (g.slot < 0 && a.db && j0 == 0 && r < a.n)
+                put_grad(a.db, r, have ? sum : __uint_as_float(0x7FC00000u), a.grad_dtype, a.accumulate);
+            for (int c = 0; c < ZERO_WG_TILE / 32; c++) {
+                float v[32];
+                if (have) {
+                    read_accumulator(tmem + acc * ZERO_WG_TILE + c * 32 + ((uint32_t)(warp - 4) << 21), v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) v[e] = __uint_as_float(0x7FC00000u);
+                }
+                if (g.slot < 0) {
+                    put_row<DT>(a, r, j0 + c * 32, v, sum);
+                } else {                                      // four columns of 32 rows: one run of 512 bytes
+                    float4* o = reinterpret_cast<float4*>(a.slots + (int64_t)g.slot * ZERO_WG_SLOT) +
+                                ((rank * 4 + warp - 4) * 64 + c * 8) * 32 + lane;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) o[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Adds the parts of the cut tiles in token order and writes them out: a warp takes 32
+// rows and 32 columns of a tile.
+template <int DT>
+__global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ WgradArgs a)
+{
+    const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int64_t q = unit >> 6;
+    const int strip = (int)(unit >> 3) & 7, c = (int)unit & 7;      // (SM, warp) of the rows; 32 columns
+    if (q >= a.rest) return;
+    const int64_t units = (int64_t)a.rest * a.steps;
+    // pair of unit u: the largest p with floor(p units / pairs) <= u
+    const int64_t p0 = ((q * a.steps + 1) * a.rest_pairs - 1) / units;
+    const int64_t p1 = ((q + 1) * a.steps * a.rest_pairs - 1) / units;
+    if (p0 == p1) return;                                            // not cut
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 32; e++) v[e] = 0.0f;
+    for (int64_t p = p0; p <= p1; p++) {
+        const int64_t slot = 2 * p + (p * units / a.rest_pairs / a.steps < q);
+        const float4* s = reinterpret_cast<const float4*>(a.slots + slot * ZERO_WG_SLOT) + (strip * 64 + c * 8) * 32 + lane;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const float4 f = __ldcg(s + e * 32);
+            v[4 * e] += f.x;
+            v[4 * e + 1] += f.y;
+            v[4 * e + 2] += f.z;
+            v[4 * e + 3] += f.w;
+        }
+    }
+    int64_t i0, j0;
+    wgrad_place(a, (int64_t)a.waves * a.pairs + q, i0, j0);
+    const int64_t r = i0 + strip * 32 + lane;
+    const float sum = column_sum(a, r);
+    if (a.db && j0 == 0 && c == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
+    put_row<DT>(a, r, j0 + c * 32, v, sum);
+}
+
+// Column sums of dy over ZERO_WG_SUMS token ranges (blockIdx.y).
+template <int DT>
+__global__ void __launch_bounds__(256) k_wgrad_sums(const __grid_constant__ WgradArgs a)
+{
+    __shared__ float part[8][32];
+    const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int64_t t1 = (blockIdx.y + 1) * a.tokens / ZERO_WG_SUMS;
+    float s = 0.0f;
+    if (i < a.n)
+        for (int64_t t = blockIdx.y * a.tokens / ZERO_WG_SUMS + (threadIdx.x >> 5); t < t1; t += 8)
+            s += widen1<DT>(__ldg(a.dy + t * a.ldy + i));
+    part[threadIdx.x >> 5][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32 || i >= a.n) return;
+    s = 0.0f;
+    for (int w = 0; w < 8; w++) s += part[w][threadIdx.x];
+    a.sums[blockIdx.y * a.n + i] = s;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) k_wgrad(const WgradArgs a)
+__global__ void __launch_bounds__(256) k_wgrad_plain(const __grid_constant__ WgradArgs a)
 {
     __shared__ float sy[16][64], sx[16][64];
     const int64_t i0 = (int64_t)blockIdx.y * 64, j0 = (int64_t)blockIdx.x * 64;
@@ -46,7 +572,7 @@ __global__ void __launch_bounds__(256) k_wgrad(const WgradArgs a)
             sy[e / 64][e % 64] = in && i < a.n ? widen1<DT>(a.dy[t * a.ldy + i]) : 0.0f;
             float v = 0.0f;
             if (in && j < a.k) {
-                const uint8_t* row = a.ckpt + t * a.stride;
+                const uint8_t* row = a.ckpt + t * act_stride(a.k);
                 uint32_t e = row[a.wide + j / 32];
                 if (DT == 0 && (e < 103 || e > 136)) e = 255;      // outside fp16
                 v = (float)(int8_t)row[j] * __uint_as_float(e << 23);
@@ -92,11 +618,75 @@ bool sizes_ok(int64_t tokens, int64_t n, int64_t k)
     return tokens >= 0 && tokens < (1ll << 31) && n >= 1 && n <= (1ll << 24) && k >= 1 && k <= ZERO_ACT_MAX_COLS;
 }
 
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t steps_of(int64_t tokens) { return up(tokens, ZERO_WG_TOK); }
+
+// Workspace: the status word (256 bytes), the column sums, the parts.
+int64_t sums_bytes(int64_t n) { return up(ZERO_WG_SUMS * n * 4, 256) * 256; }
+
+decltype(&cuTensorMapEncodeTiled) encode()
+{
+    static decltype(&cuTensorMapEncodeTiled) fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p);
+    }();
+    return fn;
+}
+
+bool tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t cols, int64_t rows, int64_t pitch,
+                int box_cols, int box_rows, CUtensorMapSwizzle swizzle)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode()(m, type, 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of SMs that run a launch's clusters at the same time; 0: a CUDA call failed.
+int device_pairs()
+{
+    static std::mutex lock;
+    static int pairs[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> hold(lock);
+    if (pairs[dev] == 0) {
+        for (const void* fn : {(const void*)k_wgrad<0>, (const void*)k_wgrad<1>})
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ZERO_WG_SMEM) != cudaSuccess)
+                return 0;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(2 * ZERO_WG_PAIRS);
+        c.blockDim = dim3(ZERO_WG_THREADS);
+        c.dynamicSmemBytes = ZERO_WG_SMEM;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        c.attrs = &at;
+        c.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_wgrad<1>, &c) != cudaSuccess) return 0;
+        pairs[dev] = n < 1 ? 1 : n > ZERO_WG_PAIRS ? ZERO_WG_PAIRS : n;
+    }
+    return pairs[dev];
+}
+
+bool launch(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream)
+{
+    return cudaLaunchKernel(fn, grid, dim3(threads), args, smem, static_cast<cudaStream_t>(stream)) == cudaSuccess;
+}
+
 }  // namespace
 
 extern "C" uint64_t zero_act_wgrad_workspace(int64_t tokens, int64_t n, int64_t k)
 {
-    return sizes_ok(tokens, n, k) ? 16 : 0;
+    if (!sizes_ok(tokens, n, k)) return 0;
+    const bool cut = steps_of(tokens) >= 2 * ZERO_WG_PART;
+    return 256 + (uint64_t)sums_bytes(n) + (cut ? 2ull * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4 : 0);
 }
 
 extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int64_t tokens, int64_t n,
@@ -108,13 +698,20 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     if ((dtype != ZERO_FP16 && dtype != ZERO_BF16) || (grad_dtype != dtype && grad_dtype != ZERO_FP32))
         return ZERO_EINVAL;
     if (!sizes_ok(tokens, n, k) || ldw < k || ldw > (1ll << 31)) return ZERO_EINVAL;
-    const uintptr_t ge = grad_dtype == ZERO_FP32 ? 4 : 2;
+    const int64_t ge = grad_dtype == ZERO_FP32 ? 4 : 2;
     if (!dw || !aligned_to(dw, ge) || !aligned_to(db, ge) || !work || !aligned_to(work, 16) ||
         !aligned_to(col_scale, 2) || !aligned_to(col_shift, 2))
         return ZERO_EINVAL;
     if (tokens > 0 && (!dy || !aligned_to(dy, 2) || ldy < n || ldy > (1ll << 31) || !ckpt ||
                        !aligned_to(ckpt, 16)))
         return ZERO_EINVAL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        if (accumulate) return ZERO_OK;
+        if (cudaMemset2DAsync(dw, ldw * ge, 0, k * ge, n, st) != cudaSuccess) return ZERO_ECUDA;
+        if (db && cudaMemsetAsync(db, 0, n * ge, st) != cudaSuccess) return ZERO_ECUDA;
+        return ZERO_OK;
+    }
     WgradArgs a{};
     a.dy = static_cast<const uint16_t*>(dy);
     a.ckpt = static_cast<const uint8_t*>(ckpt);
@@ -122,15 +719,51 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.shift = static_cast<const uint16_t*>(col_shift);
     a.dw = dw;
     a.db = db;
+    a.err = static_cast<int32_t*>(work);
+    a.sums = reinterpret_cast<float*>(static_cast<char*>(work) + 256);
+    a.slots = reinterpret_cast<float*>(static_cast<char*>(work) + 256 + sums_bytes(n));
     a.tokens = tokens; a.n = n; a.k = k; a.ldy = ldy; a.ldw = ldw;
     a.wide = act_wide(k);
-    a.stride = act_stride(k);
     a.grad_dtype = grad_dtype;
     a.accumulate = accumulate != 0;
-    const void* fn = dtype == ZERO_FP16 ? (const void*)k_wgrad<0> : (const void*)k_wgrad<1>;
-    void* args[] = {&a};
-    return cudaLaunchKernel(fn, dim3((unsigned)((k + 63) / 64), (unsigned)((n + 63) / 64)), dim3(256), args, 0,
-                            static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? ZERO_OK
-               : ZERO_ECUDA;
+    a.vec = aligned_to(dw, 16) && ldw * ge % 16 == 0;
+    const bool half = dtype == ZERO_FP16;
+    void* args[] = {&a, nullptr, nullptr, nullptr};
+    if (!aligned_to(dy, 16) || ldy % 8 != 0)
+        return launch(half ? (const void*)k_wgrad_plain<0> : (const void*)k_wgrad_plain<1>,
+                      dim3((unsigned)up(k, 64), (unsigned)up(n, 64)), 256, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
+    a.pairs = device_pairs();
+    if (a.pairs == 0 || !encode()) return ZERO_ECUDA;
+    a.steps = steps_of(tokens);
+    a.tiles_n = (int)up(n, ZERO_WG_TILE);
+    a.tiles_k = (int)up(k, ZERO_WG_TILE);
+    a.tiles = (int64_t)a.tiles_n * a.tiles_k;
+    a.waves = (int)(a.tiles / a.pairs);
+    a.rest = (int)(a.tiles % a.pairs);
+    a.rest_pairs = a.rest;
+    if (a.rest > 0 && a.steps >= 2 * ZERO_WG_PART) {
+        const int64_t parts = a.rest * a.steps / ZERO_WG_PART;
+        a.rest_pairs = (int)(parts < a.rest ? a.rest : parts < a.pairs ? parts : a.pairs);
+    }
+    CUtensorMap my, mc, me;
+    const int64_t stride = act_stride(k);
+    if (!tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, dy, n, tokens, ldy * 2, 64, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tensor_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 128, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !tensor_map(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 16, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return ZERO_ECUDA;
+    if ((col_shift || db) &&
+        !launch(half ? (const void*)k_wgrad_sums<0> : (const void*)k_wgrad_sums<1>,
+                dim3((unsigned)up(n, 32), ZERO_WG_SUMS), 256, 0, args, stream))
+        return ZERO_ECUDA;
+    args[1] = &my;
+    args[2] = &mc;
+    args[3] = &me;
+    const int run = a.waves > 0 ? a.pairs : a.rest_pairs;
+    if (!launch(half ? (const void*)k_wgrad<0> : (const void*)k_wgrad<1>, dim3(2 * run), ZERO_WG_THREADS, ZERO_WG_SMEM, args,
+                stream))
+        return ZERO_ECUDA;
+    if (a.rest_pairs > a.rest &&
+        !launch(half ? (const void*)k_wgrad_join<0> : (const void*)k_wgrad_join<1>, dim3(a.rest * 8), 256, 0, args, stream))
+        return ZERO_ECUDA;
+    return ZERO_OK;
 }

@@ -33,7 +33,15 @@ namespace zero {
 
 #define ZERO_WG_TILE 256                    // rows and columns of a pair's tile
 #define ZERO_WG_TOK 64                      // tokens of a stage
-#define ZERO_WG_STAGES 5
+#ifndef ZERO_WG_STAGES
+#define ZERO_WG_STAGES 6                    // loaded stages (dy rows, codes)
+#endif
+#ifndef ZERO_WG_WIDE
+#define ZERO_WG_WIDE 4                      // widened stages
+#endif
+#ifndef ZERO_WG_GROUPS
+#define ZERO_WG_GROUPS 4                    // groups of widening warps, a stage each
+#endif
 #define ZERO_WG_THREADS 512                 // warps 0 TMA, 1 products, 4-7 output, 8-15 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
@@ -43,8 +51,8 @@ namespace zero {
 #define ZERO_WG_A 16384
 #define ZERO_WG_C 8192
 #define ZERO_WG_E 1024
-#define ZERO_WG_STAGE (2 * ZERO_WG_A + ZERO_WG_C + ZERO_WG_E)
-#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + 1024)
+#define ZERO_WG_STAGE (ZERO_WG_A + ZERO_WG_C + ZERO_WG_E)
+#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + ZERO_WG_WIDE * ZERO_WG_A + 1024)
 #define ZERO_WG_SLOT (ZERO_WG_TILE * ZERO_WG_TILE)     // floats of a part
 
 struct WgradArgs {
@@ -186,26 +194,21 @@ static __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the barrier of the pair's first SM that lies at this SM's address `bar`.
+// Arrive on the barrier of the pair's first SM that lies at this SM's address `bar`.  What
+// the arrival announces lies in this SM's own shared or tensor memory and is ordered for the
+// tensor cores by the proxy fence or the tcgen05 fence before it, so the arrival itself
+// carries no cluster-wide release (which, with the matching acquire in the wait, cost a third of
+// the rate: 1089 against 1504 TFLOP/s at 8192 x 4096 x 4096).
 static __device__ __forceinline__ void arrive_first(uint32_t bar)
 {
     asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
-                 " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
-}
-static __device__ __forceinline__ uint32_t try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok;
+                 " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
 }
 // Bounded wait: false when it gave up (here or in another warp of this SM).
 static __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
     for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT; it++) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*dead) return false;
     }
     *dead = 1;
@@ -291,6 +294,12 @@ static __device__ __forceinline__ uint32_t code_scale(uint32_t e)
     return s | s << 16;
 }
 
+// a group's stage index advances by GROUPS and wraps once; a place's previous products are
+// found on a barrier that cannot have gone round in between; a thread's further tokens
+// keep their swizzle
+static_assert(ZERO_WG_GROUPS <= ZERO_WG_STAGES && ZERO_WG_WIDE < ZERO_WG_STAGES &&
+              (ZERO_WG_TOK / ZERO_WG_GROUPS) % 8 == 0, "ring sizes");
+
 struct WgradShared {
     uint64_t full[ZERO_WG_STAGES];          // a stage's bytes have come
     uint64_t ready[ZERO_WG_STAGES];         // both SMs' operands are in place (first SM's)
@@ -309,6 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     extern __shared__ unsigned char raw[];
     __shared__ WgradShared sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t wide = base + ZERO_WG_STAGES * ZERO_WG_STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
@@ -316,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < ZERO_WG_STAGES; s++) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.ready[s]), 16);
+            mbar_init(smem_u32(&sh.ready[s]), 16 / ZERO_WG_GROUPS);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int s = 0; s < 2; s++) {
@@ -359,8 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     mbar_expect_tx(bar, ZERO_WG_A + ZERO_WG_C + ZERO_WG_E);
                     tma_box(at, &map_y, x, y, bar);
                     tma_box(at + 8192, &map_y, x + 64, y, bar);
-                    tma_box(at + 2 * ZERO_WG_A, &map_c, c, y, bar);
-                    tma_box(at + 2 * ZERO_WG_A + ZERO_WG_C, &map_e, e, y, bar);
+                    tma_box(at + ZERO_WG_A, &map_c, c, y, bar);
+                    tma_box(at + ZERO_WG_A + ZERO_WG_C, &map_e, e, y, bar);
                     issued++;
                     if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -370,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             for (int64_t q = issued > ZERO_WG_STAGES ? issued - ZERO_WG_STAGES : 0; q < issued; q++) {
                 const int k = (int)(q % ZERO_WG_STAGES);
                 const uint32_t parity = (uint32_t)(q / ZERO_WG_STAGES & 1);
-                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !try_wait_cluster(smem_u32(&sh.full[k]), parity); it++) {
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(smem_u32(&sh.full[k]), parity); it++) {
                 }
                 if (!*dead) pair_wait(smem_u32(&sh.empty[k]), parity, dead, a.err);
             }
@@ -381,12 +391,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             // fp32 sums of fp16/bf16 operands, both with the contracted axis strided, 256 x 256
             const uint32_t what = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | 1u << 15 | 1u << 16 |
                                   (uint32_t)(ZERO_WG_TILE >> 3) << 17 | (uint32_t)(ZERO_WG_TILE >> 4) << 24;
-            int s = 0;
+            int s = 0, b = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
+            int i = 0;
+            for (; ok && wgrad_segment(a, pair, i, g); i++) {
                 const int acc = i & 1;
-                if (i >= 2 && !pair_wait(smem_u32(&sh.sum_empty[acc]), (uint32_t)((i >> 1) - 1) & 1u, dead, a.err)) break;
+                if (i >= 2 && !pair_wait(smem_u32(&sh.sum_empty[acc]), (uint32_t)((i >> 1) - 1) & 1u, dead, a.err)) {
+                    ok = false;
+                    break;
+                }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int64_t t = g.s0; t < g.s1; t++) {
                     if (!pair_wait(smem_u32(&sh.ready[s]), ph, dead, a.err)) {
@@ -394,71 +408,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t at = base + s * ZERO_WG_STAGE;
-                    const uint64_t da = operand(at), db = operand(at + ZERO_WG_A);
+                    const uint64_t da = operand(base + s * ZERO_WG_STAGE), db = operand(wide + b * ZERO_WG_A);
 #pragma unroll
                     for (int q = 0; q < ZERO_WG_TOK / 16; q++)
                         product(tmem + acc * ZERO_WG_TILE, da + q * (2048 >> 4), db + q * (2048 >> 4), what,
                                 t > g.s0 || q > 0);
                     commit_both(smem_u32(&sh.empty[s]));
                     if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+                    if (++b == ZERO_WG_WIDE) b = 0;
                 }
                 if (ok) commit_both(smem_u32(&sh.sum_full[acc]));
             }
+            // the other SM's last arrivals are here before this SM can exit: one that came
+            // after would find no barrier
+            for (int q = i > 2 ? i - 2 : 0; ok && q < i; q++)
+                ok = pair_wait(smem_u32(&sh.sum_empty[q & 1]), (uint32_t)(q >> 1) & 1u, dead, a.err);
             if (*dead) {                                     // let the products in flight finish
                 commit_both(smem_u32(&sh.drain));
-                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !try_wait_cluster(smem_u32(&sh.drain), 0); it++) {
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(smem_u32(&sh.drain), 0); it++) {
                 }
             }
         }
     } else if (warp >= 8) {
-        // ---- codes to 16-bit values: a thread takes one token's block of 32 columns ----
-        // The order in which a thread takes its block's halves (h) makes the eight lanes of
-        // each shared-memory access fall on different 16-byte columns, reading and writing.
-        const int w = threadIdx.x - 256, blk = w & 3, tok = w >> 2;
-        const int h = (blk >> 1) ^ (tok & 1);
-        const uint32_t from = tok * 128 + blk * 32, row = (blk >> 1) * 8192 + tok * 128;
-        int s = 0;
-        uint32_t ph = 0;
+        // ---- codes to 16-bit values ----
+        // Groups of warps take stages in turn, so a stage's latencies (its barrier, shared
+        // memory, the fence before the tensor cores read) overlap the other groups' work.  A
+        // thread takes a token's block of 32 columns, and further tokens of the stage.  The
+        // order in which it takes a block's halves (h) makes the eight lanes of each shared-
+        // memory access fall on different 16-byte columns, reading and writing.
+        constexpr int GROUPS = ZERO_WG_GROUPS, TOKENS = ZERO_WG_TOK / GROUPS;
+        const int w = (threadIdx.x - 256) % (256 / GROUPS), group = (threadIdx.x - 256) / (256 / GROUPS);
+        const int blk = w & 3, tok = w >> 2, h = (blk >> 1) ^ (tok & 1);
+        const uint32_t from = tok * 128 + blk * 32 + 16 * h, row = (blk >> 1) * 8192 + tok * 128;
+        const uint32_t col = (uint32_t)(((blk & 1) * 4 + 2 * h) ^ (tok & 7)) * 16;
+        int s = group, b = group % ZERO_WG_WIDE, skip = group;
+        int f = (group - ZERO_WG_WIDE + ZERO_WG_STAGES) % ZERO_WG_STAGES;   // stage whose products free the place
+        uint32_t ph = 0, fph = group < ZERO_WG_WIDE;        // parity 1 of an unused barrier does not wait
         bool ok = true;
         for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
             int64_t i0, j0;
             wgrad_place(a, g.tile, i0, j0);
             const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * 128) / 32 & 15) + blk;
-            for (int64_t t = g.s0; t < g.s1; t++) {
+            const int64_t len = g.s1 - g.s0;
+            int64_t t = skip;
+            for (; t < len; t += GROUPS) {
                 if (!pair_wait(smem_u32(&sh.full[s]), ph, dead, a.err)) {
                     ok = false;
                     break;
                 }
-                const uint32_t at = base + s * ZERO_WG_STAGE, codes = at + 2 * ZERO_WG_A;
-                uint32_t e, q[2][4];
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(codes + ZERO_WG_C + eat));
+                const uint32_t codes = base + s * ZERO_WG_STAGE + ZERO_WG_A, to = wide + b * ZERO_WG_A + row;
+                uint32_t e[GROUPS], q[GROUPS][2][4];
 #pragma unroll
-                for (int c = 0; c < 2; c++)
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(q[c][0]), "=r"(q[c][1]), "=r"(q[c][2]), "=r"(q[c][3])
-                                 : "r"(codes + from + 16 * (c ^ h)));
-                const uint32_t sc = code_scale<DT>(e);
+                for (int u = 0; u < GROUPS; u++) {
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[u]) : "r"(codes + ZERO_WG_C + eat + u * TOKENS * 16));
 #pragma unroll
-                for (int c = 0; c < 2; c++)
+                    for (int c = 0; c < 2; c++)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(q[u][c][0]), "=r"(q[u][c][1]), "=r"(q[u][c][2]), "=r"(q[u][c][3])
+                                     : "r"(codes + u * TOKENS * 128 + (from ^ 16 * c)));
+                }
+                // the place is free once the stage ZERO_WG_WIDE before this one has been multiplied
+                if (!pair_wait(smem_u32(&sh.empty[f]), fph, dead, a.err)) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
-                    for (int p = 0; p < 2; p++) {              // eight codes -> 16 bytes
-                        uint32_t r[4];
+                for (int u = 0; u < GROUPS; u++) {
+                    const uint32_t sc = code_scale<DT>(e[u]);
 #pragma unroll
-                        for (int d = 0; d < 4; d++) {
-                            const uint32_t x = DT == 1 ? q[c][2 * p + d / 2] : q[c][2 * p + d / 2] ^ 0x80808080u;
-                            r[d] = widen_codes<DT>(x, d & 1 ? 0x4342 : 0x4140, sc);
+                    for (int c = 0; c < 2; c++)
+#pragma unroll
+                        for (int p = 0; p < 2; p++) {          // eight codes -> 16 bytes
+                            uint32_t r[4];
+#pragma unroll
+                            for (int d = 0; d < 4; d++) {
+                                const uint32_t x = q[u][c][2 * p + d / 2];
+                                r[d] = widen_codes<DT>(DT == 1 ? x : x ^ 0x80808080u, d & 1 ? 0x4342 : 0x4140, sc);
+                            }
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                         ::"r"(to + u * TOKENS * 128 + (col ^ (2 * c + p) * 16)), "r"(r[0]), "r"(r[1]),
+                                         "r"(r[2]), "r"(r[3]) : "memory");
                         }
-                        const uint32_t col = ((blk & 1) * 4 + 2 * (c ^ h) + p) ^ (tok & 7);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(at + ZERO_WG_A + row + 16 * col), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                                     : "memory");
-                    }
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_first(smem_u32(&sh.ready[s]));
-                if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+                s += GROUPS;
+                if (s >= ZERO_WG_STAGES) { s -= ZERO_WG_STAGES; ph ^= 1u; }
+                f += GROUPS;
+                if (f >= ZERO_WG_STAGES) { f -= ZERO_WG_STAGES; fph ^= 1u; }
+                b = (b + GROUPS) % ZERO_WG_WIDE;
             }
+            skip = (int)(t - len);
         }
     } else if (warp >= 4) {
         // ---- output: warp w has rows 32 (w - 4) + lane of this SM's half ----

@@ -9,6 +9,7 @@
 #pragma once
 
 #include "zero_common.cuh"
+#include "zero_qwz.cuh"                  // pairs of fp32 values and their arithmetic
 
 namespace zero {
 
@@ -40,127 +41,178 @@ static __device__ __forceinline__ uint32_t act_exponent(uint32_t amax_bits, int 
     return (uint32_t)(e < lo ? lo : e > hi ? hi : e);
 }
 
-// 2^(127 - E), the factor from values to codes; 0 for a bad block.
-static __device__ __forceinline__ float act_step(uint32_t e)
+// ---- chunks: eight consecutive columns, held as four pairs ---------------------------
+static __device__ __forceinline__ f32x2_t fma2(f32x2_t a, f32x2_t b, f32x2_t c)
 {
-    return e == ZERO_ACT_BAD ? 0.0f : __uint_as_float((254u - e) << 23);
+    f32x2_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+static __device__ __forceinline__ f32x2_t both(float a) { return pack2(a, a); }
+static __device__ __forceinline__ float either(f32x2_t a)              // the pair's sum
+{
+    float x, y;
+    unpack2(a, x, y);
+    return x + y;
 }
 
-// Four codes packed in a word, from four values and their block's factor.  Adding
-// 1.5 * 2^23 rounds to the nearest integer, ties to even, and leaves it in the low
-// byte.  Only a block whose exponent was cut at the type's largest can pass 127,
-// so the clamp is left to that case (`top`, uniform per block).  A bad block's
-// codes are 0 whatever its values.
-static __device__ __forceinline__ uint32_t act_codes4(float a, float b, float c, float d, float step,
-                                                      bool top, bool bad)
+// Eight codes -> eight values.  The byte of a code, XOR 128, in the mantissa of 2^23
+// is 2^23 + 128 + c exactly; one subtraction leaves c.  E = 255 gives the scale
+// inf, and 0 * inf = NaN.
+static __device__ __forceinline__ void act_values(uint2 q, uint32_t e, f32x2_t (&v)[4])
 {
-    const float rnd = 12582912.0f;
-    a *= step; b *= step; c *= step; d *= step;
-    if (top) {
-        a = fminf(fmaxf(a, -127.0f), 127.0f);
-        b = fminf(fmaxf(b, -127.0f), 127.0f);
-        c = fminf(fmaxf(c, -127.0f), 127.0f);
-        d = fminf(fmaxf(d, -127.0f), 127.0f);
-    }
-    const uint32_t u0 = __float_as_uint(__fadd_rn(a, rnd)), u1 = __float_as_uint(__fadd_rn(b, rnd));
-    const uint32_t u2 = __float_as_uint(__fadd_rn(c, rnd)), u3 = __float_as_uint(__fadd_rn(d, rnd));
-    const uint32_t w = __byte_perm(__byte_perm(u0, u1, 0x0040), __byte_perm(u2, u3, 0x0040), 0x5410);
-    return bad ? 0u : w;
-}
-
-// Eight codes (a lane's chunk) -> eight values in fp32.  Byte b of a code, XOR 128,
-// in the mantissa of 2^23 is 2^23 + 128 + c exactly; one subtraction leaves c.
-static __device__ __forceinline__ void act_values8(uint2 q, uint32_t e, float (&v)[8])
-{
-    const float scale = __uint_as_float(e << 23);          // E = 255: inf, and 0 * inf = NaN
+    const f32x2_t scale = both(__uint_as_float(e << 23)), bias = both(8388736.0f);
     const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t m = __byte_perm(w[i / 4], 0x4B000000u, 0x7650 + (i % 4));
-        v[i] = (__uint_as_float(m) - 8388736.0f) * scale;
+    for (int i = 0; i < 4; i++) {
+        const uint32_t a = __byte_perm(w[i / 2], 0x4B000000u, 0x7650 + (2 * i) % 4);
+        const uint32_t b = __byte_perm(w[i / 2], 0x4B000000u, 0x7650 + (2 * i + 1) % 4);
+        v[i] = mul2(sub2(pack2(__uint_as_float(a), __uint_as_float(b)), bias), scale);
     }
 }
 
-// ---- rows of 8-element chunks ----------------------------------------------------
-// Eight elements of a row, elements at or past n (1..8 in range) read as 0.
-// VEC: the address is 16-byte aligned and all eight lie in the row.
-template <int DT>
-static __device__ __forceinline__ float load1(const void* p, int64_t i)
+// Eight codes packed in two words, from eight values and their block's exponent byte.
+// step = 2^(127 - E).  Adding 1.5 * 2^23 rounds to the nearest integer, ties to even,
+// and leaves it in the low byte (the product is exact, so one fused operation does
+// both).  Only a block whose exponent was cut at the type's largest (`hi`) can pass
+// 127, so the clamp is left to that case.  A bad block's codes are 0.
+static __device__ __forceinline__ uint2 act_codes(const f32x2_t (&v)[4], uint32_t e, int hi)
 {
-    if (DT == 2) return __ldg(static_cast<const float*>(p) + i);
-    return widen1<DT>(__ldg(static_cast<const uint16_t*>(p) + i));
-}
-
-template <int DT>
-static __device__ __forceinline__ void load8(const void* p, int64_t i, int n, bool vec, float (&v)[8])
-{
-    if (vec && n >= 8) {
-        if (DT == 2) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-            const float4 b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    if (e == ZERO_ACT_BAD) return make_uint2(0, 0);
+    const f32x2_t step = both(__uint_as_float((254u - e) << 23)), rnd = both(12582912.0f);
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float a, b;
+        if ((int)e == hi) {
+            unpack2(mul2(v[i], step), a, b);
+            a = __fadd_rn(fminf(fmaxf(a, -127.0f), 127.0f), 12582912.0f);
+            b = __fadd_rn(fminf(fmaxf(b, -127.0f), 127.0f), 12582912.0f);
         } else {
-            const uint4 q = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
-            widen2<DT & 1>(q.x, v[0], v[1]);
-            widen2<DT & 1>(q.y, v[2], v[3]);
-            widen2<DT & 1>(q.z, v[4], v[5]);
-            widen2<DT & 1>(q.w, v[6], v[7]);
+            unpack2(fma2(v[i], step, rnd), a, b);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = j < n ? load1<DT>(p, i + j) : 0.0f;
+        u[2 * i] = __float_as_uint(a);
+        u[2 * i + 1] = __float_as_uint(b);
     }
-}
-
-template <int DT>
-static __device__ __forceinline__ void store8(void* p, int64_t i, int n, bool vec, const float (&v)[8])
-{
-    if (vec && n >= 8) {
-        if (DT == 2) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
-        } else {
-            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i),
-                   make_uint4(narrow2<DT & 1>(v[0], v[1]), narrow2<DT & 1>(v[2], v[3]),
-                              narrow2<DT & 1>(v[4], v[5]), narrow2<DT & 1>(v[6], v[7])));
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (j < n) {
-                if (DT == 2) static_cast<float*>(p)[i + j] = v[j];
-                else static_cast<uint16_t*>(p)[i + j] = narrow1<DT & 1>(v[j]);
-            }
-    }
-}
-
-// Quantize and store one 8-column chunk: the four lanes of a block (consecutive,
-// lane % 4 the chunk's place in its block) agree on the exponent by two shuffles.
-// `row` is the checkpoint's row, col the chunk's first column, wide the row's code
-// bytes; elements past the row's end are 0 in v.  All 32 lanes of the warp take
-// part; `live` lanes store.
-static __device__ __forceinline__ void act_store_chunk(const float (&v)[8], uint8_t* row, int col, int wide,
-                                                       int stride, int lo, int hi, bool live)
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (!live) return;
-    const uint32_t e = act_exponent(m, lo, hi);
-    const float step = act_step(e);
-    const bool top = (int)e == hi, bad = e == ZERO_ACT_BAD;
     uint2 q;
-    q.x = act_codes4(v[0], v[1], v[2], v[3], step, top, bad);
-    q.y = act_codes4(v[4], v[5], v[6], v[7], step, top, bad);
+    q.x = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    q.y = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
+    return q;
+}
+
+// Store a chunk's codes; the first lane of a block its exponent; the lanes of a row's
+// last block the zeros after the exponents.  `row` is the checkpoint's row.
+static __device__ __forceinline__ void act_put(uint8_t* row, int col, int wide, int stride, uint2 q, uint32_t e)
+{
     *reinterpret_cast<uint2*>(row + col) = q;
     const int sub = (col >> 3) & 3;
     if (sub == 0) row[wide + (col >> 5)] = (uint8_t)e;
-    if (col + 8 * (4 - sub) == wide)                        // the row's last block
+    if (col + 8 * (4 - sub) == wide)
         for (int i = wide + (wide >> 5) + sub; i < stride; i += 4) row[i] = 0;
+}
+
+// Largest magnitude of three, NaN if any is.
+static __device__ __forceinline__ float amax3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Quantize and store a chunk of fp32 values.  The four lanes of a block are consecutive
+// and agree on the exponent by two shuffles: all lanes of the warp take part, `live` ones
+// store.  Values past the row's end are 0.
+static __device__ __forceinline__ void act_store(const f32x2_t (&v)[4], uint8_t* row, int col, int wide,
+                                                 int stride, int lo, int hi, bool live)
+{
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) unpack2(v[i], x[2 * i], x[2 * i + 1]);
+    float m = amax3(amax3(amax3(x[0], x[1], x[2]), x[3], x[4]), amax3(x[5], x[6], x[7]), 0.0f);
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!live) return;
+    const uint32_t e = act_exponent(__float_as_uint(m), lo, hi);
+    act_put(row, col, wide, stride, act_codes(v, e, hi), e);
+}
+
+// ---- a chunk as it lies in memory (T: 0 fp16, 1 bf16, 2 fp32) ------------------------
+template <int T> struct Raw { uint4 q[T == 2 ? 2 : 1]; };
+
+// Elements i .. i+8 of p, those at or past n (of the chunk's eight) read as 0.  `vec`: the
+// address is 16-byte aligned.  WHOLE: that is known, and n is at least 8 or at most 0.
+template <int T, bool WHOLE = false>
+static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* p, int64_t i, int n, bool vec)
+{
+    if ((WHOLE || vec) && n >= 8) {
+        if (T == 2) {
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+            r.q[0] = __ldcs(s);
+            r.q[T == 2] = __ldcs(s + 1);
+        } else {
+            r.q[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+        }
+        return;
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        w[j] = WHOLE || j >= n ? 0u
+               : T == 2 ? __ldg(static_cast<const uint32_t*>(p) + i + j)
+                        : (uint32_t)__ldg(static_cast<const uint16_t*>(p) + i + j);
+    if (T == 2) {
+        r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        r.q[T == 2] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+        r.q[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+}
+
+template <int T>
+static __device__ __forceinline__ void widen_chunk(const Raw<T>& r, f32x2_t (&v)[4])
+{
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+    if (T == 2) {
+        const uint32_t x[4] = {r.q[T == 2].x, r.q[T == 2].y, r.q[T == 2].z, r.q[T == 2].w};
+        v[0] = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        v[1] = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        v[2] = pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        v[3] = pack2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            float a, b;
+            widen2<T & 1>(w[j], a, b);
+            v[j] = pack2(a, b);
+        }
+    }
+}
+
+template <int T, bool WHOLE = false>
+static __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, bool vec, const f32x2_t (&v)[4])
+{
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) unpack2(v[j], x[2 * j], x[2 * j + 1]);
+    if ((WHOLE || vec) && n >= 8) {
+        if (T == 2) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+            __stcs(o, make_float4(x[0], x[1], x[2], x[3]));
+            __stcs(o + 1, make_float4(x[4], x[5], x[6], x[7]));
+        } else {
+            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i),
+                   make_uint4(narrow2<T & 1>(x[0], x[1]), narrow2<T & 1>(x[2], x[3]),
+                              narrow2<T & 1>(x[4], x[5]), narrow2<T & 1>(x[6], x[7])));
+        }
+        return;
+    }
+    if (WHOLE) return;
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < n) {
+            if (T == 2) static_cast<float*>(p)[i + j] = x[j];
+            else static_cast<uint16_t*>(p)[i + j] = narrow1<T & 1>(x[j]);
+        }
 }
 
 }  // namespace zero

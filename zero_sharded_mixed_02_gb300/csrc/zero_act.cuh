@@ -136,6 +136,41 @@ static __device__ __forceinline__ void act_store(const f32x2_t (&v)[4], uint8_t*
     act_put(row, col, wide, stride, act_codes(v, e, hi), e);
 }
 
+// The same for values below 2^100, as normalised rows are (at most sqrt(cols)): no exponent
+// is cut at the type's largest, and the exponent needs no comparison of the fraction: adding
+// 0x1FFFF to the bits carries into the exponent exactly when f > 127/64.
+static __device__ __forceinline__ void act_store_small(const f32x2_t (&v)[4], uint8_t* row, int col, int wide,
+                                                       int stride, int lo, bool live)
+{
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) unpack2(v[i], x[2 * i], x[2 * i + 1]);
+    float m = amax3(amax3(amax3(x[0], x[1], x[2]), x[3], x[4]), amax3(x[5], x[6], x[7]), 0.0f);
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!live) return;
+    int e = (int)((__float_as_uint(m) + 0x1FFFFu) >> 23) - 6;
+    e = e < lo ? lo : e;
+    const bool bad = e > 240;
+    const f32x2_t step = both(__uint_as_float((254u - (uint32_t)e) << 23)), rnd = both(12582912.0f);
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float a, b;
+        unpack2(fma2(v[i], step, rnd), a, b);
+        u[2 * i] = __float_as_uint(a);
+        u[2 * i + 1] = __float_as_uint(b);
+    }
+    uint2 q;
+    q.x = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    q.y = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
+    if (bad) {
+        q = make_uint2(0, 0);
+        e = ZERO_ACT_BAD;
+    }
+    act_put(row, col, wide, stride, q, (uint32_t)e);
+}
+
 // ---- a chunk as it lies in memory (T: 0 fp16, 1 bf16, 2 fp32) ------------------------
 template <int T> struct Raw { uint4 q[T == 2 ? 2 : 1]; };
 

@@ -9,12 +9,12 @@
 namespace zero {
 
 struct NormSumArgs {
-    const float *pre_part, *slots;
-    const void *post_w, *post_b, *gate;
+    const float *pre_part, *post_part, *slots;
+    const void *post_w, *post_b;
     void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
     int64_t rows, group, groups;
     int cols, wide, blocks, sums, dtype, grad_dtype, accumulate;
-    int col_jobs;
+    int col_jobs, flat;
     float alpha;
 };
 
@@ -36,57 +36,71 @@ static __device__ __forceinline__ void grad_out(void* p, int64_t i, float v, int
     }
 }
 
-static __device__ __forceinline__ void add_part(const float* p, int wide, int sums, float w, float4& v0, float4& v1)
+static __device__ __forceinline__ void add4(float4& v, const float* p)
 {
     const float4 s = __ldcg(reinterpret_cast<const float4*>(p));
-    v0.x = __fmaf_rn(w, s.x, v0.x); v0.y = __fmaf_rn(w, s.y, v0.y);
-    v0.z = __fmaf_rn(w, s.z, v0.z); v0.w = __fmaf_rn(w, s.w, v0.w);
-    if (sums == 2) {
-        const float4 t = __ldcg(reinterpret_cast<const float4*>(p + wide));
-        v1.x = __fmaf_rn(w, t.x, v1.x); v1.y = __fmaf_rn(w, t.y, v1.y);
-        v1.z = __fmaf_rn(w, t.z, v1.z); v1.w = __fmaf_rn(w, t.w, v1.w);
+    v.x += s.x; v.y += s.y; v.z += s.z; v.w += s.w;
+}
+
+#define ZERO_NORM_STRIPS 16
+
+__host__ __device__ inline int64_t norm_sum_jobs(const NormSumArgs& a)
+{
+    return a.col_jobs * (2 + (!a.dgate ? 0 : a.flat ? (a.groups + ZERO_NORM_STRIPS - 1) / ZERO_NORM_STRIPS : a.groups));
+}
+
+// The sums of a group's rows at column c: its blocks' slots from the group's block `first` by step.
+static __device__ __forceinline__ void add_group(const NormSumArgs& a, int64_t g, int c, int first, int step,
+                                                 float4& v0, float4& v1)
+{
+    if (a.rows == 0) return;
+    const int64_t r0 = g * a.group, r1 = r0 + a.group < a.rows ? r0 + a.group : a.rows;
+    const int64_t b1 = norm_block_of(r1 - 1, a.rows, a.blocks);
+    for (int64_t b = norm_block_of(r0, a.rows, a.blocks) + first; b <= b1; b += step) {
+        const float* p = a.slots + (b + g) * a.sums * a.wide + c;
+        add4(v0, p);
+        if (a.sums == 2) add4(v1, p + a.wide);
     }
 }
 
-// Adds the blocks' partial sums.  A job is 128 columns (four a thread) of the pre-norm's
-// sums, of the post-norm's, or of a gate group's; eight strips of threads take every
-// eighth block's part, and the strips are added in order.
-__global__ void __launch_bounds__(256) k_norm_sums(const __grid_constant__ NormSumArgs a)
+static __device__ __forceinline__ void gate_out(const NormSumArgs& a, int64_t g, int64_t c, float v0, float v1)
 {
-    __shared__ float4 s0[8][32], s1[8][32];
+    v0 *= weight_at(a.post_w, c, a.dtype);
+    if (a.post_b) v0 = __fmaf_rn(weight_at(a.post_b, c, a.dtype), v1, v0);
+    grad_out(a.dgate, g * a.cols + c, a.alpha * v0, a.grad_dtype, a.accumulate);
+}
+
+// Adds the blocks' partial sums.  A job is 128 columns (four a thread) of the pre-norm's
+// sums, of the post-norm's, or of a gate group's; the strips of threads take every
+// 16th block's part, and the strips are added in order.  Where a group spans few blocks
+// (flat), a gate job is 128 columns of 16 groups instead, a strip each.
+__global__ void __launch_bounds__(32 * ZERO_NORM_STRIPS) k_norm_sums(const __grid_constant__ NormSumArgs a)
+{
+    __shared__ float4 s0[ZERO_NORM_STRIPS][32], s1[ZERO_NORM_STRIPS][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // the pass whose sums these are
     const int strip = threadIdx.y;
-    const int64_t jobs = a.col_jobs * (2 + (a.dgate ? a.groups : 0));
+    const int64_t jobs = norm_sum_jobs(a);
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         float4 v0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v1 = v0;
         const int64_t what = job / a.col_jobs;
-        const int c = (int)(job - what * a.col_jobs) * 128 + 4 * threadIdx.x;
-        if (c < a.wide && a.rows > 0) {
-            if (what == 0) {
-                if (a.dpre_w || a.dpre_b)
-#pragma unroll 4
-                    for (int b = strip; b < a.blocks; b += 8)
-                        add_part(a.pre_part + (int64_t)b * a.sums * a.wide + c, a.wide, a.sums, 1.0f, v0, v1);
-            } else if (what == 1) {
-                if (a.dpost_w || a.dpost_b)
-                    for (int b = strip; b < a.blocks; b += 8) {
-                        const int64_t g0 = norm_row0(b, a.rows, a.blocks) / a.group;
-                        const int64_t g1 = (norm_row0(b + 1, a.rows, a.blocks) - 1) / a.group;
-                        for (int64_t g = g0; g <= g1; g++) {
-                            float4 q0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q1 = q0;
-                            add_part(a.slots + (b + g) * a.sums * a.wide + c, a.wide, a.sums, a.alpha, q0, q1);
+        if (what >= 2 && a.flat) {
+            const int64_t g = (what - 2) * ZERO_NORM_STRIPS + strip;
+            const int c = (int)(job - what * a.col_jobs) * 128 + 4 * threadIdx.x;
+            if (g >= a.groups || c >= a.wide) continue;
+            add_group(a, g, c, 0, 1, v0, v1);
 #pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const float w = c + e < a.cols ? weight_at(a.gate, g * a.cols + c + e, a.dtype) : 0.0f;
-                                (&v0.x)[e] = __fmaf_rn(w, (&q0.x)[e], (&v0.x)[e]);
-                                (&v1.x)[e] = __fmaf_rn(w, (&q1.x)[e], (&v1.x)[e]);
-                            }
-                        }
-                    }
-            } else {
-                const int64_t g = what - 2, r0 = g * a.group, r1 = r0 + a.group < a.rows ? r0 + a.group : a.rows;
-                const int64_t b1 = norm_block_of(r1 - 1, a.rows, a.blocks);
-                for (int64_t b = norm_block_of(r0, a.rows, a.blocks) + strip; b <= b1; b += 8)
-                    add_part(a.slots + (b + g) * a.sums * a.wide + c, a.wide, a.sums, a.alpha, v0, v1);
+            for (int e = 0; e < 4; e++)
+                if (c + e < a.cols) gate_out(a, g, c + e, (&v0.x)[e], (&v1.x)[e]);
+            continue;
+        }
+        const int c = (int)(job - what * a.col_jobs) * 128 + 4 * threadIdx.x;
+        if (what >= 2) {
+            if (c < a.wide) add_group(a, what - 2, c, strip, ZERO_NORM_STRIPS, v0, v1);
+        } else if (const float* p = what == 0 ? a.pre_part : a.post_part; p && c < a.wide) {
+#pragma unroll 8
+            for (int b = strip; b < a.blocks; b += ZERO_NORM_STRIPS) {
+                add4(v0, p + (int64_t)b * a.sums * a.wide + c);
+                if (a.sums == 2) add4(v1, p + (int64_t)b * a.sums * a.wide + a.wide + c);
             }
         }
         __syncthreads();                                     // the previous job's reads are done
@@ -98,7 +112,7 @@ __global__ void __launch_bounds__(256) k_norm_sums(const __grid_constant__ NormS
         if (own >= a.cols) continue;
         float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < ZERO_NORM_STRIPS; i++) {
             t0 += reinterpret_cast<const float*>(s0[i])[strip * 32 + threadIdx.x];
             t1 += reinterpret_cast<const float*>(s1[i])[strip * 32 + threadIdx.x];
         }
@@ -106,12 +120,10 @@ __global__ void __launch_bounds__(256) k_norm_sums(const __grid_constant__ NormS
             if (a.dpre_w) grad_out(a.dpre_w, own, t0, a.grad_dtype, a.accumulate);
             if (a.dpre_b) grad_out(a.dpre_b, own, t1, a.grad_dtype, a.accumulate);
         } else if (what == 1) {
-            if (a.dpost_w) grad_out(a.dpost_w, own, t0, a.grad_dtype, a.accumulate);
-            if (a.dpost_b) grad_out(a.dpost_b, own, t1, a.grad_dtype, a.accumulate);
+            if (a.dpost_w) grad_out(a.dpost_w, own, a.alpha * t0, a.grad_dtype, a.accumulate);
+            if (a.dpost_b) grad_out(a.dpost_b, own, a.alpha * t1, a.grad_dtype, a.accumulate);
         } else {
-            t0 *= weight_at(a.post_w, own, a.dtype);
-            if (a.post_b) t0 = __fmaf_rn(weight_at(a.post_b, own, a.dtype), t1, t0);
-            grad_out(a.dgate, (what - 2) * a.cols + own, t0, a.grad_dtype, a.accumulate);
+            gate_out(a, what - 2, own, t0, t1);
         }
     }
 }
@@ -218,7 +230,8 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.ckpt_y = static_cast<uint8_t*>(ckpt_y);
     a.ckpt_x = static_cast<uint8_t*>(ckpt_x);
     a.stats = stats;
-    a.rows = (uint32_t)d.rows; a.ldh = ldh; a.ldy = ldy; a.ldho = ldho; a.ldx = ldx;
+    a.rows = (uint32_t)d.rows;
+    a.ldh = (uint32_t)ldh; a.ldy = (uint32_t)ldy; a.ldho = (uint32_t)ldho; a.ldx = (uint32_t)ldx;
     a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
     a.cols = (int)d.cols;
     a.wide = (int)act_wide(d.cols);
@@ -253,7 +266,7 @@ extern "C" uint64_t zero_norm_workspace(const zero_norm_t* norm)
 {
     if (!description_ok(norm)) return 0;
     const uint64_t blocks = norm->rows < ZERO_NORM_BLOCKS ? norm->rows : ZERO_NORM_BLOCKS;
-    return 16 + (2 * blocks + (uint64_t)groups_of(*norm)) * 2 * (uint64_t)act_wide(norm->cols) * sizeof(float);
+    return 16 + (3 * blocks + (uint64_t)groups_of(*norm)) * 2 * (uint64_t)act_wide(norm->cols) * sizeof(float);
 }
 
 extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void* dh_out, int64_t lddho,
@@ -283,11 +296,9 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     }
     const bool sums = dpost_w || dpost_b || dgate || dpre_w || dpre_b;
     if (sums && (!work || !aligned_to(work, 16))) return ZERO_EINVAL;
-    const bool slots = dpost_w || dpost_b || dgate;
     const bool two = dpre_b || dpost_b || (dgate && d.post_b);
     int64_t blocks = 0;
-    float* const slot_sums = static_cast<float*>(work);
-    float* pre_part = nullptr;
+    float *pre_part = nullptr, *post_part = nullptr, *slots = nullptr;
     if (d.rows > 0) {
         NormBwdArgs a{};
         a.dh_out = dh_out; a.dx = dx; a.dh = dh; a.dy = dy;
@@ -295,8 +306,9 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.ckpt_y = static_cast<const uint8_t*>(ckpt_y);
         a.ckpt_x = static_cast<const uint8_t*>(ckpt_x);
         a.stats = stats;
-        a.rows = d.rows; a.lddho = lddho; a.lddx = lddx; a.lddh = lddh; a.lddy = lddy;
-        a.group = d.group_rows ? d.group_rows : d.rows;
+        a.rows = (uint32_t)d.rows;
+        a.lddho = (uint32_t)lddho; a.lddx = (uint32_t)lddx; a.lddh = (uint32_t)lddh; a.lddy = (uint32_t)lddy;
+        a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
         a.cols = (int)d.cols;
         a.wide = (int)act_wide(d.cols);
         a.stride = (int)act_stride(d.cols);
@@ -319,9 +331,14 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         if (blocks == 0) return ZERO_ECUDA;
         if (blocks > ZERO_NORM_BLOCKS) blocks = ZERO_NORM_BLOCKS;
         if (blocks > d.rows) blocks = d.rows;
-        pre_part = slot_sums + (blocks + groups_of(d)) * (two ? 2 : 1) * a.wide;
-        a.slots = slots ? slot_sums : nullptr;
-        a.pre_part = dpre_w || dpre_b ? pre_part : nullptr;
+        const int64_t part = blocks * (two ? 2 : 1) * a.wide;
+        float* at = static_cast<float*>(work);
+        if (dpre_w || dpre_b) pre_part = at;
+        if (dpost_w || dpost_b) post_part = at + part;
+        if (dgate) slots = at + 2 * part;
+        a.pre_part = pre_part;
+        a.post_part = post_part;
+        a.slots = slots;
         void* args[] = {&a};
         if (cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), args, 0,
                              static_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -329,8 +346,8 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     }
     if (!sums) return ZERO_OK;
     NormSumArgs a{};
-    a.pre_part = pre_part; a.slots = slot_sums;
-    a.post_w = d.post_w; a.post_b = d.post_b; a.gate = d.gate;
+    a.pre_part = pre_part; a.post_part = post_part; a.slots = slots;
+    a.post_w = d.post_w; a.post_b = d.post_b;
     a.dpost_w = dpost_w; a.dpost_b = dpost_b; a.dgate = dgate; a.dpre_w = dpre_w; a.dpre_b = dpre_b;
     a.rows = d.rows;
     a.group = d.group_rows ? d.group_rows : d.rows > 0 ? d.rows : 1;
@@ -342,10 +359,17 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     a.alpha = d.alpha;
     a.wide = (int)act_wide(d.cols);
     a.col_jobs = (int)((d.cols + 127) / 128);
-    const int64_t jobs = a.col_jobs * (2 + (dgate ? a.groups : 0));
-    void* args[] = {&a};
-    return cudaLaunchKernel((const void*)k_norm_sums, dim3((unsigned)(jobs < (1 << 30) ? jobs : 1 << 30)),
-                            dim3(32, 8), args, 0, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? ZERO_OK
-               : ZERO_ECUDA;
+    a.flat = a.groups * 4 > blocks;
+    const int64_t jobs = norm_sum_jobs(a);
+    // placed while the pass drains; it waits for the pass's sums itself
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(jobs < (1 << 30) ? jobs : 1 << 30));
+    c.blockDim = dim3(32, ZERO_NORM_STRIPS);
+    c.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, k_norm_sums, a) == cudaSuccess ? ZERO_OK : ZERO_ECUDA;
 }

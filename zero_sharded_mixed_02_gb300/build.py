@@ -21,8 +21,10 @@ SOURCES = ["zero_abi.cu", "zero_step_fp16.cu", "zero_step_bf16.cu", "zero_step_q
            "zero_step_q_bf16.cu", "zero_gather.cu",
            "zero_noalloc.cu", "zero_qwz.cu", "zero_ckpt.cu", "zero_offload.cu",
            "zero_cpu_adam.cpp", "zero_act.cu", "zero_wgrad.cu", "zero_norm.cu",
-           "zero_norm_forward_fp16.cu", "zero_norm_forward_bf16.cu", "zero_norm_backward_fp16.cu",
-           "zero_norm_backward_bf16.cu"]
+           "zero_norm_forward_fp16.cu", "zero_norm_forward_fp16_fp32.cu",
+           "zero_norm_forward_bf16.cu", "zero_norm_forward_bf16_fp32.cu",
+           "zero_norm_backward_fp16.cu", "zero_norm_backward_fp16_fp32.cu",
+           "zero_norm_backward_bf16.cu", "zero_norm_backward_bf16_fp32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]

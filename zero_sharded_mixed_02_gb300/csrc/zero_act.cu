@@ -20,7 +20,7 @@ namespace zero {
 struct ActArgs {
     const void* x;          // or the output of load
     uint8_t* ckpt;
-    int64_t ld;
+    uint32_t ld;
     uint32_t chunks;        // rows * per_row, below 2^31
     uint32_t per_row;       // chunks of a row
     uint32_t magic, shift;  // q / per_row = (q * magic) >> (32 + shift) for q < 2^31
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_save(const __grid_constant
         const uint32_t q = first + u * ZERO_THREADS;
         act_place(a, q, row[u], col[u]);
         if (q >= a.chunks) col[u] = a.wide;                  // nothing to read or write
-        load_chunk<T>(r[u], a.x, row[u] * a.ld + col[u], a.cols - col[u], a.vec);
+        load_chunk<T>(r[u], row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], a.vec);
     }
 #pragma unroll
     for (int u = 0; u < ZERO_ACT_UNROLL; u++) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_load(const __grid_constant
         if (col[u] < a.cols) {
             f32x2_t v[4];
             act_values(c[u], e[u], v);
-            store_chunk<T>(const_cast<void*>(a.x), row[u] * a.ld + col[u], a.cols - col[u], a.vec, v);
+            store_chunk<T>(row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], a.vec, v);
         }
 }
 
@@ -142,7 +142,7 @@ zero_status_t run(bool save, zero_dtype_t dtype, const void* x, int64_t rows, in
     while ((1u << l) < a.per_row) l++;
     a.magic = (uint32_t)(((1ull << (31 + l)) + a.per_row - 1) / a.per_row);
     a.shift = l - 1;
-    a.ld = ld;
+    a.ld = (uint32_t)ld;
     a.lo = act_lo(dtype);
     a.hi = act_hi(dtype);
     a.vec = aligned_to(x, 16) && ld * size % 16 == 0;

@@ -102,13 +102,13 @@ static __device__ __forceinline__ uint2 act_codes(const f32x2_t (&v)[4], uint32_
 
 // Store a chunk's codes; the first lane of a block its exponent; the lanes of a row's
 // last block the zeros after the exponents.  `row` is the checkpoint's row.
-static __device__ __forceinline__ void act_put(uint8_t* row, int col, int wide, int stride, uint2 q, uint32_t e)
+static __device__ __forceinline__ void act_put(uint8_t* row, uint32_t col, uint32_t wide, uint32_t stride, uint2 q, uint32_t e)
 {
     *reinterpret_cast<uint2*>(row + col) = q;
-    const int sub = (col >> 3) & 3;
+    const uint32_t sub = (col >> 3) & 3;
     if (sub == 0) row[wide + (col >> 5)] = (uint8_t)e;
     if (col + 8 * (4 - sub) == wide)
-        for (int i = wide + (wide >> 5) + sub; i < stride; i += 4) row[i] = 0;
+        for (uint32_t i = wide + (wide >> 5) + sub; i < stride; i += 4) row[i] = 0;
 }
 
 // Largest magnitude of three, NaN if any is.
@@ -174,10 +174,16 @@ static __device__ __forceinline__ void act_store_small(const f32x2_t (&v)[4], ui
 // ---- a chunk as it lies in memory (T: 0 fp16, 1 bf16, 2 fp32) ------------------------
 template <int T> struct Raw { uint4 q[T == 2 ? 2 : 1]; };
 
-// Elements i .. i+8 of p, those at or past n (of the chunk's eight) read as 0.  `vec`: the
-// address is 16-byte aligned.  WHOLE: that is known, and n is at least 8 or at most 0.
+// Elements i .. i+8 of a row, those at or past n (of the chunk's eight) read as 0.  `vec`: the
+// row is 16-byte aligned.  WHOLE: that is known, and n is at least 8 or at most 0.  The row's
+// address is the same in all threads and i is not, so the sum needs no arithmetic a thread.
+template <int T>
+static __device__ __forceinline__ const void* row_of(const void* p, int64_t row, uint32_t ld)
+{
+    return static_cast<const char*>(p) + row * (int64_t)((uint64_t)ld * (T == 2 ? 4 : 2));
+}
 template <int T, bool WHOLE = false>
-static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* p, int64_t i, int n, bool vec)
+static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* p, uint32_t i, int n, bool vec)
 {
     if ((WHOLE || vec) && n >= 8) {
         if (T == 2) {
@@ -224,8 +230,9 @@ static __device__ __forceinline__ void widen_chunk(const Raw<T>& r, f32x2_t (&v)
 }
 
 template <int T, bool WHOLE = false>
-static __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, bool vec, const f32x2_t (&v)[4])
+static __device__ __forceinline__ void store_chunk(const void* row, uint32_t i, int n, bool vec, const f32x2_t (&v)[4])
 {
+    void* p = const_cast<void*>(row);
     float x[8];
 #pragma unroll
     for (int j = 0; j < 4; j++) unpack2(v[j], x[2 * j], x[2 * j + 1]);

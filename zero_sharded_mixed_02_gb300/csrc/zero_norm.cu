@@ -234,8 +234,8 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.ldh = (uint32_t)ldh; a.ldy = (uint32_t)ldy; a.ldho = (uint32_t)ldho; a.ldx = (uint32_t)ldx;
     a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
     a.cols = (int)d.cols;
-    a.wide = (int)act_wide(d.cols);
-    a.stride = (int)act_stride(d.cols);
+    a.wide = (uint32_t)act_wide(d.cols);
+    a.stride = (uint32_t)act_stride(d.cols);
     a.lo = act_lo(d.dtype);
     a.hi = act_hi(d.dtype);
     a.post = d.post; a.pre = d.pre;
@@ -248,11 +248,11 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.vec_w = vec_weights(d);
     a.vec_g = vec_rows(d.gate, d.cols, d.dtype);
     int v = 1, threads = 32;
-    row_shape(a.wide, v, threads);
-    const bool whole = d.cols % 8 == 0 && a.vec_h && (!y || a.vec_y) && (!h_out || a.vec_ho) && (!x || a.vec_x) &&
-                       a.vec_w && (!d.gate || a.vec_g);
-    const void* fn = d.dtype == ZERO_FP16 ? norm_forward_fp16(d.res_dtype, v, whole)
-                                          : norm_forward_bf16(d.res_dtype, v, whole);
+    row_shape((int)a.wide, v, threads);
+    const bool whole = d.cols % 8 == 0 && y && a.vec_h && a.vec_y && a.vec_ho && (!x || a.vec_x) && a.vec_w &&
+                       (!d.gate || a.vec_g);
+    const void* fn = d.dtype == ZERO_FP16 ? norm_forward_fp16(d.res_dtype, v, d.post, d.pre, whole)
+                                          : norm_forward_bf16(d.res_dtype, v, d.post, d.pre, whole);
     const int64_t most = resident(fn, threads);
     if (most == 0) return ZERO_ECUDA;
     void* args[] = {&a};
@@ -296,7 +296,7 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     }
     const bool sums = dpost_w || dpost_b || dgate || dpre_w || dpre_b;
     if (sums && (!work || !aligned_to(work, 16))) return ZERO_EINVAL;
-    const bool two = dpre_b || dpost_b || (dgate && d.post_b);
+    bool two = dpre_b || dpost_b || (dgate && d.post_b);
     int64_t blocks = 0;
     float *pre_part = nullptr, *post_part = nullptr, *slots = nullptr;
     if (d.rows > 0) {
@@ -310,8 +310,8 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.lddho = (uint32_t)lddho; a.lddx = (uint32_t)lddx; a.lddh = (uint32_t)lddh; a.lddy = (uint32_t)lddy;
         a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
         a.cols = (int)d.cols;
-        a.wide = (int)act_wide(d.cols);
-        a.stride = (int)act_stride(d.cols);
+        a.wide = (uint32_t)act_wide(d.cols);
+        a.stride = (uint32_t)act_stride(d.cols);
         a.post = d.post; a.pre = d.pre;
         a.alpha = d.alpha;
         a.inv_cols = 1.0f / (float)d.cols;
@@ -322,11 +322,12 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.vec_w = vec_weights(d);
         a.vec_g = vec_rows(d.gate, d.cols, d.dtype);
         int v = 1, threads = 32;
-        row_shape(a.wide, v, threads);
-        const bool whole = d.cols % 8 == 0 && (!dh_out || a.vec_dho) && (!dx || a.vec_dx) && (!dh || a.vec_dh) &&
-                           (!dy || a.vec_dy) && a.vec_w && (!d.gate || a.vec_g);
-        const void* fn = d.dtype == ZERO_FP16 ? norm_backward_fp16(d.res_dtype, v, two, whole)
-                                              : norm_backward_bf16(d.res_dtype, v, two, whole);
+        row_shape((int)a.wide, v, threads);
+        const bool whole = d.cols % 8 == 0 && dy && (!dh_out || a.vec_dho) && (!dx || a.vec_dx) &&
+                           (!dh || a.vec_dh) && a.vec_dy && a.vec_w && (!d.gate || a.vec_g);
+        const void* fn = d.dtype == ZERO_FP16
+                             ? norm_backward_fp16(d.res_dtype, v, d.post, d.pre, whole, two)
+                             : norm_backward_bf16(d.res_dtype, v, d.post, d.pre, whole, two);
         blocks = resident(fn, threads);
         if (blocks == 0) return ZERO_ECUDA;
         if (blocks > ZERO_NORM_BLOCKS) blocks = ZERO_NORM_BLOCKS;

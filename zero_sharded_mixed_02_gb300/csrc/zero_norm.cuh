@@ -31,7 +31,9 @@ struct NormArgs {
     float* stats;
     uint32_t ldh, ldy, ldho, ldx;
     uint32_t rows, group;              // group >= 1
-    int cols, wide, stride, lo, hi;
+    int cols;
+    uint32_t wide, stride;
+    int lo, hi;
     int post, pre;
     float eps, alpha, inv_cols;
     int vec_h, vec_y, vec_ho, vec_x, vec_w, vec_g;
@@ -47,17 +49,19 @@ struct NormBwdArgs {
     float* slots;            // [blocks + groups][sums][wide]: S (and S0) of a block's rows of a group
     uint32_t lddho, lddx, lddh, lddy;
     uint32_t rows, group;
-    int cols, wide, stride, post, pre;
+    int cols;
+    uint32_t wide, stride;
+    int post, pre;
     float alpha, inv_cols;
     int vec_dho, vec_dx, vec_dh, vec_dy, vec_w, vec_g;
 };
 
-// Kernels by type of the stream (DT or fp32), chunks per thread (1, 2, 4), both sums wanted,
-// and whether every row and weight is read in whole aligned chunks.
-const void* norm_forward_fp16(int res, int v, bool whole);
-const void* norm_forward_bf16(int res, int v, bool whole);
-const void* norm_backward_fp16(int res, int v, bool two, bool whole);
-const void* norm_backward_bf16(int res, int v, bool two, bool whole);
+// Kernels by type of the stream (DT or fp32), chunks per thread (1, 2, 4), the norms' kinds,
+// and whether every row and weight is read in whole aligned chunks (and y or dy is there).
+const void* norm_forward_fp16(int res, int v, int post, int pre, bool whole);
+const void* norm_forward_bf16(int res, int v, int post, int pre, bool whole);
+const void* norm_backward_fp16(int res, int v, int post, int pre, bool whole, bool& two);
+const void* norm_backward_bf16(int res, int v, int post, int pre, bool whole, bool& two);
 
 // Rows [row0(b), row0(b + 1)) belong to block b; the block of row r is the largest b with row0(b) <= r.
 __host__ __device__ inline int64_t norm_row0(int64_t b, int64_t rows, int64_t blocks) { return b * rows / blocks; }
@@ -68,7 +72,7 @@ __host__ __device__ inline int64_t norm_block_of(int64_t r, int64_t rows, int64_
 
 // Eight weights (cached: every row of a block reads the same ones).
 template <int DT, bool WHOLE>
-static __device__ __forceinline__ void load_weights(const void* p, int64_t i, int n, bool vec, f32x2_t (&v)[4])
+static __device__ __forceinline__ void load_weights(const void* p, uint32_t i, int n, bool vec, f32x2_t (&v)[4])
 {
     Raw<DT> r;
     const uint16_t* w = static_cast<const uint16_t*>(p);
@@ -176,21 +180,26 @@ static __device__ __forceinline__ void normalise(f32x2_t (&v)[V][4], const int (
     for (int c = 0; c < V; c++) times(v[c], both(rstd));
 }
 
-// WHOLE: every chunk of every matrix and weight is whole and aligned (cols a multiple of
-// 8); otherwise each tensor's flag says how it is read.  Two blocks of one row an SM
-// (16 warps each, 64 registers) beat one block of two rows at a time, which does fewer
-// instructions (weights and branches shared) but leaves half the warps to hide latencies:
-// 165 against 174 us at 16384 x 4096 with an fp32 stream.
-template <int DT, int RT, int V, bool WHOLE>
+// POST and PRE: the norms' kinds (zero_norm_kind_t) for rows of whole aligned chunks with a
+// block (y) in them; -1: any kinds, sizes and alignments, by the arguments.  Knowing them
+// saves a fifth of the instructions, which bound the pass next to HBM.  Two blocks of one row
+// an SM (16 warps each, 64 registers) beat one block of two rows at a time, which does
+// fewer instructions (weights and branches shared) but leaves half the warps to hide
+// latencies: 165 against 174 us at 16384 x 4096 with an fp32 stream.
+template <int DT, int RT, int V, int POST, int PRE>
 __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
     k_norm_forward(const __grid_constant__ NormArgs a)
 {
+    constexpr bool WHOLE = POST >= 0;
+    const int post = WHOLE ? POST : a.post, pre = WHOLE ? PRE : a.pre;
+    const bool block = WHOLE || a.y;
     __shared__ norm_buf_t buf;
-    int turn = 0, col[V], n[V];
+    int turn = 0, n[V];
+    uint32_t col[V];
 #pragma unroll
     for (int c = 0; c < V; c++) {
         col[c] = 8 * (threadIdx.x + c * blockDim.x);
-        n[c] = a.cols - col[c];
+        n[c] = a.cols - (int)col[c];
     }
     Raw<RT> rh[V];
     Raw<DT> ry[V];
@@ -198,10 +207,11 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
     uint32_t row = (uint32_t)norm_row0(blockIdx.x, a.rows, gridDim.x);
     uint32_t grp = row / a.group, in_group = row - grp * a.group;
     auto fetch = [&](uint32_t at) {
+        const void *ph = row_of<RT>(a.h, at, a.ldh), *py = row_of<DT>(a.y, at, a.ldy);
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            load_chunk<RT, WHOLE>(rh[c], a.h, (int64_t)at * a.ldh + col[c], n[c], a.vec_h);
-            if (a.y) load_chunk<DT, WHOLE>(ry[c], a.y, (int64_t)at * a.ldy + col[c], n[c], a.vec_y);
+            load_chunk<RT, WHOLE>(rh[c], ph, col[c], n[c], a.vec_h);
+            if (block) load_chunk<DT, WHOLE>(ry[c], py, col[c], n[c], a.vec_y);
         }
     };
     fetch(row);
@@ -210,29 +220,30 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
 #pragma unroll
         for (int c = 0; c < V; c++) {
             widen_chunk<RT>(rh[c], h[c]);
-            if (a.y) widen_chunk<DT>(ry[c], y[c]);
+            if (block) widen_chunk<DT>(ry[c], y[c]);
         }
         if (row + 1 < end) fetch(row + 1);
         float mu2 = 0.0f, r2 = 1.0f, mu1 = 0.0f, r1 = 1.0f;
-        if (a.y) {
-            if (a.post) normalise<V>(y, n, a.post, a.eps, a.inv_cols, mu2, r2, buf, turn);
+        if (block) {
+            if (post) normalise<V>(y, n, post, a.eps, a.inv_cols, mu2, r2, buf, turn);
+            const void* gate = row_of<DT>(a.gate, grp, a.cols);
 #pragma unroll
             for (int c = 0; c < V; c++) {
                 if (a.ckpt_y) {
                     uint8_t* p = a.ckpt_y + (int64_t)row * a.stride;
-                    if (a.post) act_store_small(y[c], p, col[c], a.wide, a.stride, a.lo, col[c] < a.wide);
+                    if (post) act_store_small(y[c], p, col[c], a.wide, a.stride, a.lo, col[c] < a.wide);
                     else act_store(y[c], p, col[c], a.wide, a.stride, a.lo, a.hi, col[c] < a.wide);
                 }
-                if (a.post_w) {
+                if (post && a.post_w) {
                     load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, w);
                     times(y[c], w);
                 }
-                if (a.post_b) {
+                if (post && a.post_b) {
                     load_weights<DT, WHOLE>(a.post_b, col[c], n[c], a.vec_w, w);
                     plus(y[c], w);
                 }
                 if (a.gate) {
-                    load_weights<DT, WHOLE>(a.gate, (int64_t)grp * a.cols + col[c], n[c], a.vec_g, w);
+                    load_weights<DT, WHOLE>(gate, col[c], n[c], a.vec_g, w);
                     times(y[c], w);
                 }
                 const f32x2_t alpha = both(a.alpha);
@@ -240,12 +251,14 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                 for (int j = 0; j < 4; j++) h[c][j] = fma2(alpha, y[c][j], h[c][j]);
             }
         }
-        if (a.h_out)
+        if (WHOLE || a.h_out) {
+            const void* p = row_of<RT>(a.h_out, row, a.ldho);
 #pragma unroll
-            for (int c = 0; c < V; c++)
-                store_chunk<RT, WHOLE>(a.h_out, (int64_t)row * a.ldho + col[c], n[c], a.vec_ho, h[c]);
-        if (a.pre) {
-            normalise<V>(h, n, a.pre, a.eps, a.inv_cols, mu1, r1, buf, turn);
+            for (int c = 0; c < V; c++) store_chunk<RT, WHOLE>(p, col[c], n[c], a.vec_ho, h[c]);
+        }
+        if (pre) {
+            normalise<V>(h, n, pre, a.eps, a.inv_cols, mu1, r1, buf, turn);
+            const void* px = row_of<DT>(a.x, row, a.ldx);
 #pragma unroll
             for (int c = 0; c < V; c++) {
                 if (a.ckpt_x)
@@ -259,7 +272,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                     load_weights<DT, WHOLE>(a.pre_b, col[c], n[c], a.vec_w, w);
                     plus(h[c], w);
                 }
-                store_chunk<DT, WHOLE>(a.x, (int64_t)row * a.ldx + col[c], n[c], a.vec_x, h[c]);
+                store_chunk<DT, WHOLE>(px, col[c], n[c], a.vec_x, h[c]);
             }
         }
         if (a.stats && threadIdx.x == 0)
@@ -291,47 +304,34 @@ static __device__ __forceinline__ void get_sums(const float* p, f32x2_t (&v)[4])
     }
 }
 
-// sum of a b, of a
-template <int V>
-static __device__ __forceinline__ float dot(const f32x2_t (&a)[V][4], const f32x2_t (&b)[V][4])
-{
-    f32x2_t t = both(0.0f);
-#pragma unroll
-    for (int c = 0; c < V; c++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) t = fma2(a[c][j], b[c][j], t);
-    return either(t);
-}
-template <int V>
-static __device__ __forceinline__ float total(const f32x2_t (&a)[V][4])
-{
-    f32x2_t t = both(0.0f);
-#pragma unroll
-    for (int c = 0; c < V; c++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) t = add2(t, a[c][j]);
-    return either(t);
-}
-
 // One reduction a row serves both norms.  With g = pre_w dx, u = gate post_w and
 // B = dh_out + r1 g,
 //   D = B - r1 (mean(g) + mean(g xh) xh),
 // so the post-norm's sums of u D and u D yh follow from sums that do not need D:
 //   sum u yh D = sum u yh B - r1 (mean(g) sum u yh + mean(g xh) sum u yh xh)
 // and the same without yh.  A second reduction, after D, would cost its latency once more.
-template <int DT, int RT, int V, bool TWO, bool WHOLE>
+//
+// POST and PRE as in the forward pass (known kinds: whole aligned rows with dy wanted).
+template <int DT, int RT, int V, int POST, int PRE, bool TWO>
 __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __grid_constant__ NormBwdArgs a)
 {
     // one wave of blocks: the kernel that adds their sums may be placed already
     asm volatile("griddepcontrol.launch_dependents;");
+    constexpr bool WHOLE = POST >= 0;
+    const int post = WHOLE ? POST : a.post, pre = WHOLE ? PRE : a.pre;
     __shared__ norm_buf_t buf;
     constexpr int SUMS = TWO ? 2 : 1;
-    int turn = 0, col[V], n[V];
+    // with more than one chunk a thread, what follows from the codes and weights is made again
+    // after the reduction rather than held across it
+    constexpr bool AGAIN = V > 1;
+    constexpr int KEEP = AGAIN ? 1 : V;
+    int turn = 0, n[V];
+    uint32_t col[V];
     f32x2_t pw[V][4], sw[V][4], pb[TWO ? V : 1][4], sb[TWO ? V : 1][4];
 #pragma unroll
     for (int c = 0; c < V; c++) {
         col[c] = 8 * (threadIdx.x + c * blockDim.x);
-        n[c] = a.cols - col[c];
+        n[c] = a.cols - (int)col[c];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             pw[c][j] = sw[c][j] = both(0.0f);
@@ -348,14 +348,15 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
     float r1 = 1.0f, r2 = 1.0f;
     auto fetch = [&](uint32_t r) {
         const uint8_t *px = a.ckpt_x + (int64_t)r * a.stride, *py = a.ckpt_y + (int64_t)r * a.stride;
+        const void *pd = row_of<RT>(a.dh_out, r, a.lddho), *pdx = row_of<DT>(a.dx, r, a.lddx);
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            if (a.dh_out) load_chunk<RT, WHOLE>(rd[c], a.dh_out, (int64_t)r * a.lddho + col[c], n[c], a.vec_dho);
-            if (a.pre) load_chunk<DT, WHOLE>(rx[c], a.dx, (int64_t)r * a.lddx + col[c], n[c], a.vec_dx);
+            if (a.dh_out) load_chunk<RT, WHOLE>(rd[c], pd, col[c], n[c], a.vec_dho);
+            if (pre) load_chunk<DT, WHOLE>(rx[c], pdx, col[c], n[c], a.vec_dx);
             qx[c] = qy[c] = make_uint2(0, 0);
             ex[c] = ey[c] = 0;
-            if (col[c] < a.cols) {
-                if (a.pre) {
+            if (n[c] > 0) {
+                if (pre) {
                     qx[c] = __ldcs(reinterpret_cast<const uint2*>(px + col[c]));
                     ex[c] = __ldg(px + a.wide + (col[c] >> 5));
                 }
@@ -370,6 +371,17 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             r2 = st.y;
             r1 = st.w;
         }
+    };
+    auto scales = [&](int c, f32x2_t (&u)[4]) {              // gate post_w
+        f32x2_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) u[j] = both(1.0f);
+        if (a.gate) load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, u);
+        if (post && a.post_w) {
+            load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, w);
+            times(u, w);
+        }
+        end_of_row(u, n[c]);
     };
     // The sums of the block's rows of group grp go to the slot block + group: along the
     // rows both only grow, so no two pairs share one.  Times the group's gate they are
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                 float* p = a.post_part + (int64_t)blockIdx.x * SUMS * a.wide + col[c];
                 if (a.gate) {
                     f32x2_t w[4];
-                    load_weights<DT, WHOLE>(a.gate, (int64_t)grp * a.cols + col[c], n[c], a.vec_g, w);
+                    load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, w);
                     times(sw[c], w);
                     if (TWO) times(sb[c], w);
                 }
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
         }
         again = true;
     };
-    const bool sums = a.slots || a.post_part, layer = a.pre == ZERO_NORM_LAYER || a.post == ZERO_NORM_LAYER;
+    const bool sums = a.slots || a.post_part, layer = pre == ZERO_NORM_LAYER || post == ZERO_NORM_LAYER;
     fetch(row);
     for (; row < end; row++) {
         if (left == 0) {
@@ -417,17 +429,22 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             left = a.group;
         }
         left--;
-        f32x2_t b[V][4], u[V][4], xh[V][4], yh[V][4], w[4];
+        f32x2_t b[V][4], u[KEEP][4], xh[KEEP][4], yh[KEEP][4], t[8];
         const float k1 = r1, k2 = r2;
-        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        uint2 cx[V], cy[V];                                  // the row's codes, when read again after the sums
+        uint32_t fx[V], fy[V];
+#pragma unroll
+        for (int k = 0; k < 8; k++) t[k] = both(0.0f);
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            if (a.pre) {
+            const int q = AGAIN ? 0 : c;
+            f32x2_t w[4];
+            if (pre) {                                       // b = g
                 widen_chunk<DT>(rx[c], b[c]);
-                act_values(qx[c], ex[c], xh[c]);
+                act_values(qx[c], ex[c], xh[q]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    pw[c][j] = fma2(b[c][j], xh[c][j], pw[c][j]);
+                    pw[c][j] = fma2(b[c][j], xh[q][j], pw[c][j]);
                     if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
                 }
                 if (a.pre_w) {
@@ -436,89 +453,102 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; j++) b[c][j] = xh[c][j] = both(0.0f);
+                for (int j = 0; j < 4; j++) b[c][j] = xh[q][j] = both(0.0f);
             }
-            act_values(qy[c], ey[c], yh[c]);
-#pragma unroll
-            for (int j = 0; j < 4; j++) u[c][j] = both(1.0f);
-            if (a.gate) load_weights<DT, WHOLE>(a.gate, (int64_t)grp * a.cols + col[c], n[c], a.vec_g, u[c]);
-            if (a.post_w) {
-                load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, w);
-                times(u[c], w);
-            }
-            end_of_row(u[c], n[c]);
-        }
-        s[0] = dot<V>(b, xh);
-        if (layer) s[3] = total<V>(b);
-#pragma unroll
-        for (int c = 0; c < V; c++) {                        // b = B from here, xh and yh as read
-#pragma unroll
-            for (int j = 0; j < 4; j++) w[j] = both(0.0f);
-            if (a.dh_out) widen_chunk<RT>(rd[c], w);
-#pragma unroll
-            for (int j = 0; j < 4; j++) b[c][j] = fma2(both(k1), b[c][j], w[j]);
-        }
-        if (row + 1 < end) fetch(row + 1);
-        {
-            f32x2_t uy[V][4];
-#pragma unroll
-            for (int c = 0; c < V; c++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) uy[c][j] = mul2(u[c][j], yh[c][j]);
-            s[1] = dot<V>(uy, b);
-            s[2] = dot<V>(uy, xh);
-            if (layer) {
-                s[4] = total<V>(uy);
-                s[5] = dot<V>(u, b);
-                s[6] = total<V>(u);
-                s[7] = dot<V>(u, xh);
-            }
-        }
-        if (layer) {
-            block_sum<8>(s, buf, turn);
-        } else {
-            float t[3] = {s[0], s[1], s[2]};
-            block_sum<3>(t, buf, turn);
-            s[0] = t[0];
-            s[1] = t[1];
-            s[2] = t[2];
-        }
-        // D = b - p1 xh - p0;  dy = alpha r2 (u D - q1 yh - q0)
-        const float p1 = k1 * s[0] * a.inv_cols, p0 = a.pre == ZERO_NORM_LAYER ? k1 * s[3] * a.inv_cols : 0.0f;
-#pragma unroll
-        for (int c = 0; c < V; c++)
+            act_values(qy[c], ey[c], yh[q]);
+            scales(c, u[q]);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                if (layer) b[c][j] = sub2(b[c][j], both(p0));
-                b[c][j] = fma2(both(-p1), xh[c][j], b[c][j]);
+                if (pre) t[0] = fma2(b[c][j], xh[q][j], t[0]);
+                if (pre == ZERO_NORM_LAYER) t[3] = add2(t[3], b[c][j]);
+                w[j] = both(0.0f);
             }
-        if (a.dh)
+            if (a.dh_out) widen_chunk<RT>(rd[c], w);
 #pragma unroll
-            for (int c = 0; c < V; c++)
-                store_chunk<RT, WHOLE>(a.dh, (int64_t)row * a.lddh + col[c], n[c], a.vec_dh, b[c]);
-        if (!a.dy) continue;
-        if (sums)
-#pragma unroll
-            for (int c = 0; c < V; c++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    sw[c][j] = fma2(b[c][j], yh[c][j], sw[c][j]);
-                    if (TWO) sb[c][j] = add2(sb[c][j], b[c][j]);
+            for (int j = 0; j < 4; j++) {
+                b[c][j] = fma2(both(k1), b[c][j], w[j]);     // b = B
+                if (post) {
+                    const f32x2_t uy = mul2(u[q][j], yh[q][j]);
+                    t[1] = fma2(uy, b[c][j], t[1]);
+                    if (pre) t[2] = fma2(uy, xh[q][j], t[2]);
+                    if (pre == ZERO_NORM_LAYER) t[4] = add2(t[4], uy);
                 }
+                if (post == ZERO_NORM_LAYER) {
+                    t[5] = fma2(u[q][j], b[c][j], t[5]);
+                    if (pre == ZERO_NORM_LAYER) t[6] = add2(t[6], u[q][j]);
+                    if (pre) t[7] = fma2(u[q][j], xh[q][j], t[7]);
+                }
+            }
+            if (AGAIN) {
+                cx[c] = qx[c]; cy[c] = qy[c];
+                fx[c] = ex[c]; fy[c] = ey[c];
+            }
+        }
+        if (row + 1 < end) fetch(row + 1);
+        float s[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) s[k] = either(t[k]);
+        if (!WHOLE || (layer && POST > 0)) {
+            if (layer) {
+                block_sum<8>(s, buf, turn);
+            } else {
+                float three[3] = {s[0], s[1], s[2]};
+                block_sum<3>(three, buf, turn);
+                s[0] = three[0];
+                s[1] = three[1];
+                s[2] = three[2];
+            }
+        } else if (POST > 0) {
+            float three[3] = {s[0], s[1], s[2]};
+            block_sum<3>(three, buf, turn);
+            s[0] = three[0];
+            s[1] = three[1];
+            s[2] = three[2];
+        } else {                                             // the pre-norm alone
+            float two[2] = {s[0], s[3]};
+            block_sum<2>(two, buf, turn);
+            s[0] = two[0];
+            s[3] = two[1];
+        }
+        // D = b - p1 xh - p0;  dy = alpha r2 (u D - q1 yh - q0)
+        const float p1 = k1 * s[0] * a.inv_cols, p0 = pre == ZERO_NORM_LAYER ? k1 * s[3] * a.inv_cols : 0.0f;
+        const void *pdh = row_of<RT>(a.dh, row, a.lddh), *pdy = row_of<DT>(a.dy, row, a.lddy);
         float scale = a.alpha, q1 = 0.0f, q0 = 0.0f;
-        if (a.post) {
+        if (post) {
             scale *= k2;
             q1 = (s[1] - p0 * s[4] - p1 * s[2]) * a.inv_cols;
-            if (a.post == ZERO_NORM_LAYER) q0 = (s[5] - p0 * s[6] - p1 * s[7]) * a.inv_cols;
+            if (post == ZERO_NORM_LAYER) q0 = (s[5] - p0 * s[6] - p1 * s[7]) * a.inv_cols;
         }
 #pragma unroll
         for (int c = 0; c < V; c++) {
+            const int q = AGAIN ? 0 : c;
+            if (AGAIN) {
+                // (the empty statement keeps the compiler from holding the first reading)
+                asm volatile("" : "+r"(cx[c].x), "+r"(cx[c].y), "+r"(cy[c].x), "+r"(cy[c].y));
+                act_values(cx[c], fx[c], xh[q]);
+                act_values(cy[c], fy[c], yh[q]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const f32x2_t e = layer ? fma2(u[c][j], b[c][j], both(-q0)) : mul2(u[c][j], b[c][j]);
-                b[c][j] = mul2(both(scale), fma2(both(-q1), yh[c][j], e));
+                if (pre == ZERO_NORM_LAYER) b[c][j] = sub2(b[c][j], both(p0));
+                b[c][j] = fma2(both(-p1), xh[q][j], b[c][j]);
             }
-            store_chunk<DT, WHOLE>(a.dy, (int64_t)row * a.lddy + col[c], n[c], a.vec_dy, b[c]);
+            if (a.dh) store_chunk<RT, WHOLE>(pdh, col[c], n[c], a.vec_dh, b[c]);
+            if (!WHOLE && !a.dy) continue;
+            if (sums)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    sw[c][j] = fma2(b[c][j], yh[q][j], sw[c][j]);
+                    if (TWO) sb[c][j] = add2(sb[c][j], b[c][j]);
+                }
+            if (AGAIN) scales(c, u[q]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f32x2_t e = post == ZERO_NORM_LAYER ? fma2(u[q][j], b[c][j], both(-q0)) : mul2(u[q][j], b[c][j]);
+                if (post) e = fma2(both(-q1), yh[q][j], e);
+                b[c][j] = mul2(both(scale), e);
+            }
+            store_chunk<DT, WHOLE>(pdy, col[c], n[c], a.vec_dy, b[c]);
         }
     }
     if (sums) flush();
@@ -534,30 +564,31 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
 }
 
 template <int DT, int RT, int V>
-static const void* norm_forward_of(bool whole)
+static const void* norm_forward_of(int post, int pre, bool whole)
 {
-    return whole ? (const void*)k_norm_forward<DT, RT, V, true> : (const void*)k_norm_forward<DT, RT, V, false>;
+    if (whole) {
+        if (post == 0 && pre == 1) return (const void*)k_norm_forward<DT, RT, V, 0, 1>;
+        if (post == 0 && pre == 2) return (const void*)k_norm_forward<DT, RT, V, 0, 2>;
+        if (post == 1 && pre == 1) return (const void*)k_norm_forward<DT, RT, V, 1, 1>;
+        if (post == 2 && pre == 2) return (const void*)k_norm_forward<DT, RT, V, 2, 2>;
+    }
+    return (const void*)k_norm_forward<DT, RT, V, -1, -1>;
 }
+// `two`: both sums are wanted; set where the kernel keeps both all the same.
 template <int DT, int RT, int V>
-static const void* norm_backward_of(bool two, bool whole)
+static const void* norm_backward_of(int post, int pre, bool whole, bool& two)
 {
-    if (two)
-        return whole ? (const void*)k_norm_backward<DT, RT, V, true, true>
-                     : (const void*)k_norm_backward<DT, RT, V, true, false>;
-    return whole ? (const void*)k_norm_backward<DT, RT, V, false, true>
-                 : (const void*)k_norm_backward<DT, RT, V, false, false>;
-}
-template <int DT, int RT>
-static const void* norm_forward_of(int v, bool whole)
-{
-    return v == 1 ? norm_forward_of<DT, RT, 1>(whole) : v == 2 ? norm_forward_of<DT, RT, 2>(whole)
-                                                               : norm_forward_of<DT, RT, 4>(whole);
-}
-template <int DT, int RT>
-static const void* norm_backward_of(int v, bool two, bool whole)
-{
-    return v == 1 ? norm_backward_of<DT, RT, 1>(two, whole) : v == 2 ? norm_backward_of<DT, RT, 2>(two, whole)
-                                                                     : norm_backward_of<DT, RT, 4>(two, whole);
+    if (whole && (!two || pre == 2)) {
+        if (post == 0 && pre == 1) return (const void*)k_norm_backward<DT, RT, V, 0, 1, false>;
+        if (post == 1 && pre == 1) return (const void*)k_norm_backward<DT, RT, V, 1, 1, false>;
+        if (pre == 2 && (post == 0 || post == 2)) {
+            two = true;
+            return post == 0 ? (const void*)k_norm_backward<DT, RT, V, 0, 2, true>
+                             : (const void*)k_norm_backward<DT, RT, V, 2, 2, true>;
+        }
+    }
+    return two ? (const void*)k_norm_backward<DT, RT, V, -1, -1, true>
+               : (const void*)k_norm_backward<DT, RT, V, -1, -1, false>;
 }
 
 }  // namespace zero

@@ -1,7 +1,14 @@
-// The block norms' backward kernels for bf16 (zero_norm.cuh).
+// The block norms' backward kernels for bf16 (zero_norm.cuh); the stream in the same type.
 #include "zero_norm.cuh"
 
-const void* zero::norm_backward_bf16(int res, int v, bool two, bool whole)
+namespace zero {
+const void* norm_backward_bf16_fp32(int res, int v, int post, int pre, bool whole, bool& two);
+}
+
+const void* zero::norm_backward_bf16(int res, int v, int post, int pre, bool whole, bool& two)
 {
-    return res == 2 ? norm_backward_of<1, 2>(v, two, whole) : norm_backward_of<1, 1>(v, two, whole);
+    if (res == 2) return norm_backward_bf16_fp32(res, v, post, pre, whole, two);
+    return v == 1   ? norm_backward_of<1, 1, 1>(post, pre, whole, two)
+           : v == 2 ? norm_backward_of<1, 1, 2>(post, pre, whole, two)
+                    : norm_backward_of<1, 1, 4>(post, pre, whole, two);
 }

@@ -1,7 +1,14 @@
-// The block norms' forward kernels for fp16 (zero_norm.cuh).
+// The block norms' forward kernels for fp16 (zero_norm.cuh); the stream in the same type.
 #include "zero_norm.cuh"
 
-const void* zero::norm_forward_fp16(int res, int v, bool whole)
+namespace zero {
+const void* norm_forward_fp16_fp32(int res, int v, int post, int pre, bool whole);
+}
+
+const void* zero::norm_forward_fp16(int res, int v, int post, int pre, bool whole)
 {
-    return res == 2 ? norm_forward_of<0, 2>(v, whole) : norm_forward_of<0, 0>(v, whole);
+    if (res == 2) return norm_forward_fp16_fp32(res, v, post, pre, whole);
+    return v == 1   ? norm_forward_of<0, 0, 1>(post, pre, whole)
+           : v == 2 ? norm_forward_of<0, 0, 2>(post, pre, whole)
+                    : norm_forward_of<0, 0, 4>(post, pre, whole);
 }

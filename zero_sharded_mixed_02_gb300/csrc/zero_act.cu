@@ -23,15 +23,14 @@ struct ActArgs {
     uint32_t ld;
     uint32_t chunks;        // rows * per_row, below 2^31
     uint32_t per_row;       // chunks of a row
-    uint32_t magic, shift;  // q / per_row = (q * magic) >> (32 + shift) for q < 2^31
+    uint32_t magic, shift;  // q / per_row = (q * magic) >> (32 + shift) for q < 2^31; 0: per_row is 1
     int cols, wide, stride; // columns, code bytes and bytes of a checkpoint row
     int lo, hi;
-    int vec;                // rows of x are 16-byte aligned
 };
 
 static __device__ __forceinline__ void act_place(const ActArgs& a, uint32_t q, int64_t& row, int& col)
 {
-    const uint32_t r = __umulhi(q, a.magic) >> a.shift;
+    const uint32_t r = a.magic ? __umulhi(q, a.magic) >> a.shift : q;
     row = r;
     col = (int)(q - r * a.per_row) * 8;
 }
@@ -40,17 +39,14 @@ static __device__ __forceinline__ void act_place(const ActArgs& a, uint32_t q, i
 template <int T>
 static __device__ __forceinline__ uint32_t act_amax(const Raw<T>& r)
 {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+    uint32_t m = 0;
     if (T == 2) {
-        const uint32_t x[4] = {r.q[T == 2].x, r.q[T == 2].y, r.q[T == 2].z, r.q[T == 2].w};
-        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; j++) m = max(m, max(w[j] & 0x7FFFFFFFu, x[j] & 0x7FFFFFFFu));
+        for (int j = 0; j < (T == 2 ? 8 : 4); j++) m = max(m, r.w[j] & 0x7FFFFFFFu);
         return m;
     }
-    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j++) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    for (int j = 0; j < 4; j++) m = __vmaxu2(m, r.w[j] & 0x7FFF7FFFu);
     return max(m & 0xFFFFu, m >> 16);                        // still in the 16-bit type
 }
 template <int T>
@@ -71,7 +67,7 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_save(const __grid_constant
         const uint32_t q = first + u * ZERO_THREADS;
         act_place(a, q, row[u], col[u]);
         if (q >= a.chunks) col[u] = a.wide;                  // nothing to read or write
-        load_chunk<T>(r[u], row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], a.vec);
+        load_chunk<T>(r[u], row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], true);
     }
 #pragma unroll
     for (int u = 0; u < ZERO_ACT_UNROLL; u++) {
@@ -110,7 +106,76 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_load(const __grid_constant
         if (col[u] < a.cols) {
             f32x2_t v[4];
             act_values(c[u], e[u], v);
-            store_chunk<T>(row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], a.vec, v);
+            store_chunk<T>(row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], true, nullptr, v);
+        }
+}
+
+// Rows that are not aligned to vectors: a warp takes ZERO_ACT_ANY blocks of 32 columns, a
+// lane a column of each, so that an access of the warp is one short run.  The flat list is
+// then of blocks (a.chunks, a.per_row count them).
+#define ZERO_ACT_ANY 8
+
+template <int T>
+__global__ void __launch_bounds__(ZERO_THREADS) k_act_save_any(const __grid_constant__ ActArgs a)
+{
+    const uint32_t first = (blockIdx.x * (ZERO_THREADS / 32) + (threadIdx.x >> 5)) * ZERO_ACT_ANY;
+    const int lane = threadIdx.x & 31;
+    float v[ZERO_ACT_ANY];
+    int64_t row[ZERO_ACT_ANY];
+    int col[ZERO_ACT_ANY];
+#pragma unroll
+    for (int u = 0; u < ZERO_ACT_ANY; u++) {
+        act_place(a, first + u, row[u], col[u]);
+        col[u] *= 4;                                         // place() counts columns by eights
+        v[u] = 0.0f;
+        if (first + u < a.chunks && col[u] + lane < a.cols) {
+            const uint32_t b = load_bits<T>(row_of<T>(a.x, row[u], a.ld), col[u] + lane);
+            v[u] = T == 2 ? __uint_as_float(b) : widen1<T & 1>((uint16_t)b);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < ZERO_ACT_ANY; u++) {
+        if (first + u >= a.chunks) break;
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[u]) & 0x7FFFFFFFu);
+        const uint32_t e = act_exponent(m, a.lo, a.hi);
+        uint8_t* p = a.ckpt + row[u] * a.stride;
+        float t = v[u] * __uint_as_float((254u - (e == ZERO_ACT_BAD ? 127u : e)) << 23);
+        t = __fadd_rn(fminf(fmaxf(t, -127.0f), 127.0f), 12582912.0f);
+        p[col[u] + lane] = e == ZERO_ACT_BAD ? 0 : (uint8_t)__float_as_uint(t);
+        const int blk = col[u] >> 5;
+        if (lane == 0) p[a.wide + blk] = (uint8_t)e;
+        if (blk + 1 == (a.wide >> 5) && a.wide + blk + 1 + lane < a.stride) p[a.wide + blk + 1 + lane] = 0;
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(ZERO_THREADS) k_act_load_any(const __grid_constant__ ActArgs a)
+{
+    const uint32_t first = (blockIdx.x * (ZERO_THREADS / 32) + (threadIdx.x >> 5)) * ZERO_ACT_ANY;
+    const int lane = threadIdx.x & 31;
+    int c[ZERO_ACT_ANY];
+    uint32_t e[ZERO_ACT_ANY];
+    int64_t row[ZERO_ACT_ANY];
+    int col[ZERO_ACT_ANY];
+#pragma unroll
+    for (int u = 0; u < ZERO_ACT_ANY; u++) {
+        act_place(a, first + u, row[u], col[u]);
+        col[u] *= 4;
+        c[u] = 0;
+        e[u] = 0;
+        if (first + u < a.chunks) {
+            const uint8_t* p = a.ckpt + row[u] * a.stride;
+            c[u] = (int8_t)__ldg(p + col[u] + lane);
+            e[u] = __ldg(p + a.wide + (col[u] >> 5));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < ZERO_ACT_ANY; u++)
+        if (first + u < a.chunks && col[u] + lane < a.cols) {
+            const float v = (float)c[u] * __uint_as_float(e[u] << 23);
+            void* p = const_cast<void*>(row_of<T>(a.x, row[u], a.ld));
+            if (T == 2) static_cast<float*>(p)[col[u] + lane] = v;
+            else static_cast<uint16_t*>(p)[col[u] + lane] = narrow1<T & 1>(v);
         }
 }
 
@@ -136,24 +201,25 @@ zero_status_t run(bool save, zero_dtype_t dtype, const void* x, int64_t rows, in
     a.cols = (int)cols;
     a.wide = (int)act_wide(cols);
     a.stride = (int)act_stride(cols);
-    a.per_row = (uint32_t)(a.wide / 8);
+    const bool vec = aligned_to(x, 16) && ld * size % 16 == 0;
+    a.per_row = (uint32_t)(a.wide / (vec ? 8 : 32));
     // ceil(log2 per_row) = l: magic = ceil(2^(31 + l) / per_row) fits 32 bits and is exact for q < 2^31
-    uint32_t l = 2;
+    // (from two chunks a row; 0 says one)
+    uint32_t l = 1;
     while ((1u << l) < a.per_row) l++;
-    a.magic = (uint32_t)(((1ull << (31 + l)) + a.per_row - 1) / a.per_row);
+    a.magic = a.per_row == 1 ? 0 : (uint32_t)(((1ull << (31 + l)) + a.per_row - 1) / a.per_row);
     a.shift = l - 1;
     a.ld = (uint32_t)ld;
     a.lo = act_lo(dtype);
     a.hi = act_hi(dtype);
-    a.vec = aligned_to(x, 16) && ld * size % 16 == 0;
-    const void* fn = save ? (dtype == ZERO_FP16   ? (const void*)k_act_save<0>
-                             : dtype == ZERO_BF16 ? (const void*)k_act_save<1>
-                                                  : (const void*)k_act_save<2>)
-                          : (dtype == ZERO_FP16   ? (const void*)k_act_load<0>
-                             : dtype == ZERO_BF16 ? (const void*)k_act_load<1>
-                                                  : (const void*)k_act_load<2>);
+    static const void* const kernels[2][2][3] = {
+        {{(const void*)k_act_load_any<0>, (const void*)k_act_load_any<1>, (const void*)k_act_load_any<2>},
+         {(const void*)k_act_load<0>, (const void*)k_act_load<1>, (const void*)k_act_load<2>}},
+        {{(const void*)k_act_save_any<0>, (const void*)k_act_save_any<1>, (const void*)k_act_save_any<2>},
+         {(const void*)k_act_save<0>, (const void*)k_act_save<1>, (const void*)k_act_save<2>}}};
+    const void* fn = kernels[save][vec][dtype];
     // as many rows a launch as keep its chunk numbers, the last block's idle ones too, below 2^31
-    const int64_t per_block = ZERO_ACT_UNROLL * ZERO_THREADS;
+    const int64_t per_block = vec ? ZERO_ACT_UNROLL * ZERO_THREADS : ZERO_ACT_ANY * ZERO_THREADS / 32;
     const int64_t most = ((1ll << 31) - per_block) / a.per_row;
     for (int64_t r = 0; r < rows; r += most) {
         const int64_t n = rows - r < most ? rows - r : most;

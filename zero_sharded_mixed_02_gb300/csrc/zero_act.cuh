@@ -172,89 +172,152 @@ static __device__ __forceinline__ void act_store_small(const f32x2_t (&v)[4], ui
 }
 
 // ---- a chunk as it lies in memory (T: 0 fp16, 1 bf16, 2 fp32) ------------------------
-template <int T> struct Raw { uint4 q[T == 2 ? 2 : 1]; };
+// Rows are read and written in 16-byte vectors where they are aligned to them.  Where they
+// are not, single elements 8 columns apart in neighbouring lanes would touch as many memory
+// sectors as lanes; instead the warp, whose 32 chunks are 256 consecutive columns, takes
+// 32 neighbouring columns an instruction and turns them into chunks (and back) through its
+// own 1 KB of shared memory (`stage`).  WHOLE: every row is aligned and every chunk lies
+// in the row (n >= 8) or past it (n <= 0).
+template <int T> struct Raw { uint32_t w[T == 2 ? 8 : 4]; };
 
-// Elements i .. i+8 of a row, those at or past n (of the chunk's eight) read as 0.  `vec`: the
-// row is 16-byte aligned.  WHOLE: that is known, and n is at least 8 or at most 0.  The row's
-// address is the same in all threads and i is not, so the sum needs no arithmetic a thread.
+// The row's address is the same in all threads, so adding a column needs no arithmetic a thread.
 template <int T>
 static __device__ __forceinline__ const void* row_of(const void* p, int64_t row, uint32_t ld)
 {
     return static_cast<const char*>(p) + row * (int64_t)((uint64_t)ld * (T == 2 ? 4 : 2));
 }
-template <int T, bool WHOLE = false>
-static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* p, uint32_t i, int n, bool vec)
+
+template <int T>
+static __device__ __forceinline__ uint32_t load_bits(const void* p, uint32_t i)
 {
-    if ((WHOLE || vec) && n >= 8) {
-        if (T == 2) {
-            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-            r.q[0] = __ldcs(s);
-            r.q[T == 2] = __ldcs(s + 1);
-        } else {
-            r.q[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    return T == 2 ? __ldg(static_cast<const uint32_t*>(p) + i) : (uint32_t)__ldg(static_cast<const uint16_t*>(p) + i);
+}
+
+// Columns i .. i+8 of a row, those at or past n (of the eight) read as 0.  Unless `vec`, a
+// lane has columns lane + 32 k of its warp's 256, for unstage().
+template <int T, bool WHOLE = false>
+static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* row, uint32_t i, int n, bool vec)
+{
+    if (WHOLE || vec) {
+        if (n >= 8) {
+            const uint4* s = T == 2 ? reinterpret_cast<const uint4*>(static_cast<const float*>(row) + i)
+                                    : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
+#pragma unroll
+            for (int k = 0; k < (T == 2 ? 2 : 1); k++) {
+                const uint4 q = __ldcs(s + k);
+                r.w[4 * k] = q.x; r.w[4 * k + 1] = q.y; r.w[4 * k + 2] = q.z; r.w[4 * k + 3] = q.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < (T == 2 ? 8 : 4); k++) {
+            if (T == 2) r.w[k] = !WHOLE && k < n ? load_bits<T>(row, i + k) : 0u;
+            else r.w[k] = (!WHOLE && 2 * k < n ? load_bits<T>(row, i + 2 * k) : 0u) |
+                          (!WHOLE && 2 * k + 1 < n ? load_bits<T>(row, i + 2 * k + 1) << 16 : 0u);
         }
         return;
     }
-    uint32_t w[8];
+    const int lane = threadIdx.x & 31, m = n + 7 * lane;      // lane's first of the warp's columns: i - 8 lane + lane
+    const uint32_t at = i - 7 * lane;
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        w[j] = WHOLE || j >= n ? 0u
-               : T == 2 ? __ldg(static_cast<const uint32_t*>(p) + i + j)
-                        : (uint32_t)__ldg(static_cast<const uint16_t*>(p) + i + j);
+    for (int k = 0; k < (T == 2 ? 8 : 4); k++) {
+        if (T == 2) r.w[k] = 32 * k < m ? load_bits<T>(row, at + 32 * k) : 0u;
+        else r.w[k] = (64 * k < m ? load_bits<T>(row, at + 64 * k) : 0u) |
+                      (64 * k + 32 < m ? load_bits<T>(row, at + 64 * k + 32) << 16 : 0u);
+    }
+}
+
+// What load_chunk() read without `vec`, as the lane's eight columns.
+template <int T>
+static __device__ __forceinline__ void unstage(Raw<T>& r, float* stage)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
     if (T == 2) {
-        r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        r.q[T == 2] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int k = 0; k < 8; k++) stage[lane + 32 * k] = __uint_as_float(r.w[T == 2 ? k : 0]);
     } else {
-        r.q[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        uint16_t* h = reinterpret_cast<uint16_t*>(stage);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            h[lane + 64 * k] = (uint16_t)r.w[k];
+            h[lane + 64 * k + 32] = (uint16_t)(r.w[k] >> 16);
+        }
+    }
+    __syncwarp();
+    const uint4* s = reinterpret_cast<const uint4*>(stage) + lane * (T == 2 ? 2 : 1);
+#pragma unroll
+    for (int k = 0; k < (T == 2 ? 2 : 1); k++) {
+        const uint4 q = s[k];
+        r.w[4 * k] = q.x; r.w[4 * k + 1] = q.y; r.w[4 * k + 2] = q.z; r.w[4 * k + 3] = q.w;
     }
 }
 
 template <int T>
 static __device__ __forceinline__ void widen_chunk(const Raw<T>& r, f32x2_t (&v)[4])
 {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
-    if (T == 2) {
-        const uint32_t x[4] = {r.q[T == 2].x, r.q[T == 2].y, r.q[T == 2].z, r.q[T == 2].w};
-        v[0] = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-        v[1] = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-        v[2] = pack2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-        v[3] = pack2(__uint_as_float(x[2]), __uint_as_float(x[3]));
-    } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            float a, b;
-            widen2<T & 1>(w[j], a, b);
-            v[j] = pack2(a, b);
+    for (int j = 0; j < 4; j++) {
+        float a, b;
+        if (T == 2) {
+            a = __uint_as_float(r.w[T == 2 ? 2 * j : 0]);
+            b = __uint_as_float(r.w[T == 2 ? 2 * j + 1 : 0]);
+        } else {
+            widen2<T & 1>(r.w[j], a, b);
         }
+        v[j] = pack2(a, b);
     }
+}
+template <int T, bool WHOLE>
+static __device__ __forceinline__ void widen_chunk(Raw<T>& r, f32x2_t (&v)[4], bool vec, float* stage)
+{
+    if (!WHOLE && !vec) unstage<T>(r, stage);
+    widen_chunk<T>(r, v);
 }
 
 template <int T, bool WHOLE = false>
-static __device__ __forceinline__ void store_chunk(const void* row, uint32_t i, int n, bool vec, const f32x2_t (&v)[4])
+static __device__ __forceinline__ void store_chunk(const void* row, uint32_t i, int n, bool vec, float* stage,
+                                                   const f32x2_t (&v)[4])
 {
     void* p = const_cast<void*>(row);
     float x[8];
 #pragma unroll
     for (int j = 0; j < 4; j++) unpack2(v[j], x[2 * j], x[2 * j + 1]);
-    if ((WHOLE || vec) && n >= 8) {
-        if (T == 2) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            __stcs(o, make_float4(x[0], x[1], x[2], x[3]));
-            __stcs(o + 1, make_float4(x[4], x[5], x[6], x[7]));
-        } else {
-            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i),
-                   make_uint4(narrow2<T & 1>(x[0], x[1]), narrow2<T & 1>(x[2], x[3]),
-                              narrow2<T & 1>(x[4], x[5]), narrow2<T & 1>(x[6], x[7])));
-        }
-        return;
+    uint4 q[T == 2 ? 2 : 1];
+    if (T == 2) {
+        q[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        q[T == 2] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+        q[0] = make_uint4(narrow2<T & 1>(x[0], x[1]), narrow2<T & 1>(x[2], x[3]), narrow2<T & 1>(x[4], x[5]),
+                          narrow2<T & 1>(x[6], x[7]));
     }
-    if (WHOLE) return;
+    if ((WHOLE || vec) && n >= 8) {
+        uint4* o = T == 2 ? reinterpret_cast<uint4*>(static_cast<float*>(p) + i)
+                          : reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i);
+        __stcs(o, q[0]);
+        if (T == 2) __stcs(o + 1, q[T == 2]);
+    } else if (!WHOLE && vec) {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (j < n) {
-            if (T == 2) static_cast<float*>(p)[i + j] = x[j];
-            else static_cast<uint16_t*>(p)[i + j] = narrow1<T & 1>(x[j]);
-        }
+        for (int j = 0; j < 8; j++)
+            if (j < n) {
+                if (T == 2) static_cast<float*>(p)[i + j] = x[j];
+                else static_cast<uint16_t*>(p)[i + j] = narrow1<T & 1>(x[j]);
+            }
+    } else if (!WHOLE) {
+        const int lane = threadIdx.x & 31, m = n + 7 * lane;
+        const uint32_t at = i - 7 * lane;
+        __syncwarp();
+        uint4* s = reinterpret_cast<uint4*>(stage) + lane * (T == 2 ? 2 : 1);
+        s[0] = q[0];
+        if (T == 2) s[T == 2] = q[T == 2];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (32 * k < m) {
+                if (T == 2) static_cast<float*>(p)[at + 32 * k] = stage[lane + 32 * k];
+                else static_cast<uint16_t*>(p)[at + 32 * k] = reinterpret_cast<const uint16_t*>(stage)[lane + 32 * k];
+            }
+    }
 }
 
 }  // namespace zero

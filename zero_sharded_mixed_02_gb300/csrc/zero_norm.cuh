@@ -72,13 +72,19 @@ __host__ __device__ inline int64_t norm_block_of(int64_t r, int64_t rows, int64_
 
 // Eight weights (cached: every row of a block reads the same ones).
 template <int DT, bool WHOLE>
-static __device__ __forceinline__ void load_weights(const void* p, uint32_t i, int n, bool vec, f32x2_t (&v)[4])
+static __device__ __forceinline__ void load_weights(const void* p, uint32_t i, int n, bool vec, float* stage,
+                                                    f32x2_t (&v)[4])
 {
     Raw<DT> r;
-    const uint16_t* w = static_cast<const uint16_t*>(p);
-    if ((WHOLE || vec) && n >= 8) r.q[0] = __ldg(reinterpret_cast<const uint4*>(w + i));
-    else load_chunk<DT, WHOLE>(r, p, i, n, false);
-    widen_chunk<DT>(r, v);
+    if (WHOLE) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (n >= 8) q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+        r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+        widen_chunk<DT>(r, v);
+    } else {
+        load_chunk<DT>(r, p, i, n, vec);
+        widen_chunk<DT, false>(r, v, vec, stage);
+    }
 }
 
 // Sums of N values over the block, the same bits in every thread: shuffles inside a
@@ -194,6 +200,8 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
     const int post = WHOLE ? POST : a.post, pre = WHOLE ? PRE : a.pre;
     const bool block = WHOLE || a.y;
     __shared__ norm_buf_t buf;
+    __shared__ __align__(16) float stages[WHOLE ? 1 : ZERO_NORM_THREADS / 32][256];
+    float* stage = stages[WHOLE ? 0 : threadIdx.x >> 5];
     int turn = 0, n[V];
     uint32_t col[V];
 #pragma unroll
@@ -219,8 +227,8 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         f32x2_t h[V][4], y[V][4], w[4];
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            widen_chunk<RT>(rh[c], h[c]);
-            if (block) widen_chunk<DT>(ry[c], y[c]);
+            widen_chunk<RT, WHOLE>(rh[c], h[c], a.vec_h, stage);
+            if (block) widen_chunk<DT, WHOLE>(ry[c], y[c], a.vec_y, stage);
         }
         if (row + 1 < end) fetch(row + 1);
         float mu2 = 0.0f, r2 = 1.0f, mu1 = 0.0f, r1 = 1.0f;
@@ -235,15 +243,15 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                     else act_store(y[c], p, col[c], a.wide, a.stride, a.lo, a.hi, col[c] < a.wide);
                 }
                 if (post && a.post_w) {
-                    load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, w);
+                    load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, stage, w);
                     times(y[c], w);
                 }
                 if (post && a.post_b) {
-                    load_weights<DT, WHOLE>(a.post_b, col[c], n[c], a.vec_w, w);
+                    load_weights<DT, WHOLE>(a.post_b, col[c], n[c], a.vec_w, stage, w);
                     plus(y[c], w);
                 }
                 if (a.gate) {
-                    load_weights<DT, WHOLE>(gate, col[c], n[c], a.vec_g, w);
+                    load_weights<DT, WHOLE>(gate, col[c], n[c], a.vec_g, stage, w);
                     times(y[c], w);
                 }
                 const f32x2_t alpha = both(a.alpha);
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         if (WHOLE || a.h_out) {
             const void* p = row_of<RT>(a.h_out, row, a.ldho);
 #pragma unroll
-            for (int c = 0; c < V; c++) store_chunk<RT, WHOLE>(p, col[c], n[c], a.vec_ho, h[c]);
+            for (int c = 0; c < V; c++) store_chunk<RT, WHOLE>(p, col[c], n[c], a.vec_ho, stage, h[c]);
         }
         if (pre) {
             normalise<V>(h, n, pre, a.eps, a.inv_cols, mu1, r1, buf, turn);
@@ -265,14 +273,14 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                     act_store_small(h[c], a.ckpt_x + (int64_t)row * a.stride, col[c], a.wide, a.stride, a.lo,
                                     col[c] < a.wide);
                 if (a.pre_w) {
-                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, w);
+                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, stage, w);
                     times(h[c], w);
                 }
                 if (a.pre_b) {
-                    load_weights<DT, WHOLE>(a.pre_b, col[c], n[c], a.vec_w, w);
+                    load_weights<DT, WHOLE>(a.pre_b, col[c], n[c], a.vec_w, stage, w);
                     plus(h[c], w);
                 }
-                store_chunk<DT, WHOLE>(px, col[c], n[c], a.vec_x, h[c]);
+                store_chunk<DT, WHOLE>(px, col[c], n[c], a.vec_x, stage, h[c]);
             }
         }
         if (a.stats && threadIdx.x == 0)
@@ -320,6 +328,8 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
     constexpr bool WHOLE = POST >= 0;
     const int post = WHOLE ? POST : a.post, pre = WHOLE ? PRE : a.pre;
     __shared__ norm_buf_t buf;
+    __shared__ __align__(16) float stages[WHOLE ? 1 : ZERO_NORM_THREADS / 32][256];
+    float* stage = stages[WHOLE ? 0 : threadIdx.x >> 5];
     constexpr int SUMS = TWO ? 2 : 1;
     // with more than one chunk a thread, what follows from the codes and weights is made again
     // after the reduction rather than held across it
@@ -376,9 +386,9 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
         f32x2_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) u[j] = both(1.0f);
-        if (a.gate) load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, u);
+        if (a.gate) load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, stage, u);
         if (post && a.post_w) {
-            load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, w);
+            load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, stage, w);
             times(u, w);
         }
         end_of_row(u, n[c]);
@@ -391,6 +401,9 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
     auto flush = [&]() {
 #pragma unroll
         for (int c = 0; c < V; c++) {
+            f32x2_t w[4];
+            if (a.post_part && a.gate)                       // all lanes: a warp reads together
+                load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, stage, w);
             if (col[c] >= a.wide) continue;
             if (a.slots) {
                 float* p = a.slots + ((int64_t)blockIdx.x + grp) * SUMS * a.wide + col[c];
@@ -400,8 +413,6 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             if (a.post_part) {
                 float* p = a.post_part + (int64_t)blockIdx.x * SUMS * a.wide + col[c];
                 if (a.gate) {
-                    f32x2_t w[4];
-                    load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, w);
                     times(sw[c], w);
                     if (TWO) times(sb[c], w);
                 }
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             const int q = AGAIN ? 0 : c;
             f32x2_t w[4];
             if (pre) {                                       // b = g
-                widen_chunk<DT>(rx[c], b[c]);
+                widen_chunk<DT, WHOLE>(rx[c], b[c], a.vec_dx, stage);
                 act_values(qx[c], ex[c], xh[q]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                     if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
                 }
                 if (a.pre_w) {
-                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, w);
+                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, stage, w);
                     times(b[c], w);
                 }
             } else {
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                 if (pre == ZERO_NORM_LAYER) t[3] = add2(t[3], b[c][j]);
                 w[j] = both(0.0f);
             }
-            if (a.dh_out) widen_chunk<RT>(rd[c], w);
+            if (a.dh_out) widen_chunk<RT, WHOLE>(rd[c], w, a.vec_dho, stage);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 b[c][j] = fma2(both(k1), b[c][j], w[j]);     // b = B
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                 if (pre == ZERO_NORM_LAYER) b[c][j] = sub2(b[c][j], both(p0));
                 b[c][j] = fma2(both(-p1), xh[q][j], b[c][j]);
             }
-            if (a.dh) store_chunk<RT, WHOLE>(pdh, col[c], n[c], a.vec_dh, b[c]);
+            if (a.dh) store_chunk<RT, WHOLE>(pdh, col[c], n[c], a.vec_dh, stage, b[c]);
             if (!WHOLE && !a.dy) continue;
             if (sums)
 #pragma unroll
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                 if (post) e = fma2(both(-q1), yh[q][j], e);
                 b[c][j] = mul2(both(scale), e);
             }
-            store_chunk<DT, WHOLE>(pdy, col[c], n[c], a.vec_dy, b[c]);
+            store_chunk<DT, WHOLE>(pdy, col[c], n[c], a.vec_dy, stage, b[c]);
         }
     }
     if (sums) flush();

@@ -176,8 +176,8 @@ static __device__ __forceinline__ void act_store_small(const f32x2_t (&v)[4], ui
 // are not, single elements 8 columns apart in neighbouring lanes would touch as many memory
 // sectors as lanes; instead the warp, whose 32 chunks are 256 consecutive columns, takes
 // 32 neighbouring columns an instruction and turns them into chunks (and back) through its
-// own 1 KB of shared memory (`stage`).  WHOLE: every row is aligned and every chunk lies
-// in the row (n >= 8) or past it (n <= 0).
+// own 1 KB of shared memory (`stage`).  WHOLE: every row is aligned (an fp32 one to 32 bytes)
+// and every chunk lies in the row (n >= 8) or past it (n <= 0).
 template <int T> struct Raw { uint32_t w[T == 2 ? 8 : 4]; };
 
 // The row's address is the same in all threads, so adding a column needs no arithmetic a thread.
@@ -199,6 +199,14 @@ template <int T, bool WHOLE = false>
 static __device__ __forceinline__ void load_chunk(Raw<T>& r, const void* row, uint32_t i, int n, bool vec)
 {
     if (WHOLE || vec) {
+        if (WHOLE && T == 2 && n >= 8) {
+            const float* s = static_cast<const float*>(row) + i;
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[T == 2 ? 4 : 0]),
+                           "=r"(r.w[T == 2 ? 5 : 0]), "=r"(r.w[T == 2 ? 6 : 0]), "=r"(r.w[T == 2 ? 7 : 0])
+                         : "l"(s));
+            return;
+        }
         if (n >= 8) {
             const uint4* s = T == 2 ? reinterpret_cast<const uint4*>(static_cast<const float*>(row) + i)
                                     : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
@@ -290,6 +298,13 @@ static __device__ __forceinline__ void store_chunk(const void* row, uint32_t i, 
     } else {
         q[0] = make_uint4(narrow2<T & 1>(x[0], x[1]), narrow2<T & 1>(x[2], x[3]), narrow2<T & 1>(x[4], x[5]),
                           narrow2<T & 1>(x[6], x[7]));
+    }
+    if (WHOLE && T == 2) {
+        if (n >= 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(p) + i),
+                         "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                         : "memory");
+        return;
     }
     if ((WHOLE || vec) && n >= 8) {
         uint4* o = T == 2 ? reinterpret_cast<uint4*>(static_cast<float*>(p) + i)

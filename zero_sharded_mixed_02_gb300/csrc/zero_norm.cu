@@ -140,6 +140,9 @@ int64_t elem(int dtype) { return dtype == ZERO_FP32 ? 4 : 2; }
 // Rows of a matrix are read in 16-byte vectors if they are aligned to them.
 int vec_rows(const void* p, int64_t ld, int dtype) { return p && aligned_to(p, 16) && ld * elem(dtype) % 16 == 0; }
 
+// ... and in whole chunks if the columns are too and an fp32 one is aligned to 32 bytes.
+bool whole_rows(const void* p, int64_t ld, int dtype) { return aligned_to(p, dtype == ZERO_FP32 ? 32 : 16) && ld % 8 == 0; }
+
 bool matrix_ok(const void* p, int64_t ld, int64_t cols, int dtype)
 {
     return p && aligned_to(p, elem(dtype)) && ld >= cols && ld <= (1ll << 31);
@@ -183,24 +186,31 @@ void row_shape(int wide, int& v, int& threads)
     threads = ((chunks + v - 1) / v + 31) / 32 * 32;
 }
 
-// Resident blocks of a kernel on the current device, looked up once for each kernel and
-// block size; 0: a CUDA call failed.
-int64_t resident(const void* fn, int threads)
+// Resident blocks of a kernel on the current device (0: a CUDA call failed) and its SMs,
+// looked up once for each kernel and shape of its blocks.
+int64_t resident(const void* fn, int threads, int smem, int& sms)
 {
-    struct Known { const void* fn; int dev, threads; int64_t blocks; };
+    struct Known { const void* fn; int dev, threads, smem, sms; int64_t blocks; };
     static std::mutex lock;
     static Known known[256];
     static int count = 0;
-    int dev = 0, sms = 0, occ = 0;
+    int dev = 0, occ = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> hold(lock);
     for (int i = 0; i < count; i++)
-        if (known[i].fn == fn && known[i].dev == dev && known[i].threads == threads) return known[i].blocks;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, 0) != cudaSuccess)
+        if (known[i].fn == fn && known[i].dev == dev && known[i].threads == threads && known[i].smem == smem) {
+            sms = known[i].sms;
+            return known[i].blocks;
+        }
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, fn) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)at.sharedSizeBytes) !=
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem) != cudaSuccess)
         return 0;
     const int64_t blocks = (int64_t)sms * (occ > 0 ? occ : 1);
-    if (count < 256) known[count++] = {fn, dev, threads, blocks};
+    if (count < 256) known[count++] = {fn, dev, threads, smem, sms, blocks};
     return blocks;
 }
 
@@ -249,14 +259,16 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.vec_g = vec_rows(d.gate, d.cols, d.dtype);
     int v = 1, threads = 32;
     row_shape((int)a.wide, v, threads);
-    const bool whole = d.cols % 8 == 0 && y && a.vec_h && a.vec_y && a.vec_ho && (!x || a.vec_x) && a.vec_w &&
-                       (!d.gate || a.vec_g);
+    const bool whole = d.cols % 8 == 0 && y && whole_rows(h, ldh, d.res_dtype) && a.vec_y &&
+                       whole_rows(h_out, ldho, d.res_dtype) && (!x || a.vec_x) && a.vec_w && (!d.gate || a.vec_g);
     const void* fn = d.dtype == ZERO_FP16 ? norm_forward_fp16(d.res_dtype, v, d.post, d.pre, whole)
                                           : norm_forward_bf16(d.res_dtype, v, d.post, d.pre, whole);
-    const int64_t most = resident(fn, threads);
+    const int smem = 16 * (d.post_b || d.pre_b ? ZERO_NORM_WORDS_BIAS : ZERO_NORM_WORDS) * v * threads;
+    int sms = 0;
+    const int64_t most = resident(fn, threads, smem, sms);
     if (most == 0) return ZERO_ECUDA;
     void* args[] = {&a};
-    return cudaLaunchKernel(fn, dim3((unsigned)(d.rows < most ? d.rows : most)), dim3(threads), args, 0,
+    return cudaLaunchKernel(fn, dim3((unsigned)(d.rows < most ? d.rows : most)), dim3(threads), args, smem,
                             static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? ZERO_OK
                : ZERO_ECUDA;
@@ -323,15 +335,22 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.vec_g = vec_rows(d.gate, d.cols, d.dtype);
         int v = 1, threads = 32;
         row_shape((int)a.wide, v, threads);
-        const bool whole = d.cols % 8 == 0 && dy && (!dh_out || a.vec_dho) && (!dx || a.vec_dx) &&
-                           (!dh || a.vec_dh) && a.vec_dy && a.vec_w && (!d.gate || a.vec_g);
+        const bool whole = d.cols % 8 == 0 && dy && (!dh_out || whole_rows(dh_out, lddho, d.res_dtype)) &&
+                           (!dx || a.vec_dx) && (!dh || whole_rows(dh, lddh, d.res_dtype)) && a.vec_dy && a.vec_w &&
+                           (!d.gate || a.vec_g);
+        int smem = 0;
         const void* fn = d.dtype == ZERO_FP16
-                             ? norm_backward_fp16(d.res_dtype, v, d.post, d.pre, whole, two)
-                             : norm_backward_bf16(d.res_dtype, v, d.post, d.pre, whole, two);
-        blocks = resident(fn, threads);
+                             ? norm_backward_fp16(d.res_dtype, v, d.post, d.pre, whole, two, smem)
+                             : norm_backward_bf16(d.res_dtype, v, d.post, d.pre, whole, two, smem);
+        smem *= threads;
+        int sms = 0;
+        blocks = resident(fn, threads, smem, sms);
         if (blocks == 0) return ZERO_ECUDA;
         if (blocks > ZERO_NORM_BLOCKS) blocks = ZERO_NORM_BLOCKS;
-        if (blocks > d.rows) blocks = d.rows;
+        // At least four rows a block where that leaves a block an SM: a block's partial sums cost
+        // as much as two or three rows (512 x 1600: 20.7 us with a block a row, 13 us so).
+        const int64_t rows4 = (d.rows + 3) / 4, one = d.rows < sms ? d.rows : sms;
+        if (blocks > (rows4 > one ? rows4 : one)) blocks = rows4 > one ? rows4 : one;
         const int64_t part = blocks * (two ? 2 : 1) * a.wide;
         float* at = static_cast<float*>(work);
         if (dpre_w || dpre_b) pre_part = at;
@@ -341,7 +360,7 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.post_part = post_part;
         a.slots = slots;
         void* args[] = {&a};
-        if (cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), args, 0,
+        if (cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), args, smem,
                              static_cast<cudaStream_t>(stream)) != cudaSuccess)
             return ZERO_ECUDA;
     }

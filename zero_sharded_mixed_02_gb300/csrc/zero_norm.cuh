@@ -60,8 +60,8 @@ struct NormBwdArgs {
 // and whether every row and weight is read in whole aligned chunks (and y or dy is there).
 const void* norm_forward_fp16(int res, int v, int post, int pre, bool whole);
 const void* norm_forward_bf16(int res, int v, int post, int pre, bool whole);
-const void* norm_backward_fp16(int res, int v, int post, int pre, bool whole, bool& two);
-const void* norm_backward_bf16(int res, int v, int post, int pre, bool whole, bool& two);
+const void* norm_backward_fp16(int res, int v, int post, int pre, bool whole, bool& two, int& smem);
+const void* norm_backward_bf16(int res, int v, int post, int pre, bool whole, bool& two, int& smem);
 
 // Rows [row0(b), row0(b + 1)) belong to block b; the block of row r is the largest b with row0(b) <= r.
 __host__ __device__ inline int64_t norm_row0(int64_t b, int64_t rows, int64_t blocks) { return b * rows / blocks; }
@@ -150,6 +150,89 @@ static __device__ __forceinline__ void plus(f32x2_t (&v)[4], const f32x2_t (&w)[
     for (int j = 0; j < 4; j++) v[j] = add2(v[j], w[j]);
 }
 
+// ---- weights in shared memory ------------------------------------------------------
+static __device__ __forceinline__ uint4 shared16(uint32_t at)
+{
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at));
+    return q;
+}
+static __device__ __forceinline__ void put16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+static __device__ __forceinline__ void put_chunk(uint32_t at, uint32_t step, const f32x2_t (&v)[4])
+{
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) unpack2(v[j], x[2 * j], x[2 * j + 1]);
+    put16(at, __float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    put16(at + step, __float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+}
+static __device__ __forceinline__ void get_chunk(uint32_t at, uint32_t step, f32x2_t (&v)[4])
+{
+    const uint4 x = shared16(at), y = shared16(at + step);
+    v[0] = pack2(__uint_as_float(x.x), __uint_as_float(x.y));
+    v[1] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
+    v[2] = pack2(__uint_as_float(y.x), __uint_as_float(y.y));
+    v[3] = pack2(__uint_as_float(y.z), __uint_as_float(y.w));
+}
+// Eight 16-bit values.
+template <int DT>
+static __device__ __forceinline__ void get16(uint32_t at, f32x2_t (&v)[4])
+{
+    const uint4 q = shared16(at);
+    Raw<DT> r;
+    r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+    widen_chunk<DT>(r, v);
+}
+template <int DT>
+static __device__ __forceinline__ void put_16(uint32_t at, const f32x2_t (&v)[4])
+{
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) unpack2(v[j], x[2 * j], x[2 * j + 1]);
+    put16(at, narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]), narrow2<DT>(x[4], x[5]), narrow2<DT>(x[6], x[7]));
+}
+
+// The weights of a thread's chunk, as the passes use them, lie in shared memory as 16-byte
+// words [word][thread]: 0, 1: u = gate post_w in fp32; 2: pre_w in 16 bits; and with biases
+// 3, 4: gate post_b in fp32; 5: pre_b.  They are read from there each row: fewer
+// instructions than loading and widening them, and L1 need not hold them.  u (and
+// words 3, 4) are made again where the gate's group changes.  A thread reads what it wrote.
+#define ZERO_NORM_WORDS 3
+#define ZERO_NORM_WORDS_BIAS 6
+template <int DT, bool WHOLE>
+static __device__ __forceinline__ void put_gate(uint32_t at, uint32_t step, const void* gate, const void* post_w,
+                                                const void* post_b, uint32_t i, int n, int vec_g, int vec_w,
+                                                float* stage)
+{
+    f32x2_t g[4], u[4], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) g[j] = both(1.0f);
+    if (gate) load_weights<DT, WHOLE>(gate, i, n, vec_g, stage, g);
+#pragma unroll
+    for (int j = 0; j < 4; j++) u[j] = g[j];
+    if (post_w) {
+        load_weights<DT, WHOLE>(post_w, i, n, vec_w, stage, w);
+        times(u, w);
+    }
+    end_of_row(u, n);
+    put_chunk(at, step, u);
+    if (post_b) {
+        load_weights<DT, WHOLE>(post_b, i, n, vec_w, stage, w);
+        times(w, g);
+        put_chunk(at + 3 * step, step, w);
+    }
+}
+template <int DT, bool WHOLE>
+static __device__ __forceinline__ void put_pre(uint32_t at, const void* p, uint32_t i, int n, int vec_w, float* stage)
+{
+    f32x2_t w[4];
+    load_weights<DT, WHOLE>(p, i, n, vec_w, stage, w);
+    put_16<DT>(at, w);
+}
+
 // ---- forward ---------------------------------------------------------------------
 // A row held as v (zeros past its end) is normalised; its mean and 1/deviation returned.
 template <int V>
@@ -222,6 +305,22 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
             if (block) load_chunk<DT, WHOLE>(ry[c], py, col[c], n[c], a.vec_y);
         }
     };
+    extern __shared__ __align__(16) unsigned char raw[];
+    const uint32_t step = 16 * blockDim.x, words = (a.post_b || a.pre_b ? ZERO_NORM_WORDS_BIAS : ZERO_NORM_WORDS) * step;
+    const uint32_t weights = (uint32_t)__cvta_generic_to_shared(raw) + 16 * threadIdx.x;
+    auto refresh = [&]() {
+        if (!a.gate && !a.post_w && !a.post_b) return;
+        const void* gate = a.gate ? row_of<DT>(a.gate, grp, a.cols) : nullptr;
+#pragma unroll
+        for (int c = 0; c < V; c++)
+            put_gate<DT, WHOLE>(weights + c * words, step, gate, a.post_w, a.post_b, col[c], n[c], a.vec_g, a.vec_w, stage);
+    };
+#pragma unroll
+    for (int c = 0; c < V; c++) {
+        if (a.pre_w) put_pre<DT, WHOLE>(weights + c * words + 2 * step, a.pre_w, col[c], n[c], a.vec_w, stage);
+        if (a.pre_b) put_pre<DT, WHOLE>(weights + c * words + 5 * step, a.pre_b, col[c], n[c], a.vec_w, stage);
+    }
+    refresh();
     fetch(row);
     for (; row < end; row++) {
         f32x2_t h[V][4], y[V][4], w[4];
@@ -234,7 +333,6 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         float mu2 = 0.0f, r2 = 1.0f, mu1 = 0.0f, r1 = 1.0f;
         if (block) {
             if (post) normalise<V>(y, n, post, a.eps, a.inv_cols, mu2, r2, buf, turn);
-            const void* gate = row_of<DT>(a.gate, grp, a.cols);
 #pragma unroll
             for (int c = 0; c < V; c++) {
                 if (a.ckpt_y) {
@@ -242,17 +340,13 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                     if (post) act_store_small(y[c], p, col[c], a.wide, a.stride, a.lo, col[c] < a.wide);
                     else act_store(y[c], p, col[c], a.wide, a.stride, a.lo, a.hi, col[c] < a.wide);
                 }
-                if (post && a.post_w) {
-                    load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, stage, w);
+                if (a.gate || a.post_w) {
+                    get_chunk(weights + c * words, step, w);
                     times(y[c], w);
                 }
-                if (post && a.post_b) {
-                    load_weights<DT, WHOLE>(a.post_b, col[c], n[c], a.vec_w, stage, w);
+                if (a.post_b) {
+                    get_chunk(weights + c * words + 3 * step, step, w);
                     plus(y[c], w);
-                }
-                if (a.gate) {
-                    load_weights<DT, WHOLE>(gate, col[c], n[c], a.vec_g, stage, w);
-                    times(y[c], w);
                 }
                 const f32x2_t alpha = both(a.alpha);
 #pragma unroll
@@ -273,11 +367,11 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
                     act_store_small(h[c], a.ckpt_x + (int64_t)row * a.stride, col[c], a.wide, a.stride, a.lo,
                                     col[c] < a.wide);
                 if (a.pre_w) {
-                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, stage, w);
+                    get16<DT>(weights + c * words + 2 * step, w);
                     times(h[c], w);
                 }
                 if (a.pre_b) {
-                    load_weights<DT, WHOLE>(a.pre_b, col[c], n[c], a.vec_w, stage, w);
+                    get16<DT>(weights + c * words + 5 * step, w);
                     plus(h[c], w);
                 }
                 store_chunk<DT, WHOLE>(px, col[c], n[c], a.vec_x, stage, h[c]);
@@ -285,9 +379,10 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         }
         if (a.stats && threadIdx.x == 0)
             reinterpret_cast<float4*>(a.stats)[row] = make_float4(mu2, r2, mu1, r1);
-        if (++in_group == a.group) {
+        if (++in_group == a.group && row + 1 < end) {
             in_group = 0;
             grp++;
+            if (a.gate) refresh();
         }
     }
 }
@@ -319,14 +414,13 @@ static __device__ __forceinline__ void get_sums(const float* p, f32x2_t (&v)[4])
 //   sum u yh D = sum u yh B - r1 (mean(g) sum u yh + mean(g xh) sum u yh xh)
 // and the same without yh.  A second reduction, after D, would cost its latency once more.
 //
-// POST and PRE as in the forward pass (known kinds: whole aligned rows with dy wanted).
-template <int DT, int RT, int V, int POST, int PRE, bool TWO>
+template <int DT, int RT, int V, bool TWO>
 __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __grid_constant__ NormBwdArgs a)
 {
     // one wave of blocks: the kernel that adds their sums may be placed already
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr bool WHOLE = POST >= 0;
-    const int post = WHOLE ? POST : a.post, pre = WHOLE ? PRE : a.pre;
+    constexpr bool WHOLE = false;
+    const int post = a.post, pre = a.pre;
     __shared__ norm_buf_t buf;
     __shared__ __align__(16) float stages[WHOLE ? 1 : ZERO_NORM_THREADS / 32][256];
     float* stage = stages[WHOLE ? 0 : threadIdx.x >> 5];
@@ -382,17 +476,22 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             r1 = st.w;
         }
     };
-    auto scales = [&](int c, f32x2_t (&u)[4]) {              // gate post_w
-        f32x2_t w[4];
+    extern __shared__ __align__(16) unsigned char raw[];
+    const uint32_t step = 16 * blockDim.x, words = ZERO_NORM_WORDS * step;
+    const uint32_t weights = (uint32_t)__cvta_generic_to_shared(raw) + 16 * threadIdx.x;
+    auto refresh = [&]() {
+        const void* gate = a.gate ? row_of<DT>(a.gate, grp, a.cols) : nullptr;
 #pragma unroll
-        for (int j = 0; j < 4; j++) u[j] = both(1.0f);
-        if (a.gate) load_weights<DT, WHOLE>(row_of<DT>(a.gate, grp, a.cols), col[c], n[c], a.vec_g, stage, u);
-        if (post && a.post_w) {
-            load_weights<DT, WHOLE>(a.post_w, col[c], n[c], a.vec_w, stage, w);
-            times(u, w);
-        }
-        end_of_row(u, n[c]);
+        for (int c = 0; c < V; c++)
+            put_gate<DT, WHOLE>(weights + c * words, step, gate, post ? a.post_w : nullptr, nullptr, col[c], n[c], a.vec_g,
+                                a.vec_w, stage);
     };
+    auto scales = [&](int c, f32x2_t (&u)[4]) { get_chunk(weights + c * words, step, u); };
+    if (a.pre_w)
+#pragma unroll
+        for (int c = 0; c < V; c++)
+            put_pre<DT, WHOLE>(weights + c * words + 2 * step, a.pre_w, col[c], n[c], a.vec_w, stage);
+    refresh();
     // The sums of the block's rows of group grp go to the slot block + group: along the
     // rows both only grow, so no two pairs share one.  Times the group's gate they are
     // added to the block's sums for the post-norm's weights, which stay in the workspace
@@ -438,6 +537,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
             if (sums) flush();
             grp++;
             left = a.group;
+            if (a.gate) refresh();
         }
         left--;
         f32x2_t b[V][4], u[KEEP][4], xh[KEEP][4], yh[KEEP][4], t[8];
@@ -459,7 +559,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
                     if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
                 }
                 if (a.pre_w) {
-                    load_weights<DT, WHOLE>(a.pre_w, col[c], n[c], a.vec_w, stage, w);
+                    get16<DT>(weights + c * words + 2 * step, w);
                     times(b[c], w);
                 }
             } else {
@@ -499,27 +599,14 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
         float s[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) s[k] = either(t[k]);
-        if (!WHOLE || (layer && POST > 0)) {
-            if (layer) {
-                block_sum<8>(s, buf, turn);
-            } else {
-                float three[3] = {s[0], s[1], s[2]};
-                block_sum<3>(three, buf, turn);
-                s[0] = three[0];
-                s[1] = three[1];
-                s[2] = three[2];
-            }
-        } else if (POST > 0) {
+        if (layer) {
+            block_sum<8>(s, buf, turn);
+        } else {
             float three[3] = {s[0], s[1], s[2]};
             block_sum<3>(three, buf, turn);
             s[0] = three[0];
             s[1] = three[1];
             s[2] = three[2];
-        } else {                                             // the pre-norm alone
-            float two[2] = {s[0], s[3]};
-            block_sum<2>(two, buf, turn);
-            s[0] = two[0];
-            s[3] = two[1];
         }
         // D = b - p1 xh - p0;  dy = alpha r2 (u D - q1 yh - q0)
         const float p1 = k1 * s[0] * a.inv_cols, p0 = pre == ZERO_NORM_LAYER ? k1 * s[3] * a.inv_cols : 0.0f;
@@ -574,6 +661,331 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, 1) k_norm_backward(const __
     }
 }
 
+// ---- backward, whole aligned rows --------------------------------------------------
+// The next rows' chunks are copied to shared memory asynchronously instead of being held in
+// registers, and what the reduction separates, codes and weights, is read from there again.
+// That leaves 64 registers enough without bias sums: two blocks of 16 warps an SM instead of
+// one.
+//
+// A thread's part of a row is three 16-byte words [word][thread] (dx, both checkpoints' codes,
+// and the stream's gradient if that is of 16 bits); it reads what it copied itself, so there
+// is no barrier for the copies.  An fp32 stream's 1 KB a warp is copied 16 neighbouring bytes
+// a lane and read 32 bytes a lane (copies 32 bytes apart would fetch every sector twice);
+// word p lies at p ^ (p >> 3 & 1), so that eight lanes' reads fall on different banks.
+static __device__ __forceinline__ void copy16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+static __device__ __forceinline__ void copy8(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+// Sums of four values over the block, the same bits in every thread.  A warp halves the
+// values a lane holds with each of the first two exchanges, so a group of eight lanes ends
+// with one value's sum: half the shuffles of four sums side by side.
+typedef float norm_buf4_t[2][4][16];
+static __device__ __forceinline__ void block_sum4(float (&v)[4], norm_buf4_t& buf, int& turn)
+{
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool hi = lane & 16, odd = lane & 8;
+    float a = hi ? v[2] : v[0], b = hi ? v[3] : v[1];
+    a += __shfl_xor_sync(0xFFFFFFFFu, hi ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xFFFFFFFFu, hi ? v[1] : v[3], 16);
+    float c = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);   // value lane / 8
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+    if (warps > 1) {
+        const int w = lane & 7;
+        if (w == 0) buf[turn][lane >> 3][threadIdx.x >> 5] = c;
+        __syncthreads();
+        c = w < warps ? buf[turn][lane >> 3][w] : 0.0f;
+        if (w + 8 < warps) c += buf[turn][lane >> 3][w + 8];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+        turn ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = __shfl_sync(0xFFFFFFFFu, c, 8 * i);
+}
+
+#ifndef ZERO_NORM_AHEAD
+#define ZERO_NORM_AHEAD 2                                    // rows in shared memory
+#endif
+#define ZERO_NORM_PART 48                                    // bytes of a thread's part of a chunk
+// Shared memory of a thread: its parts of the rows (an fp32 stream 32 bytes more) and weights.
+template <int RT, int V> struct NormRing {
+    static constexpr int bytes = V * ((ZERO_NORM_PART + (RT == 2 ? 32 : 0)) * ZERO_NORM_AHEAD + ZERO_NORM_PART);
+};
+
+template <int DT, int RT, int V, int POST, int PRE, bool TWO>
+__global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO ? 2 : 1)
+    k_norm_backward_whole(const __grid_constant__ NormBwdArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr int SUMS = TWO ? 2 : 1, PART = ZERO_NORM_PART, AHEAD = ZERO_NORM_AHEAD;
+    constexpr bool LAYER = PRE == ZERO_NORM_LAYER || POST == ZERO_NORM_LAYER, WIDE = RT == 2;
+    extern __shared__ __align__(128) unsigned char raw[];
+    __shared__ norm_buf4_t buf, buf2;
+    const uint32_t threads = blockDim.x, t = threadIdx.x, lane = t & 31;
+    // [weights][AHEAD rows: parts, then an fp32 stream], each chunk c of the V after the other
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(raw);
+    const uint32_t row_bytes = V * threads * (PART + (WIDE ? 32 : 0)), first = base + V * threads * PART;
+    const uint32_t weights = base + 16 * t, part = first + 16 * t, T16 = 16 * threads;
+    const uint32_t wide = first + V * threads * PART + (t & ~31u) * 32;                  // the warp's words
+    const uint32_t mine = wide + ((2 * lane) ^ (lane >> 2 & 1)) * 16;                    // words 2 lane, 2 lane + 1
+    int turn = 0, turn2 = 0;
+    f32x2_t pw[V][4], sw[V][4], pb[TWO ? V : 1][4], sb[TWO ? V : 1][4];
+#pragma unroll
+    for (int c = 0; c < V; c++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            pw[c][j] = sw[c][j] = both(0.0f);
+            if (TWO) pb[c][j] = sb[c][j] = both(0.0f);
+        }
+    const uint32_t end = (uint32_t)norm_row0(blockIdx.x + 1, a.rows, gridDim.x);
+    uint32_t row = (uint32_t)norm_row0(blockIdx.x, a.rows, gridDim.x);
+    uint32_t grp = row / a.group, left = (grp + 1) * a.group - row;         // rows of the group to come
+    auto chunk = [&](int c) { return t + c * threads; };
+    auto in = [&](int c) { return 8 * chunk(c) < (uint32_t)a.cols; };
+    // rows' addresses, the same in all threads and advanced row by row
+    const char *ld = static_cast<const char*>(row_of<RT>(a.dh_out, row, a.lddho));
+    const char *lx = static_cast<const char*>(row_of<DT>(a.dx, row, a.lddx));
+    const uint8_t *qx = a.ckpt_x + (int64_t)row * a.stride, *qy = a.ckpt_y + (int64_t)row * a.stride;
+    const int64_t ld_step = (int64_t)a.lddho * (WIDE ? 4 : 2), lx_step = (int64_t)a.lddx * 2;
+    uint32_t copied = row, slot = 0;                         // the next row to copy and its place
+    auto copy = [&]() {
+        if (copied < end) {
+#pragma unroll
+            for (int c = 0; c < V; c++) {
+                const uint32_t at = part + slot + c * threads * PART, k = chunk(c);
+                if (in(c)) {
+                    copy16(at, lx + 16 * k);
+                    copy8(at + T16, qx + 8 * k);
+                    if (a.ckpt_y) copy8(at + T16 + 8, qy + 8 * k);
+                    if (!WIDE && a.dh_out) copy16(at + 2 * T16, ld + 16 * k);
+                }
+                if (WIDE && a.dh_out) {
+                    // words lane and lane + 32 of the warp's 64: columns 4 p
+                    const uint32_t w = (t & ~31u) + c * threads, to = wide + slot + c * threads * 32;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t p = lane + 32 * h;
+                        if (8 * w + 4 * p < (uint32_t)a.cols) copy16(to + (p ^ (p >> 3 & 1)) * 16, ld + 32 * w + 16 * p);
+                    }
+                }
+            }
+            ld += ld_step;
+            lx += lx_step;
+            qx += a.stride;
+            qy += a.stride;
+        }
+        copied++;
+        slot = slot + row_bytes == AHEAD * row_bytes ? 0 : slot + row_bytes;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // exponents and statistics come by registers, a row ahead
+    const uint8_t *lex = qx + a.wide, *ley = qy + a.wide;
+    const float4* stats = reinterpret_cast<const float4*>(a.stats) + row;
+    uint32_t ex[V], ey[V];
+    float r1, r2;
+    auto fetch = [&]() {
+#pragma unroll
+        for (int c = 0; c < V; c++) {
+            ex[c] = ey[c] = 0;
+            if (in(c)) {
+                ex[c] = __ldg(lex + (chunk(c) >> 2));
+                if (a.ckpt_y) ey[c] = __ldg(ley + (chunk(c) >> 2));
+            }
+        }
+        const float4 st = __ldg(stats);
+        r2 = st.y;
+        r1 = st.w;
+        lex += a.stride;
+        ley += a.stride;
+        stats++;
+    };
+    // zeros where no copy comes: chunks past the row's end, tensors that are not there
+    for (uint32_t i = t; i < AHEAD * row_bytes / 16; i += threads) put16(first + 16 * i, 0, 0, 0, 0);
+    __syncthreads();
+    auto refresh = [&]() {
+        const void* gate = a.gate ? row_of<DT>(a.gate, grp, a.cols) : nullptr;
+#pragma unroll
+        for (int c = 0; c < V; c++)
+            put_gate<DT, true>(weights + c * threads * PART, T16, gate, POST ? a.post_w : nullptr, nullptr, 8 * chunk(c),
+                               in(c) ? 8 : 0, 1, 1, nullptr);
+    };
+    auto scales = [&](int c, f32x2_t (&u)[4]) { get_chunk(weights + c * threads * PART, T16, u); };
+    auto widen16 = [&](uint32_t at, f32x2_t (&v)[4]) { get16<DT>(at, v); };
+    if (a.pre_w)
+#pragma unroll
+        for (int c = 0; c < V; c++)
+            put_pre<DT, true>(weights + c * threads * PART + 2 * T16, a.pre_w, 8 * chunk(c), in(c) ? 8 : 0, 1, nullptr);
+    refresh();
+    // as in the general kernel: the group's sums to their slot, times the gate to the block's
+    const bool sums = a.slots || a.post_part;
+    bool again = false;
+    auto flush = [&]() {
+#pragma unroll
+        for (int c = 0; c < V; c++) {
+            const uint32_t k = 8 * chunk(c);
+            if (k < a.wide) {
+                if (a.slots) {
+                    float* p = a.slots + ((int64_t)blockIdx.x + grp) * SUMS * a.wide + k;
+                    put_sums(p, sw[c]);
+                    if (TWO) put_sums(p + a.wide, sb[c]);
+                }
+                if (a.post_part) {
+                    float* p = a.post_part + (int64_t)blockIdx.x * SUMS * a.wide + k;
+                    if (a.gate) {
+                        f32x2_t w[4];
+                        load_weights<DT, true>(row_of<DT>(a.gate, grp, a.cols), k, in(c) ? 8 : 0, 1, nullptr, w);
+                        times(sw[c], w);
+                        if (TWO) times(sb[c], w);
+                    }
+                    if (again) {
+                        get_sums(p, sw[c]);
+                        if (TWO) get_sums(p + a.wide, sb[c]);
+                    }
+                    put_sums(p, sw[c]);
+                    if (TWO) put_sums(p + a.wide, sb[c]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                sw[c][j] = both(0.0f);
+                if (TWO) sb[c][j] = both(0.0f);
+            }
+        }
+        again = true;
+    };
+    char* sd = static_cast<char*>(const_cast<void*>(row_of<RT>(a.dh, row, a.lddh)));
+    char* sy = static_cast<char*>(const_cast<void*>(row_of<DT>(a.dy, row, a.lddy)));
+    const int64_t sd_step = (int64_t)a.lddh * (WIDE ? 4 : 2), sy_step = (int64_t)a.lddy * 2;
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++) copy();
+    fetch();
+    uint32_t at = 0;                                         // the row's place
+    for (; row < end; row++) {
+        if (left == 0) {
+            if (sums) flush();
+            grp++;
+            left = a.group;
+            if (a.gate) refresh();
+        }
+        left--;
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        if (WIDE) __syncwarp();                              // the warp's words are all there
+        f32x2_t b[V][4], u[4], xh[4], yh[4], w[4], s2[8];
+        const float k1 = r1, k2 = r2;
+        uint32_t fx[V], fy[V];
+#pragma unroll
+        for (int k = 0; k < 8; k++) s2[k] = both(0.0f);
+#pragma unroll
+        for (int c = 0; c < V; c++) {
+            const uint32_t p = part + at + c * threads * PART;
+            widen16(p, b[c]);                                // dx, then g, then B
+            const uint4 q = shared16(p + T16);
+            act_values(make_uint2(q.x, q.y), ex[c], xh);
+            fx[c] = ex[c];
+            fy[c] = ey[c];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                pw[c][j] = fma2(b[c][j], xh[j], pw[c][j]);
+                if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
+            }
+            if (a.pre_w) {
+                widen16(weights + c * threads * PART + 2 * T16, w);
+                times(b[c], w);
+            }
+            if (WIDE) {
+                const uint32_t m = mine + at + c * threads * 32;
+                get_chunk(m, (m ^ 16) - m, w);
+            } else {
+                widen16(p + 2 * T16, w);
+            }
+            if (POST) {
+                act_values(make_uint2(q.z, q.w), ey[c], yh);
+                scales(c, u);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                s2[0] = fma2(b[c][j], xh[j], s2[0]);
+                if (PRE == ZERO_NORM_LAYER) s2[3] = add2(s2[3], b[c][j]);
+                b[c][j] = fma2(both(k1), b[c][j], w[j]);
+                if (POST) {
+                    const f32x2_t uy = mul2(u[j], yh[j]);
+                    s2[1] = fma2(uy, b[c][j], s2[1]);
+                    s2[2] = fma2(uy, xh[j], s2[2]);
+                    if (LAYER) s2[4] = add2(s2[4], uy);
+                }
+                if (POST == ZERO_NORM_LAYER) {
+                    s2[5] = fma2(u[j], b[c][j], s2[5]);
+                    s2[6] = add2(s2[6], u[j]);
+                    s2[7] = fma2(u[j], xh[j], s2[7]);
+                }
+            }
+        }
+        if (row + 1 < end) fetch();
+        float s[4] = {either(s2[0]), either(s2[1]), either(s2[2]), either(s2[3])};
+        float l[4] = {either(s2[4]), either(s2[5]), either(s2[6]), either(s2[7])};
+        block_sum4(s, buf, turn);
+        if (LAYER && POST) block_sum4(l, buf2, turn2);
+        // D = b - p1 xh - p0;  dy = alpha r2 (u D - q1 yh - q0)
+        const float p1 = k1 * s[0] * a.inv_cols, p0 = PRE == ZERO_NORM_LAYER ? k1 * s[3] * a.inv_cols : 0.0f;
+        float scale = a.alpha, q1 = 0.0f, q0 = 0.0f;
+        if (POST) {
+            scale *= k2;
+            q1 = (s[1] - p0 * l[0] - p1 * s[2]) * a.inv_cols;
+            if (POST == ZERO_NORM_LAYER) q0 = (l[1] - p0 * l[2] - p1 * l[3]) * a.inv_cols;
+        }
+#pragma unroll
+        for (int c = 0; c < V; c++) {
+            const uint32_t k = chunk(c);
+            const uint4 q = shared16(part + at + c * threads * PART + T16);
+            act_values(make_uint2(q.x, q.y), fx[c], xh);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (PRE == ZERO_NORM_LAYER) b[c][j] = sub2(b[c][j], both(p0));
+                b[c][j] = fma2(both(-p1), xh[j], b[c][j]);
+            }
+            if (a.dh) store_chunk<RT, true>(sd, 8 * k, in(c) ? 8 : 0, true, nullptr, b[c]);
+            act_values(make_uint2(q.z, q.w), fy[c], yh);
+            if (sums)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    sw[c][j] = fma2(b[c][j], yh[j], sw[c][j]);
+                    if (TWO) sb[c][j] = add2(sb[c][j], b[c][j]);
+                }
+            scales(c, u);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f32x2_t e = POST == ZERO_NORM_LAYER ? fma2(u[j], b[c][j], both(-q0)) : mul2(u[j], b[c][j]);
+                if (POST) e = fma2(both(-q1), yh[j], e);
+                b[c][j] = mul2(both(scale), e);
+            }
+            store_chunk<DT, true>(sy, 8 * k, in(c) ? 8 : 0, true, nullptr, b[c]);
+        }
+        sd += sd_step;
+        sy += sy_step;
+        if (WIDE) __syncwarp();                              // the warp's words have all been read
+        copy();
+        at = at + row_bytes == AHEAD * row_bytes ? 0 : at + row_bytes;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (sums) flush();
+    if (a.pre_part) {
+#pragma unroll
+        for (int c = 0; c < V; c++) {
+            const uint32_t k = 8 * chunk(c);
+            float* p = a.pre_part + (int64_t)blockIdx.x * SUMS * a.wide + k;
+            if (k < a.wide) {
+                put_sums(p, pw[c]);
+                if (TWO) put_sums(p + a.wide, pb[c]);
+            }
+        }
+    }
+}
+
 template <int DT, int RT, int V>
 static const void* norm_forward_of(int post, int pre, bool whole)
 {
@@ -585,21 +997,26 @@ static const void* norm_forward_of(int post, int pre, bool whole)
     }
     return (const void*)k_norm_forward<DT, RT, V, -1, -1>;
 }
-// `two`: both sums are wanted; set where the kernel keeps both all the same.
+// `two`: both sums are wanted; set where the kernel keeps both all the same.  `smem`: bytes of
+// shared memory a thread of the kernel needs.
 template <int DT, int RT, int V>
-static const void* norm_backward_of(int post, int pre, bool whole, bool& two)
+static const void* norm_backward_of(int post, int pre, bool whole, bool& two, int& smem)
 {
-    if (whole && (!two || pre == 2)) {
-        if (post == 0 && pre == 1) return (const void*)k_norm_backward<DT, RT, V, 0, 1, false>;
-        if (post == 1 && pre == 1) return (const void*)k_norm_backward<DT, RT, V, 1, 1, false>;
-        if (pre == 2 && (post == 0 || post == 2)) {
-            two = true;
-            return post == 0 ? (const void*)k_norm_backward<DT, RT, V, 0, 2, true>
-                             : (const void*)k_norm_backward<DT, RT, V, 2, 2, true>;
+    smem = 16 * ZERO_NORM_WORDS * V;
+    if constexpr (V <= 2) {
+        if (whole && (!two || pre == 2)) {
+            smem = NormRing<RT, V>::bytes;
+            if (post == 0 && pre == 1) return (const void*)k_norm_backward_whole<DT, RT, V, 0, 1, false>;
+            if (post == 1 && pre == 1) return (const void*)k_norm_backward_whole<DT, RT, V, 1, 1, false>;
+            if (pre == 2 && (post == 0 || post == 2)) {
+                two = true;
+                return post == 0 ? (const void*)k_norm_backward_whole<DT, RT, V, 0, 2, true>
+                                 : (const void*)k_norm_backward_whole<DT, RT, V, 2, 2, true>;
+            }
+            smem = 16 * ZERO_NORM_WORDS * V;
         }
     }
-    return two ? (const void*)k_norm_backward<DT, RT, V, -1, -1, true>
-               : (const void*)k_norm_backward<DT, RT, V, -1, -1, false>;
+    return two ? (const void*)k_norm_backward<DT, RT, V, true> : (const void*)k_norm_backward<DT, RT, V, false>;
 }
 
 }  // namespace zero

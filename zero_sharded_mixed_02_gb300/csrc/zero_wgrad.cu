@@ -45,15 +45,16 @@ namespace zero {
 #define ZERO_WG_THREADS 512                 // warps 0 TMA, 1 products, 4-7 output, 8-15 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
-#define ZERO_WG_SUMS 16                     // token ranges of the column sums
 
-// bytes of a stage in one SM: dy rows, codes, exponents, widened codes
+// bytes of a stage in one SM: dy rows, codes, exponents; and of widened codes (as dy rows); the
+// column sums of a tile (a row of 128 from each of the eight widening warps), two tiles deep
 #define ZERO_WG_A 16384
 #define ZERO_WG_C 8192
 #define ZERO_WG_E 1024
 #define ZERO_WG_STAGE (ZERO_WG_A + ZERO_WG_C + ZERO_WG_E)
-#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + ZERO_WG_WIDE * ZERO_WG_A + 1024)
-#define ZERO_WG_SLOT (ZERO_WG_TILE * ZERO_WG_TILE)     // floats of a part
+#define ZERO_WG_SUMS 4096
+#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + ZERO_WG_WIDE * ZERO_WG_A + 2 * ZERO_WG_SUMS + 1024)
+#define ZERO_WG_SLOT (ZERO_WG_TILE * (ZERO_WG_TILE + 1))  // floats of a part: its sums, its rows' sums of dy
 
 struct WgradArgs {
     const uint16_t* dy;
@@ -61,7 +62,7 @@ struct WgradArgs {
     const uint16_t *scale, *shift;
     void *dw, *db;
     int32_t* err;
-    float *sums, *slots;                    // column sums [ZERO_WG_SUMS][n]; parts
+    float* slots;                           // parts of cut tiles
     int64_t tokens, n, k, ldy, ldw;
     int64_t wide;
     int64_t tiles, steps;                   // steps: stages of a tile
@@ -175,13 +176,8 @@ static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, in
         if (c < m) put_grad(a.dw, at + c, v[c], a.grad_dtype, a.accumulate);
 }
 
-static __device__ __forceinline__ float column_sum(const WgradArgs& a, int64_t i)
-{
-    float s = 0.0f;
-    if ((a.shift || a.db) && i < a.n)
-        for (int p = 0; p < ZERO_WG_SUMS; p++) s += __ldg(a.sums + p * a.n + i);
-    return s;
-}
+// Whether a tile's epilogue needs its rows' sums of dy.
+static __device__ __forceinline__ bool needs_sums(const WgradArgs& a, int64_t j0) { return a.shift || (a.db && j0 == 0); }
 
 // ---- the pair's machinery ------------------------------------------------------------
 static __device__ __forceinline__ uint32_t cluster_rank()
@@ -305,6 +301,7 @@ struct WgradShared {
     uint64_t ready[ZERO_WG_STAGES];         // both SMs' operands are in place (first SM's)
     uint64_t empty[ZERO_WG_STAGES];         // the stage's products are done
     uint64_t sum_full[2], sum_empty[2];     // accumulators
+    uint64_t col_full[2], col_empty[2];     // column sums
     uint64_t drain;                         // products in flight after a wait gave up
     uint32_t tmem;
     int dead;
@@ -318,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     extern __shared__ unsigned char raw[];
     __shared__ WgradShared sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t wide = base + ZERO_WG_STAGES * ZERO_WG_STAGE;
+    const uint32_t wide = base + ZERO_WG_STAGES * ZERO_WG_STAGE, cols = wide + ZERO_WG_WIDE * ZERO_WG_A;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
@@ -332,6 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
         for (int s = 0; s < 2; s++) {
             mbar_init(smem_u32(&sh.sum_full[s]), 1);
             mbar_init(smem_u32(&sh.sum_empty[s]), 8);
+            mbar_init(smem_u32(&sh.col_full[s]), 8);
+            mbar_init(smem_u32(&sh.col_empty[s]), 4);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.dead = 0;
@@ -444,10 +443,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
         int s = group, b = group % ZERO_WG_WIDE, skip = group;
         int f = (group - ZERO_WG_WIDE + ZERO_WG_STAGES) % ZERO_WG_STAGES;   // stage whose products free the place
         uint32_t ph = 0, fph = group < ZERO_WG_WIDE;        // parity 1 of an unused barrier does not wait
+        // column sums of dy, for the tiles that need them: eight columns (chunk) of every fourth token
+        const int chunk = w & 15, tok0 = w >> 4;
+        int summed = 0;
         bool ok = true;
         for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
             int64_t i0, j0;
             wgrad_place(a, g.tile, i0, j0);
+            const bool sums = needs_sums(a, j0);
+            f32x2_t total[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) total[c] = pack2(0.0f, 0.0f);
             const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * 128) / 32 & 15) + blk;
             const int64_t len = g.s1 - g.s0;
             int64_t t = skip;
@@ -491,6 +497,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                         }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (sums) {
+                    const uint32_t at = base + s * ZERO_WG_STAGE + (chunk >> 3) * 8192;
+                    constexpr int EACH = 256 / GROUPS / 16;    // tokens a step
+#pragma unroll 4
+                    for (int k = tok0; k < ZERO_WG_TOK; k += EACH) {
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(at + k * 128 + (((chunk & 7) ^ (k & 7)) << 4)));
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            float lo, hi;
+                            widen2<DT>(v[c], lo, hi);
+                            total[c] = add2(total[c], pack2(lo, hi));
+                        }
+                    }
+                }
                 __syncwarp();
                 if (lane == 0) arrive_first(smem_u32(&sh.ready[s]));
                 s += GROUPS;
@@ -500,20 +523,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                 b = (b + GROUPS) % ZERO_WG_WIDE;
             }
             skip = (int)(t - len);
+            if (sums && ok) {
+                // the two lanes of a warp with the same columns, then a row of 128 from each warp
+                const int buf = summed & 1;
+                if (summed >= 2 && !pair_wait(smem_u32(&sh.col_empty[buf]), (uint32_t)((summed >> 1) - 1) & 1u, dead, a.err)) break;
+                float v[8];
+#pragma unroll
+                for (int c = 0; c < 4; c++) unpack2(total[c], v[2 * c], v[2 * c + 1]);
+#pragma unroll
+                for (int c = 0; c < 8; c++) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], 16);
+                if (lane < 16) {
+                    const uint32_t to = cols + buf * ZERO_WG_SUMS + (warp - 8) * 512 + chunk * 32;
+#pragma unroll
+                    for (int c = 0; c < 8; c += 4)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * c), "f"(v[c]), "f"(v[c + 1]),
+                                     "f"(v[c + 2]), "f"(v[c + 3]) : "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.col_full[buf]));
+                summed++;
+            }
         }
     } else if (warp >= 4) {
         // ---- output: warp w has rows 32 (w - 4) + lane of this SM's half ----
+        int summed = 0;
         for (int i = 0; wgrad_segment(a, pair, i, g); i++) {
             const int acc = i & 1;
             int64_t i0, j0;
             wgrad_place(a, g.tile, i0, j0);
             const int64_t r = i0 + rank * 128 + (warp - 4) * 32 + lane;
             // a wait that gave up in any lane leaves the whole warp without the sums
-            const bool have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, a.err));
+            bool have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, a.err));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const float sum = g.slot < 0 ? column_sum(a, r) : 0.0f;
-            if (g.slot < 0 && a.db && j0 == 0 && r < a.n)
-                put_grad(a.db, r, have ? sum : __uint_as_float(0x7FC00000u), a.grad_dtype, a.accumulate);
+            float* part = g.slot < 0 ? nullptr : a.slots + (int64_t)g.slot * ZERO_WG_SLOT;
+            float sum = 0.0f;
+            if (needs_sums(a, j0)) {
+                const int buf = summed & 1;
+                have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.col_full[buf]), (uint32_t)(summed >> 1) & 1u, dead, a.err)) && have;
+#pragma unroll
+                for (int w = 0; w < 8; w++) {
+                    float x;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
+                                 : "r"(cols + buf * ZERO_WG_SUMS + w * 512 + ((warp - 4) * 32 + lane) * 4));
+                    sum += x;
+                }
+                if (!have) sum = __uint_as_float(0x7FC00000u);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.col_empty[buf]));
+                summed++;
+                if (part) part[ZERO_WG_TILE * ZERO_WG_TILE + rank * 128 + (warp - 4) * 32 + lane] = sum;
+                else if (a.db && j0 == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
+            }
             for (int c = 0; c < ZERO_WG_TILE / 32; c++) {
                 float v[32];
                 if (have) {
@@ -522,10 +582,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e++) v[e] = __uint_as_float(0x7FC00000u);
                 }
-                if (g.slot < 0) {
+                if (!part) {
                     put_row<DT>(a, r, j0 + c * 32, v, sum);
                 } else {                                      // four columns of 32 rows: one run of 512 bytes
-                    float4* o = reinterpret_cast<float4*>(a.slots + (int64_t)g.slot * ZERO_WG_SLOT) +
+                    float4* o = reinterpret_cast<float4*>(part) +
                                 ((rank * 4 + warp - 4) * 64 + c * 8) * 32 + lane;
 #pragma unroll
                     for (int e = 0; e < 8; e++) o[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -557,12 +617,18 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ Wgra
     const int64_t p0 = ((q * a.steps + 1) * a.rest_pairs - 1) / units;
     const int64_t p1 = ((q + 1) * a.steps * a.rest_pairs - 1) / units;
     if (p0 == p1) return;                                            // not cut
-    float v[32];
+    int64_t i0, j0;
+    wgrad_place(a, (int64_t)a.waves * a.pairs + q, i0, j0);
+    const int64_t r = i0 + strip * 32 + lane;
+    const bool sums = needs_sums(a, j0);
+    float v[32], sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < 32; e++) v[e] = 0.0f;
     for (int64_t p = p0; p <= p1; p++) {
         const int64_t slot = 2 * p + (p * units / a.rest_pairs / a.steps < q);
-        const float4* s = reinterpret_cast<const float4*>(a.slots + slot * ZERO_WG_SLOT) + (strip * 64 + c * 8) * 32 + lane;
+        const float* part = a.slots + slot * ZERO_WG_SLOT;
+        const float4* s = reinterpret_cast<const float4*>(part) + (strip * 64 + c * 8) * 32 + lane;
+        if (sums) sum += __ldcg(part + ZERO_WG_TILE * ZERO_WG_TILE + strip * 32 + lane);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
             const float4 f = __ldcg(s + e * 32);
@@ -572,31 +638,8 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ Wgra
             v[4 * e + 3] += f.w;
         }
     }
-    int64_t i0, j0;
-    wgrad_place(a, (int64_t)a.waves * a.pairs + q, i0, j0);
-    const int64_t r = i0 + strip * 32 + lane;
-    const float sum = column_sum(a, r);
     if (a.db && j0 == 0 && c == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
     put_row<DT>(a, r, j0 + c * 32, v, sum);
-}
-
-// Column sums of dy over ZERO_WG_SUMS token ranges (blockIdx.y).
-template <int DT>
-__global__ void __launch_bounds__(256) k_wgrad_sums(const __grid_constant__ WgradArgs a)
-{
-    __shared__ float part[8][32];
-    const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    const int64_t t1 = (blockIdx.y + 1) * a.tokens / ZERO_WG_SUMS;
-    float s = 0.0f;
-    if (i < a.n)
-        for (int64_t t = blockIdx.y * a.tokens / ZERO_WG_SUMS + (threadIdx.x >> 5); t < t1; t += 8)
-            s += widen1<DT>(__ldg(a.dy + t * a.ldy + i));
-    part[threadIdx.x >> 5][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (threadIdx.x >= 32 || i >= a.n) return;
-    s = 0.0f;
-    for (int w = 0; w < 8; w++) s += part[w][threadIdx.x];
-    a.sums[blockIdx.y * a.n + i] = s;
 }
 
 template <int DT>
@@ -662,8 +705,7 @@ bool sizes_ok(int64_t tokens, int64_t n, int64_t k)
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t steps_of(int64_t tokens) { return up(tokens, ZERO_WG_TOK); }
 
-// Workspace: the status word (256 bytes), the column sums, the parts.
-int64_t sums_bytes(int64_t n) { return up(ZERO_WG_SUMS * n * 4, 256) * 256; }
+// Workspace: the status word (256 bytes), the parts.
 
 decltype(&cuTensorMapEncodeTiled) encode()
 {
@@ -727,7 +769,7 @@ extern "C" uint64_t zero_act_wgrad_workspace(int64_t tokens, int64_t n, int64_t 
 {
     if (!sizes_ok(tokens, n, k)) return 0;
     const bool cut = steps_of(tokens) >= 2 * ZERO_WG_PART;
-    return 256 + (uint64_t)sums_bytes(n) + (cut ? 2ull * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4 : 0);
+    return 256 + (cut ? 2ull * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4 : 0);
 }
 
 extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int64_t tokens, int64_t n,
@@ -761,8 +803,7 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.dw = dw;
     a.db = db;
     a.err = static_cast<int32_t*>(work);
-    a.sums = reinterpret_cast<float*>(static_cast<char*>(work) + 256);
-    a.slots = reinterpret_cast<float*>(static_cast<char*>(work) + 256 + sums_bytes(n));
+    a.slots = reinterpret_cast<float*>(static_cast<char*>(work) + 256);
     a.tokens = tokens; a.n = n; a.k = k; a.ldy = ldy; a.ldw = ldw;
     a.wide = act_wide(k);
     a.grad_dtype = grad_dtype;
@@ -791,10 +832,6 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     if (!tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, dy, n, tokens, ldy * 2, 64, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tensor_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 128, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !tensor_map(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 16, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return ZERO_ECUDA;
-    if ((col_shift || db) &&
-        !launch(half ? (const void*)k_wgrad_sums<0> : (const void*)k_wgrad_sums<1>,
-                dim3((unsigned)up(n, 32), ZERO_WG_SUMS), 256, 0, args, stream))
         return ZERO_ECUDA;
     args[1] = &my;
     args[2] = &mc;

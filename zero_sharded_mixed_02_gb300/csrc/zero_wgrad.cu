@@ -45,6 +45,7 @@ namespace zero {
 #define ZERO_WG_THREADS 512                 // warps 0 TMA, 1 products, 4-7 output, 8-15 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
+#define ZERO_WG_RANGES 32                   // most token ranges that k_wgrad_columns adds
 
 // bytes of a stage in one SM: dy rows, codes, exponents; and of widened codes (as dy rows); the
 // column sums of a tile (a row of 128 from each of the eight widening warps), two tiles deep
@@ -62,52 +63,73 @@ struct WgradArgs {
     const uint16_t *scale, *shift;
     void *dw, *db;
     int32_t* err;
-    float* slots;                           // parts of cut tiles
+    float *sums, *slots;                    // dy's columns added [ZERO_WG_RANGES][n] (null: not); parts of cut tiles
     int64_t tokens, n, k, ldy, ldw;
     int64_t wide;
-    int64_t tiles, steps;                   // steps: stages of a tile
-    int tiles_n, tiles_k, pairs, waves, rest, rest_pairs;
-    int grad_dtype, accumulate, vec;
+    int steps;                              // stages of a tile
+    uint32_t tiles_n, tiles_k, share, extra;
+    int pairs, waves, rest, rest_pairs;
+    int grad_dtype, accumulate, vec, vec_s;
+    int copied, ranges;                     // dy is k_wgrad_columns' copy; the sums' token ranges
 };
 
 // ---- the division of the work ------------------------------------------------------
 struct WgradSegment {
-    int64_t tile, s0, s1;                   // stages [s0, s1) of a tile
+    uint32_t tile;
+    int32_t s0, s1;                         // stages [s0, s1) of a tile
     int slot;                               // -1: the whole tile, else its part's place
 };
 
+// First unit (stage of a tile of the last wave) of a pair's share.
+static __host__ __device__ __forceinline__ uint32_t wgrad_share(const WgradArgs& a, uint32_t pair)
+{
+    return pair * a.share + (pair < a.extra ? pair : a.extra);
+}
+
 // Segment i of a pair; false past its last.
-static __host__ __device__ __forceinline__ bool wgrad_segment(const WgradArgs& a, int pair, int i, WgradSegment& g)
+static __host__ __device__ __forceinline__ bool wgrad_segment(const WgradArgs& a, uint32_t pair, int i, WgradSegment& g)
 {
     if (i < a.waves) {
-        g.tile = (int64_t)i * a.pairs + pair;
+        g.tile = (uint32_t)i * a.pairs + pair;
         g.s0 = 0;
         g.s1 = a.steps;
         g.slot = -1;
         return true;
     }
-    if (pair >= a.rest_pairs) return false;
-    const int64_t units = (int64_t)a.rest * a.steps;
-    const int64_t u0 = pair * units / a.rest_pairs, u1 = (pair + 1) * units / a.rest_pairs;
-    const int64_t t = u0 / a.steps + (i - a.waves);
-    int64_t b = t * a.steps, e = b + a.steps;
+    if (pair >= (uint32_t)a.rest_pairs) return false;
+    const uint32_t u0 = wgrad_share(a, pair), u1 = wgrad_share(a, pair + 1), steps = a.steps;
+    const uint32_t t = u0 / steps + (i - a.waves);
+    uint32_t b = t * steps, e = b + steps;
     if (b >= u1) return false;
     b = b > u0 ? b : u0;
     e = e < u1 ? e : u1;
-    g.tile = (int64_t)a.waves * a.pairs + t;
-    g.s0 = b - t * a.steps;
-    g.s1 = e - t * a.steps;
-    g.slot = g.s1 - g.s0 == a.steps ? -1 : 2 * pair + (i - a.waves);
+    g.tile = (uint32_t)a.waves * a.pairs + t;
+    g.s0 = (int32_t)(b - t * steps);
+    g.s1 = (int32_t)(e - t * steps);
+    g.slot = g.s1 - g.s0 == a.steps ? -1 : (int)(2 * pair) + (i - a.waves);
     return true;
 }
 
 // Tiles in an order that keeps a wave's panels few: bands of eight tiles along n.
-static __device__ __forceinline__ void wgrad_place(const WgradArgs& a, int64_t tile, int64_t& i0, int64_t& j0)
+static __host__ __device__ __forceinline__ void wgrad_place(const WgradArgs& a, uint32_t tile, int64_t& i0, int64_t& j0)
 {
-    const int64_t band = tile / (8ll * a.tiles_k), in = tile - band * 8 * a.tiles_k;
-    const int64_t high = a.tiles_n - band * 8 < 8 ? a.tiles_n - band * 8 : 8;
-    j0 = in / high * ZERO_WG_TILE;
-    i0 = (band * 8 + in % high) * ZERO_WG_TILE;
+    const uint32_t band = tile / (8u * a.tiles_k), in = tile - band * 8u * a.tiles_k;
+    const uint32_t high = a.tiles_n - band * 8 < 8 ? a.tiles_n - band * 8 : 8;
+    j0 = (int64_t)(in / high) * ZERO_WG_TILE;
+    i0 = (int64_t)(band * 8 + in % high) * ZERO_WG_TILE;
+}
+
+// For each tile of the last wave: the pairs that have parts of it, and whether the first of
+// them has it as its second tile.
+struct WgradJoin {
+    uint8_t p0[ZERO_WG_PAIRS], p1[ZERO_WG_PAIRS], second[ZERO_WG_PAIRS];
+};
+
+// Columns of the tile at j0 that are multiplied: fewer at the right edge (two SMs' halves in
+// whole blocks of 32).
+static __device__ __forceinline__ int wgrad_width(const WgradArgs& a, int64_t j0)
+{
+    return a.k - j0 >= ZERO_WG_TILE ? ZERO_WG_TILE : (int)(a.k - j0 + 63) / 64 * 64;
 }
 
 // ---- output ------------------------------------------------------------------------
@@ -124,25 +146,51 @@ static __device__ __forceinline__ void put_grad(void* p, int64_t i, float v, int
     else static_cast<uint16_t*>(p)[i] = grad_dtype == 0 ? narrow1<0>(v) : narrow1<1>(v);
 }
 
-// 32 columns from j of row i; s the row's column sum of dy.
 template <int DT>
-static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, int64_t j, float (&v)[32], float s)
+static __device__ __forceinline__ void eight(const uint16_t* p, float (&w)[8])
+{
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    widen2<DT>(q.x, w[0], w[1]);
+    widen2<DT>(q.y, w[2], w[3]);
+    widen2<DT>(q.z, w[4], w[5]);
+    widen2<DT>(q.w, w[6], w[7]);
+}
+
+// N columns from j of row i; s the row's column sum of dy.
+template <int DT, int N>
+static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, int64_t j, float (&v)[N], float s)
 {
     if (i >= a.n || j >= a.k) return;
-    const int m = a.k - j < 32 ? (int)(a.k - j) : 32;
-    if (a.scale || a.shift)
+    const int m = a.k - j < N ? (int)(a.k - j) : N;
+    if ((a.scale || a.shift) && a.vec_s && m == N) {
 #pragma unroll
-        for (int c = 0; c < 32; c++)
+        for (int c = 0; c < N; c += 8) {
+            float w[8];
+            if (a.scale) {
+                eight<DT>(a.scale + j + c, w);
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[c + e] *= w[e];
+            }
+            if (a.shift) {
+                eight<DT>(a.shift + j + c, w);
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[c + e] = __fmaf_rn(s, w[e], v[c + e]);
+            }
+        }
+    } else if (a.scale || a.shift) {
+#pragma unroll
+        for (int c = 0; c < N; c++)
             if (c < m) {
                 if (a.scale) v[c] *= widen1<DT>(__ldg(a.scale + j + c));
                 if (a.shift) v[c] = __fmaf_rn(s, widen1<DT>(__ldg(a.shift + j + c)), v[c]);
             }
+    }
     const int64_t at = i * a.ldw + j;
-    if (a.vec && m == 32) {
+    if (a.vec && m == N) {
         if (a.grad_dtype == 2) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
+            for (int c = 0; c < N; c += 4) {
                 float4 q = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                 if (a.accumulate) {
                     const float4 p = o[c / 4];
@@ -153,7 +201,7 @@ static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, in
         } else {
             uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dw) + at);
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
+            for (int c = 0; c < N; c += 8) {
                 if (a.accumulate) {
                     const uint4 p = o[c / 8];
                     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
@@ -172,12 +220,22 @@ static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, in
         return;
     }
 #pragma unroll
-    for (int c = 0; c < 32; c++)
+    for (int c = 0; c < N; c++)
         if (c < m) put_grad(a.dw, at + c, v[c], a.grad_dtype, a.accumulate);
 }
 
-// Whether a tile's epilogue needs its rows' sums of dy.
-static __device__ __forceinline__ bool needs_sums(const WgradArgs& a, int64_t j0) { return a.shift || (a.db && j0 == 0); }
+// Whether a tile adds its rows' sums of dy: for db, in the first column of tiles, unless
+// k_wgrad_columns has added them all.
+static __device__ __forceinline__ bool adds_sums(const WgradArgs& a, int64_t j0) { return a.db && j0 == 0 && !a.sums; }
+
+// Row i's sum of dy from k_wgrad_columns.
+static __device__ __forceinline__ float column_sum(const WgradArgs& a, int64_t i)
+{
+    float s = 0.0f;
+    if (a.sums && i < a.n)
+        for (int p = 0; p < a.ranges; p++) s += __ldg(a.sums + p * a.n + i);
+    return s;
+}
 
 // ---- the pair's machinery ------------------------------------------------------------
 static __device__ __forceinline__ uint32_t cluster_rank()
@@ -314,11 +372,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
 {
     extern __shared__ unsigned char raw[];
     __shared__ WgradShared sh;
+    asm volatile("griddepcontrol.launch_dependents;");       // k_wgrad_join waits for this kernel's end itself
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t wide = base + ZERO_WG_STAGES * ZERO_WG_STAGE, cols = wide + ZERO_WG_WIDE * ZERO_WG_A;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1;
+    const uint32_t pair = blockIdx.x >> 1;
     volatile int* dead = &sh.dead;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ZERO_WG_STAGES; s++) {
@@ -348,6 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
 
     if (warp == 0) {
         // ---- loads ----
+        if (a.copied) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
@@ -356,15 +416,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
                 int64_t i0, j0;
                 wgrad_place(a, g.tile, i0, j0);
-                const int x = (int)(i0 + rank * 128), c = (int)(j0 + rank * 128);
+                const int x = (int)(i0 + rank * 128), c = (int)j0 + rank * (wgrad_width(a, j0) / 2);
                 const int e = (int)a.wide + (c / 32 & ~15);
-                for (int64_t t = g.s0; t < g.s1; t++) {
+                for (int t = g.s0; t < g.s1; t++) {
                     if (issued >= ZERO_WG_STAGES && !pair_wait(smem_u32(&sh.empty[s]), ph ^ 1u, dead, a.err)) {
                         ok = false;
                         break;
                     }
                     const uint32_t at = base + s * ZERO_WG_STAGE, bar = smem_u32(&sh.full[s]);
-                    const int y = (int)(t * ZERO_WG_TOK);
+                    const int y = t * ZERO_WG_TOK;
                     mbar_expect_tx(bar, ZERO_WG_A + ZERO_WG_C + ZERO_WG_E);
                     tma_box(at, &map_y, x, y, bar);
                     tma_box(at + 8192, &map_y, x + 64, y, bar);
@@ -387,9 +447,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     } else if (warp == 1) {
         // ---- products (the first SM's thread, for both) ----
         if (lane == 0 && rank == 0) {
-            // fp32 sums of fp16/bf16 operands, both with the contracted axis strided, 256 x 256
-            const uint32_t what = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | 1u << 15 | 1u << 16 |
-                                  (uint32_t)(ZERO_WG_TILE >> 3) << 17 | (uint32_t)(ZERO_WG_TILE >> 4) << 24;
+            // fp32 sums of fp16/bf16 operands, both with the contracted axis strided, 256 x width
+            const uint32_t kind = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | 1u << 15 | 1u << 16 |
+                                  (uint32_t)(ZERO_WG_TILE >> 4) << 24;
             int s = 0, b = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -400,8 +460,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     ok = false;
                     break;
                 }
+                int64_t i0, j0;
+                wgrad_place(a, g.tile, i0, j0);
+                const uint32_t what = kind | (uint32_t)(wgrad_width(a, j0) >> 3) << 17;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int64_t t = g.s0; t < g.s1; t++) {
+                for (int t = g.s0; t < g.s1; t++) {
                     if (!pair_wait(smem_u32(&sh.ready[s]), ph, dead, a.err)) {
                         ok = false;
                         break;
@@ -450,13 +513,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
         for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
             int64_t i0, j0;
             wgrad_place(a, g.tile, i0, j0);
-            const bool sums = needs_sums(a, j0);
+            const bool sums = adds_sums(a, j0);
             f32x2_t total[4];
 #pragma unroll
             for (int c = 0; c < 4; c++) total[c] = pack2(0.0f, 0.0f);
-            const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * 128) / 32 & 15) + blk;
-            const int64_t len = g.s1 - g.s0;
-            int64_t t = skip;
+            const int half = wgrad_width(a, j0) / 2;          // this SM's columns
+            const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * half) / 32 & 15) + blk;
+            const int len = g.s1 - g.s0;
+            int t = skip;
             for (; t < len; t += GROUPS) {
                 if (!pair_wait(smem_u32(&sh.full[s]), ph, dead, a.err)) {
                     ok = false;
@@ -522,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                 if (f >= ZERO_WG_STAGES) { f -= ZERO_WG_STAGES; fph ^= 1u; }
                 b = (b + GROUPS) % ZERO_WG_WIDE;
             }
-            skip = (int)(t - len);
+            skip = t - len;
             if (sums && ok) {
                 // the two lanes of a warp with the same columns, then a row of 128 from each warp
                 const int buf = summed & 1;
@@ -546,6 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
         }
     } else if (warp >= 4) {
         // ---- output: warp w has rows 32 (w - 4) + lane of this SM's half ----
+        if (a.sums) asm volatile("griddepcontrol.wait;" ::: "memory");
         int summed = 0;
         for (int i = 0; wgrad_segment(a, pair, i, g); i++) {
             const int acc = i & 1;
@@ -556,9 +621,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             bool have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, a.err));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             float* part = g.slot < 0 ? nullptr : a.slots + (int64_t)g.slot * ZERO_WG_SLOT;
-            float sum = 0.0f;
-            if (needs_sums(a, j0)) {
+            float sum = part ? 0.0f : column_sum(a, r);
+            if (a.sums && !part && a.db && j0 == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
+            if (adds_sums(a, j0)) {
                 const int buf = summed & 1;
+                sum = 0.0f;
                 have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.col_full[buf]), (uint32_t)(summed >> 1) & 1u, dead, a.err)) && have;
 #pragma unroll
                 for (int w = 0; w < 8; w++) {
@@ -574,7 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                 if (part) part[ZERO_WG_TILE * ZERO_WG_TILE + rank * 128 + (warp - 4) * 32 + lane] = sum;
                 else if (a.db && j0 == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
             }
-            for (int c = 0; c < ZERO_WG_TILE / 32; c++) {
+            const int width = wgrad_width(a, j0);
+            for (int c = 0; c < width / 32; c++) {
                 float v[32];
                 if (have) {
                     read_accumulator(tmem + acc * ZERO_WG_TILE + c * 32 + ((uint32_t)(warp - 4) << 21), v);
@@ -583,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     for (int e = 0; e < 32; e++) v[e] = __uint_as_float(0x7FC00000u);
                 }
                 if (!part) {
-                    put_row<DT>(a, r, j0 + c * 32, v, sum);
+                    put_row<DT, 32>(a, r, j0 + c * 32, v, sum);
                 } else {                                      // four columns of 32 rows: one run of 512 bytes
                     float4* o = reinterpret_cast<float4*>(part) +
                                 ((rank * 4 + warp - 4) * 64 + c * 8) * 32 + lane;
@@ -603,34 +671,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
 }
 
 // Adds the parts of the cut tiles in token order and writes them out: a warp takes 32
-// rows and 32 columns of a tile.
+// rows and 16 columns of a tile.
 template <int DT>
-__global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ WgradArgs a)
+__global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ WgradArgs a, const __grid_constant__ WgradJoin of)
 {
-    const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    const int64_t q = unit >> 6;
-    const int strip = (int)(unit >> 3) & 7, c = (int)unit & 7;      // (SM, warp) of the rows; 32 columns
-    if (q >= a.rest) return;
-    const int64_t units = (int64_t)a.rest * a.steps;
-    // pair of unit u: the largest p with floor(p units / pairs) <= u
-    const int64_t p0 = ((q * a.steps + 1) * a.rest_pairs - 1) / units;
-    const int64_t p1 = ((q + 1) * a.steps * a.rest_pairs - 1) / units;
-    if (p0 == p1) return;                                            // not cut
+    const int q = unit >> 7;
+    const int strip = (unit >> 4) & 7, c = unit & 15;               // (SM, warp) of the rows; 16 columns
+    const int p0 = of.p0[q], p1 = of.p1[q], first = of.second[q];
     int64_t i0, j0;
-    wgrad_place(a, (int64_t)a.waves * a.pairs + q, i0, j0);
+    wgrad_place(a, (uint32_t)(a.waves * a.pairs + q), i0, j0);
     const int64_t r = i0 + strip * 32 + lane;
-    const bool sums = needs_sums(a, j0);
-    float v[32], sum = 0.0f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");              // the kernel whose parts these are
+    if (p0 == p1 || j0 + c * 16 >= a.k) return;                     // not cut, or past the right edge
+    const bool sums = adds_sums(a, j0);
+    float v[16], sum = column_sum(a, r);
 #pragma unroll
-    for (int e = 0; e < 32; e++) v[e] = 0.0f;
-    for (int64_t p = p0; p <= p1; p++) {
-        const int64_t slot = 2 * p + (p * units / a.rest_pairs / a.steps < q);
-        const float* part = a.slots + slot * ZERO_WG_SLOT;
-        const float4* s = reinterpret_cast<const float4*>(part) + (strip * 64 + c * 8) * 32 + lane;
+    for (int e = 0; e < 16; e++) v[e] = 0.0f;
+#pragma unroll 4
+    for (int p = p0; p <= p1; p++) {
+        const float* part = a.slots + (int64_t)(2 * p + (p == p0 ? first : 0)) * ZERO_WG_SLOT;
+        const float4* s = reinterpret_cast<const float4*>(part) + (strip * 64 + c * 4) * 32 + lane;
         if (sums) sum += __ldcg(part + ZERO_WG_TILE * ZERO_WG_TILE + strip * 32 + lane);
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
+        for (int e = 0; e < 4; e++) {
             const float4 f = __ldcg(s + e * 32);
             v[4 * e] += f.x;
             v[4 * e + 1] += f.y;
@@ -639,54 +704,61 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ Wgra
         }
     }
     if (a.db && j0 == 0 && c == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
-    put_row<DT>(a, r, j0 + c * 32, v, sum);
+    put_row<DT, 16>(a, r, j0 + c * 16, v, sum);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) k_wgrad_plain(const __grid_constant__ WgradArgs a)
+// A first pass over dy where one is needed: its columns added over ZERO_WG_RANGES token
+// ranges (blockIdx.y) for the norm's bias, which every tile's output needs (adding them in
+// every tile would read each dy operand from shared memory once more, the product kernel's
+// bound: 23 us more at 8192 x 6400 x 1600, this pass xx us), and rows that are not aligned to
+// 16 bytes copied to rows that are, so that TMA can read them.  A warp takes 256 columns.
+template <int DT, bool COPY>
+__global__ void __launch_bounds__(256) k_wgrad_columns(const __grid_constant__ WgradArgs a, uint16_t* out, int64_t pitch)
 {
-    __shared__ float sy[16][64], sx[16][64];
-    const int64_t i0 = (int64_t)blockIdx.y * 64, j0 = (int64_t)blockIdx.x * 64;
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float acc[4][4] = {}, sum[4] = {};
-    for (int64_t t0 = 0; t0 < a.tokens; t0 += 16) {
-        for (int e = threadIdx.x; e < 1024; e += 256) {
-            const int64_t t = t0 + e / 64, i = i0 + e % 64, j = j0 + e % 64;
-            const bool in = t < a.tokens;
-            sy[e / 64][e % 64] = in && i < a.n ? widen1<DT>(a.dy[t * a.ldy + i]) : 0.0f;
-            float v = 0.0f;
-            if (in && j < a.k) {
-                const uint8_t* row = a.ckpt + t * act_stride(a.k);
-                uint32_t e = row[a.wide + j / 32];
-                if (DT == 0 && (e < 103 || e > 136)) e = 255;      // outside fp16
-                v = (float)(int8_t)row[j] * __uint_as_float(e << 23);
-                if (e == 255) v = __uint_as_float(0x7FC00000u);
+    __shared__ float part[8][256];
+    asm volatile("griddepcontrol.launch_dependents;");       // k_wgrad waits where it reads what this writes
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t i0 = (int64_t)blockIdx.x * 256;
+    const int64_t t0 = blockIdx.y * a.tokens / gridDim.y, t1 = (blockIdx.y + 1) * a.tokens / gridDim.y;
+    float s[8];
+#pragma unroll
+    for (int c = 0; c < 8; c++) s[c] = 0.0f;
+    // a lane's columns: eight neighbours, or where rows are not aligned four pairs 64 apart
+    const int64_t i = i0 + (COPY ? 2 : 8) * lane;
+#pragma unroll (COPY ? 4 : 8)
+    for (int64_t t = t0 + warp; t < t1; t += 8) {
+        const uint16_t* p = a.dy + t * a.ldy;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (COPY) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                if (i + 64 * c < a.n) w[c] = __ldg(p + i + 64 * c);
+                if (i + 64 * c + 1 < a.n) w[c] |= (uint32_t)__ldg(p + i + 64 * c + 1) << 16;
+                if (i + 64 * c < pitch) *reinterpret_cast<uint32_t*>(out + t * pitch + i + 64 * c) = w[c];
             }
-            sx[e / 64][e % 64] = v;
+        } else if (i + 8 <= a.n) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + i));
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                if (i + c < a.n) w[c / 2] |= (uint32_t)__ldg(p + i + c) << 16 * (c & 1);
         }
-        __syncthreads();
-#pragma unroll 4
-        for (int t = 0; t < 16; t++)
-            for (int p = 0; p < 4; p++) {
-                const float y = sy[t][ti * 4 + p];
-                sum[p] += y;
-                for (int q = 0; q < 4; q++) acc[p][q] = __fmaf_rn(y, sx[t][tj * 4 + q], acc[p][q]);
-            }
-        __syncthreads();
-    }
-    for (int p = 0; p < 4; p++) {
-        const int64_t i = i0 + ti * 4 + p;
-        if (i >= a.n) continue;
-        for (int q = 0; q < 4; q++) {
-            const int64_t j = j0 + tj * 4 + q;
-            if (j >= a.k) continue;
-            float v = acc[p][q];
-            if (a.scale) v *= widen1<DT>(a.scale[j]);
-            if (a.shift) v = __fmaf_rn(sum[p], widen1<DT>(a.shift[j]), v);
-            put_grad(a.dw, i * a.ldw + j, v, a.grad_dtype, a.accumulate);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            float lo, hi;
+            widen2<DT>(w[c], lo, hi);
+            s[2 * c] += lo;
+            s[2 * c + 1] += hi;
         }
-        if (a.db && blockIdx.x == 0 && tj == 0) put_grad(a.db, i, sum[p], a.grad_dtype, a.accumulate);
     }
+    if (!a.sums) return;
+#pragma unroll
+    for (int c = 0; c < 8; c++) part[warp][COPY ? 64 * (c / 2) + 2 * lane + (c & 1) : 8 * lane + c] = s[c];
+    __syncthreads();
+    float v = 0.0f;
+    for (int w = 0; w < 8; w++) v += part[w][threadIdx.x];
+    if (i0 + threadIdx.x < a.n) a.sums[blockIdx.y * a.n + i0 + threadIdx.x] = v;
 }
 
 }  // namespace zero
@@ -699,13 +771,21 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 bool sizes_ok(int64_t tokens, int64_t n, int64_t k)
 {
-    return tokens >= 0 && tokens < (1ll << 31) && n >= 1 && n <= (1ll << 24) && k >= 1 && k <= ZERO_ACT_MAX_COLS;
+    return tokens >= 0 && tokens < (1ll << 31) && n >= 1 && n <= (1ll << 24) && k >= 1 && k <= ZERO_ACT_MAX_COLS &&
+           n * k < (1ll << 46);              // tiles are counted in 32 bits
 }
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t steps_of(int64_t tokens) { return up(tokens, ZERO_WG_TOK); }
 
-// Workspace: the status word (256 bytes), the parts.
+// Workspace: the status word (256 bytes), the columns' sums, the parts, dy's copy.
+int64_t round_bytes(int64_t b) { return up(b, 256) * 256; }
+int64_t sums_bytes(int64_t n) { return round_bytes(ZERO_WG_RANGES * n * 4); }
+int64_t parts_bytes(int64_t tokens)
+{
+    return steps_of(tokens) < 2 * ZERO_WG_PART ? 0 : round_bytes(2ll * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4);
+}
+int64_t copy_bytes(int64_t tokens, int64_t n) { return round_bytes(tokens * up(n, 8) * 16); }
 
 decltype(&cuTensorMapEncodeTiled) encode()
 {
@@ -758,9 +838,21 @@ int device_pairs()
     return pairs[dev];
 }
 
-bool launch(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream)
+// `early`: the kernel may be placed before the one ahead of it in the stream has ended, and
+// waits for it itself.
+bool launch(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream, bool early = false)
 {
-    return cudaLaunchKernel(fn, grid, dim3(threads), args, smem, static_cast<cudaStream_t>(stream)) == cudaSuccess;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelExC(&c, fn, args) == cudaSuccess;
 }
 
 }  // namespace
@@ -768,8 +860,7 @@ bool launch(const void* fn, dim3 grid, int threads, int smem, void** args, void*
 extern "C" uint64_t zero_act_wgrad_workspace(int64_t tokens, int64_t n, int64_t k)
 {
     if (!sizes_ok(tokens, n, k)) return 0;
-    const bool cut = steps_of(tokens) >= 2 * ZERO_WG_PART;
-    return 256 + (cut ? 2ull * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4 : 0);
+    return (uint64_t)(256 + sums_bytes(n) + parts_bytes(tokens) + copy_bytes(tokens, n));
 }
 
 extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int64_t tokens, int64_t n,
@@ -803,32 +894,66 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.dw = dw;
     a.db = db;
     a.err = static_cast<int32_t*>(work);
-    a.slots = reinterpret_cast<float*>(static_cast<char*>(work) + 256);
+    char* at = static_cast<char*>(work) + 256;
+    if (col_shift) a.sums = reinterpret_cast<float*>(at);
+    at += sums_bytes(n);
+    a.slots = reinterpret_cast<float*>(at);
+    at += parts_bytes(tokens);
     a.tokens = tokens; a.n = n; a.k = k; a.ldy = ldy; a.ldw = ldw;
     a.wide = act_wide(k);
     a.grad_dtype = grad_dtype;
     a.accumulate = accumulate != 0;
     a.vec = aligned_to(dw, 16) && ldw * ge % 16 == 0;
+    a.vec_s = aligned_to(col_scale, 16) && aligned_to(col_shift, 16);
     const bool half = dtype == ZERO_FP16;
     void* args[] = {&a, nullptr, nullptr, nullptr};
-    if (!aligned_to(dy, 16) || ldy % 8 != 0)
-        return launch(half ? (const void*)k_wgrad_plain<0> : (const void*)k_wgrad_plain<1>,
-                      dim3((unsigned)up(k, 64), (unsigned)up(n, 64)), 256, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
     a.pairs = device_pairs();
     if (a.pairs == 0 || !encode()) return ZERO_ECUDA;
-    a.steps = steps_of(tokens);
-    a.tiles_n = (int)up(n, ZERO_WG_TILE);
-    a.tiles_k = (int)up(k, ZERO_WG_TILE);
-    a.tiles = (int64_t)a.tiles_n * a.tiles_k;
-    a.waves = (int)(a.tiles / a.pairs);
-    a.rest = (int)(a.tiles % a.pairs);
+    a.steps = (int)steps_of(tokens);
+    a.tiles_n = (uint32_t)up(n, ZERO_WG_TILE);
+    a.tiles_k = (uint32_t)up(k, ZERO_WG_TILE);
+    const int64_t tiles = (int64_t)a.tiles_n * a.tiles_k;
+    a.waves = (int)(tiles / a.pairs);
+    a.rest = (int)(tiles % a.pairs);
     a.rest_pairs = a.rest;
+    const int64_t units = (int64_t)a.rest * a.steps;        // below 80 * 2^25
     if (a.rest > 0 && a.steps >= 2 * ZERO_WG_PART) {
-        const int64_t parts = a.rest * a.steps / ZERO_WG_PART;
+        const int64_t parts = units / ZERO_WG_PART;
         a.rest_pairs = (int)(parts < a.rest ? a.rest : parts < a.pairs ? parts : a.pairs);
+    }
+    WgradJoin join{};
+    if (a.rest > 0) {
+        a.share = (uint32_t)(units / a.rest_pairs);
+        a.extra = (uint32_t)(units % a.rest_pairs);
+        for (int p = a.rest_pairs - 1; p >= 0; p--) {       // backwards: a tile's first pair is written last
+            const uint32_t t0 = wgrad_share(a, p) / a.steps, t1 = (wgrad_share(a, p + 1) - 1) / a.steps;
+            for (uint32_t t = t0; t <= t1; t++) {
+                if (join.p1[t] == 0) join.p1[t] = (uint8_t)p;
+                join.p0[t] = (uint8_t)p;
+                join.second[t] = t > t0;
+            }
+        }
     }
     CUtensorMap my, mc, me;
     const int64_t stride = act_stride(k);
+    const bool copy = !aligned_to(dy, 16) || ldy % 8 != 0;
+    if (copy || a.sums) {
+        uint16_t* out = reinterpret_cast<uint16_t*>(at);
+        int64_t pitch = up(n, 8) * 8;
+        const void* fn = copy ? (half ? (const void*)k_wgrad_columns<0, true> : (const void*)k_wgrad_columns<1, true>)
+                              : (half ? (const void*)k_wgrad_columns<0, false> : (const void*)k_wgrad_columns<1, false>);
+        void* first[] = {&a, &out, &pitch};
+        // one wave of blocks (three an SM), at least 32 tokens each
+        const int64_t wide = up(n, 256), most = up(tokens, 32), fill = 6ll * a.pairs / wide;
+        a.ranges = (int)(fill < 1 ? 1 : fill < most ? fill : most);
+        if (a.sums && a.ranges > ZERO_WG_RANGES) a.ranges = ZERO_WG_RANGES;
+        if (!launch(fn, dim3((unsigned)wide, (unsigned)a.ranges), 256, 0, first, stream)) return ZERO_ECUDA;
+        if (copy) {
+            dy = out;
+            ldy = pitch;
+            a.copied = 1;
+        }
+    }
     if (!tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, dy, n, tokens, ldy * 2, 64, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tensor_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 128, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !tensor_map(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, ckpt, stride, tokens, stride, 16, ZERO_WG_TOK, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -837,11 +962,14 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     args[2] = &mc;
     args[3] = &me;
     const int run = a.waves > 0 ? a.pairs : a.rest_pairs;
+    // after k_wgrad_columns, placed while that still runs (cluster sizes are the kernel's own)
     if (!launch(half ? (const void*)k_wgrad<0> : (const void*)k_wgrad<1>, dim3(2 * run), ZERO_WG_THREADS, ZERO_WG_SMEM, args,
-                stream))
+                stream, copy || a.sums))
         return ZERO_ECUDA;
+    void* last[] = {&a, &join};
     if (a.rest_pairs > a.rest &&
-        !launch(half ? (const void*)k_wgrad_join<0> : (const void*)k_wgrad_join<1>, dim3(a.rest * 8), 256, 0, args, stream))
+        !launch(half ? (const void*)k_wgrad_join<0> : (const void*)k_wgrad_join<1>, dim3(a.rest * 16), 256, 0, last, stream,
+                true))
         return ZERO_ECUDA;
     return ZERO_OK;
 }

@@ -546,14 +546,16 @@ zero_status_t zero_act_load(zero_dtype_t dtype, const void* ckpt, int64_t rows, 
  *               The caller zeroes it once, before the first use (with any sizes);
  *               every call leaves it ready for the next.  Calls whose executions
  *               overlap need a workspace each.
- * Matrices need the alignment of their element; 16-byte aligned dy rows are read
- * by TMA and 16-byte aligned dw rows are written in vectors, others element by
- * element.  tokens = 0 is accepted (the sums are zero).  Sums are taken in a
- * fixed order: equal inputs give equal bits.  Asynchronous.  A bounded device
+ * Matrices need the alignment of their element; dy rows that are not 16-byte
+ * aligned are first copied to the workspace (which always has room for that: 2
+ * bytes a value of dy), 16-byte aligned dw rows are written in vectors.  tokens = 0
+ * is accepted (the sums are zero).  Sums are taken in a fixed order: equal inputs
+ * give equal bits.  Asynchronous.  A bounded device
  * wait that gives up (none should) sets the first int32 of `work` to
  * ZERO_ETIMEOUT and writes NaN where the sums are missing.
  * Errors: ZERO_EINVAL (types, sizes: tokens in [0, 2^31), n in [1, 2^24], k in
- * [1, ZERO_ACT_MAX_COLS], ldy >= n, ldw >= k; null or misaligned pointer),
+ * [1, ZERO_ACT_MAX_COLS], n k < 2^46, n <= ldy <= 2^31, k <= ldw <= 2^31; null or
+ * misaligned pointer),
  * ZERO_ECUDA. */
 zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int64_t tokens, int64_t n,
                              int64_t ldy, const void* ckpt, int64_t k, const void* col_scale,

@@ -260,6 +260,28 @@ def test_wgrad_workspace_serves_calls_of_other_sizes(env):
         seen[s] = (dw, db)
 
 
+@pytest.mark.parametrize("tokens,n,k,grad", [(30011, 776, 771, R.FP32), (8192, 1024, 1024, R.BF16), (700, 40, 100, R.BF16)])
+def test_wgrad_gives_equal_bits_over_many_calls(env, tokens, n, k, grad):
+    """Loads that land in another order must not be taken for one another: the same call, with other
+    work on the stream between some of them, gives the same bits each time."""
+    torch, z = env
+    dw, db, work = wgrad_case(env, tokens, n, k, R.BF16, grad)
+    rng = np.random.default_rng(tokens + 7 * n + 13 * k)
+    dy = torch.from_numpy(rng.standard_normal((tokens, n)) * 0.05).to(torch.bfloat16).cuda()
+    x = torch.from_numpy(activations(rng, tokens, k)).to(torch.bfloat16).cuda()
+    ckpt = save(torch, z, x.data_ptr(), R.BF16, tokens, k, k)
+    first, other = None, torch.empty(1 << 27, dtype=torch.uint8, device="cuda")
+    for i in range(400):
+        dw, db = (torch.empty(n, k, device="cuda", dtype=kind(torch, grad)), torch.empty(n, device="cuda", dtype=kind(torch, grad)))
+        if i % 3 == 0:
+            other.fill_(i & 127)                                 # the operands leave the cache
+        z.zero_act_wgrad(R.BF16, dy, tokens, n, n, ckpt, k, None, None, grad, dw, k, db, 0, work, stream(torch))
+        if first is None:
+            first = (dw, db)
+        assert torch.equal(first[0], dw) and torch.equal(first[1], db), i
+    assert int(work[:4].view(torch.int32)[0]) == 0
+
+
 @pytest.mark.parametrize("what", ["dy", "x"])
 def test_wgrad_carries_non_finite_values(env, what):
     """An infinity or NaN in dy reaches its column's gradients; in x, its block's: what the step's

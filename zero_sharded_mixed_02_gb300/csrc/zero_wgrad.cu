@@ -33,31 +33,25 @@ namespace zero {
 
 #define ZERO_WG_TILE 256                    // rows and columns of a pair's tile
 #define ZERO_WG_TOK 64                      // tokens of a stage
-#ifndef ZERO_WG_STAGES
-#define ZERO_WG_STAGES 6                    // loaded stages (dy rows, codes)
-#endif
-#ifndef ZERO_WG_WIDE
-#define ZERO_WG_WIDE 4                      // widened stages
-#endif
-#ifndef ZERO_WG_GROUPS
+#define ZERO_WG_STAGES 6                    // stages of dy rows
+#define ZERO_WG_CODES 4                     // stages of codes
+#define ZERO_WG_WIDE 5                      // widened stages
 #define ZERO_WG_GROUPS 4                    // groups of widening warps, a stage each
-#endif
-#define ZERO_WG_THREADS 512                 // warps 0 TMA, 1 products, 4-7 output, 8-15 widening
+#define ZERO_WG_WIDENERS 256                // threads that widen codes
+#define ZERO_WG_THREADS (256 + ZERO_WG_WIDENERS)    // warps 0 and 2 TMA, 1 products, 4-7 output, from 8 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
-#ifndef ZERO_WG_RUN
 #define ZERO_WG_RUN 64                      // stages an accumulator adds for an fp32 gradient
-#endif
 #define ZERO_WG_RANGES 32                   // most token ranges that k_wgrad_columns adds
 
 // bytes of a stage in one SM: dy rows, codes, exponents; and of widened codes (as dy rows); the
-// column sums of a tile (a row of 128 from each of the eight widening warps), two tiles deep
+// column sums of a tile (a row of 128 from each widening warp)
 #define ZERO_WG_A 16384
 #define ZERO_WG_C 8192
 #define ZERO_WG_E 1024
-#define ZERO_WG_STAGE (ZERO_WG_A + ZERO_WG_C + ZERO_WG_E)
-#define ZERO_WG_SUMS 4096
-#define ZERO_WG_SMEM (ZERO_WG_STAGES * ZERO_WG_STAGE + ZERO_WG_WIDE * ZERO_WG_A + 2 * ZERO_WG_SUMS + 1024)
+#define ZERO_WG_SUMS (ZERO_WG_WIDENERS / 32 * 512)
+#define ZERO_WG_SMEM \
+    (ZERO_WG_STAGES * ZERO_WG_A + ZERO_WG_CODES * (ZERO_WG_C + ZERO_WG_E) + ZERO_WG_WIDE * ZERO_WG_A + ZERO_WG_SUMS + 1024)
 #define ZERO_WG_SLOT (ZERO_WG_TILE * (ZERO_WG_TILE + 1))  // floats of a part: its sums, its rows' sums of dy
 
 struct WgradArgs {
@@ -271,6 +265,16 @@ static __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// True in one lane of a whole warp.  Code under it is known to run in one thread, so that the
+// operands of the copies and products it issues stay in the warp's uniform registers: issuing a
+// stage's four products or its copies took about 800 cycles with `lane == 0`, longer than the
+// products themselves (1161 -> 1048 us at 16384 x 4096 x 14336).
+static __device__ __forceinline__ bool elected()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
 // Every thread of both SMs; the warp is together again after it (what follows may be a
 // whole-warp instruction).
 static __device__ __forceinline__ void cluster_sync()
@@ -306,12 +310,12 @@ static __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* 
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-// Completion of every product issued so far arrives on `bar` in both SMs.
-static __device__ __forceinline__ void commit_both(uint32_t bar)
+// Completion of every product issued so far arrives on `bar` in both SMs (or in those of a mask).
+static __device__ __forceinline__ void commit_both(uint32_t bar, uint16_t sms = 3)
 {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(bar), "h"((uint16_t)3) : "memory");
+        ::"r"(bar), "h"(sms) : "memory");
 }
 // Operand in shared memory with the non-contracted axis contiguous, 128-byte swizzle:
 // groups of 64 columns are 8192 bytes apart, groups of 8 tokens 1024.
@@ -379,18 +383,29 @@ static __device__ __forceinline__ uint32_t code_scale(uint32_t e)
     return s | s << 16;
 }
 
-// a group's stage index advances by GROUPS and wraps once; the stage whose products free a
-// place is the group's own last one (its waits' order needs that) and its barrier cannot have
-// gone round in between; a thread's further tokens keep their swizzle
-static_assert(ZERO_WG_GROUPS <= ZERO_WG_STAGES && ZERO_WG_WIDE == ZERO_WG_GROUPS && ZERO_WG_WIDE < ZERO_WG_STAGES &&
-              (ZERO_WG_TOK / ZERO_WG_GROUPS) % 8 == 0, "ring sizes");
+// Three rings, as stage g of a pair (counted over all its segments) goes through them: codes
+// (slot g mod CODES, free when a group of warps has read them), dy rows (slot g mod STAGES) and
+// widened codes (place g mod WIDE), both free when the products are done.
+// A parity wait does not tell a barrier's use from the one after next, so a thread may only wait
+// for a use when it knows the one before to be over.  Threads that take every stage in turn know
+// it.  A group of widening warps takes every fourth stage, and meets a ring's barriers only now
+// and then; each barrier it waits on is therefore one of (slots x GROUPS), of which it alone
+// meets every fourth, at every use.
+// The rings' depths: six, four and five fill the 227 KB and were the fastest at 16384 x 4096 x
+// 14336 and 8192 x 4096 x 4096 (one ring of six for both loads and four places: 2 to 5 % slower,
+// of five stages 13 %).  A stage's way through them takes about 2300 cycles (850 for the loads,
+// 1100 to widen, the arrivals), its products 512.
+static_assert((ZERO_WG_WIDENERS / ZERO_WG_GROUPS / 4) % 8 == 0, "a thread's tokens keep their swizzle");
 
 struct WgradShared {
-    uint64_t full[ZERO_WG_STAGES];          // a stage's bytes have come
-    uint64_t ready[ZERO_WG_STAGES];         // both SMs' operands are in place (first SM's)
-    uint64_t empty[ZERO_WG_STAGES];         // the stage's products are done
+    uint64_t rows[ZERO_WG_STAGES * ZERO_WG_GROUPS];     // a stage's dy rows have come
+    uint64_t codes[ZERO_WG_CODES * ZERO_WG_GROUPS];     // its codes and exponents have come
+    uint64_t done[ZERO_WG_WIDE * ZERO_WG_GROUPS];       // its products are done: the place is free
+    uint64_t empty[ZERO_WG_STAGES];         // the same, for the dy rows' slot
+    uint64_t read[ZERO_WG_CODES];           // its codes have been read
+    uint64_t ready[ZERO_WG_WIDE];           // both SMs' operands are in place (first SM's)
     uint64_t sum_full[2], sum_empty[2];     // accumulators
-    uint64_t col_full[2], col_empty[2];     // column sums
+    uint64_t col_full, col_empty;           // column sums
     uint64_t drain;                         // products in flight after a wait gave up
     uint32_t tmem;
     int dead;
@@ -404,23 +419,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     extern __shared__ unsigned char raw[];
     __shared__ WgradShared sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t wide = base + ZERO_WG_STAGES * ZERO_WG_STAGE, cols = wide + ZERO_WG_WIDE * ZERO_WG_A;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base_c = base + ZERO_WG_STAGES * ZERO_WG_A, wide = base_c + ZERO_WG_CODES * (ZERO_WG_C + ZERO_WG_E);
+    const uint32_t cols = wide + ZERO_WG_WIDE * ZERO_WG_A;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t pair = blockIdx.x >> 1;
     volatile int* dead = &sh.dead;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < ZERO_WG_STAGES; s++) {
-            mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.ready[s]), 16 / ZERO_WG_GROUPS);
-            mbar_init(smem_u32(&sh.empty[s]), 1);
-        }
+        for (int s = 0; s < ZERO_WG_STAGES * ZERO_WG_GROUPS; s++) mbar_init(smem_u32(&sh.rows[s]), 1);
+        for (int s = 0; s < ZERO_WG_CODES * ZERO_WG_GROUPS; s++) mbar_init(smem_u32(&sh.codes[s]), 1);
+        for (int s = 0; s < ZERO_WG_CODES; s++) mbar_init(smem_u32(&sh.read[s]), ZERO_WG_WIDENERS / 32 / ZERO_WG_GROUPS);
+        for (int s = 0; s < ZERO_WG_STAGES; s++) mbar_init(smem_u32(&sh.empty[s]), 1);
+        for (int s = 0; s < ZERO_WG_WIDE; s++) mbar_init(smem_u32(&sh.ready[s]), 2 * ZERO_WG_WIDENERS / 32 / ZERO_WG_GROUPS);
+        for (int s = 0; s < ZERO_WG_WIDE * ZERO_WG_GROUPS; s++) mbar_init(smem_u32(&sh.done[s]), 1);
         for (int s = 0; s < 2; s++) {
             mbar_init(smem_u32(&sh.sum_full[s]), 1);
             mbar_init(smem_u32(&sh.sum_empty[s]), 8);
-            mbar_init(smem_u32(&sh.col_full[s]), 8);
-            mbar_init(smem_u32(&sh.col_empty[s]), 4);
         }
+        mbar_init(smem_u32(&sh.col_full), ZERO_WG_WIDENERS / 32);
+        mbar_init(smem_u32(&sh.col_empty), 4);
         mbar_init(smem_u32(&sh.drain), 1);
         sh.dead = 0;
         fence_mbar_init();
@@ -435,52 +452,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
     WgradSegment g;
 
-    if (warp == 0) {
-        // ---- loads ----
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            int64_t issued = 0;
+    if (warp == 0 || warp == 2) {
+        // ---- loads: warp 0 dy rows, warp 2 codes and exponents ----
+        if (elected()) {
+            const bool codes = warp == 2;
+            const uint32_t ring = codes ? ZERO_WG_CODES : ZERO_WG_STAGES, bars = ring * ZERO_WG_GROUPS;
+            const uint32_t loads = smem_u32(codes ? sh.codes : sh.rows), frees = smem_u32(codes ? sh.read : sh.empty);
+            uint32_t n = 0, s = 0, l = 0, ph = 0;            // stages issued; slot, barrier, the slot's turn
             bool ok = true;
             for (int i = 0; ok && wgrad_segment(a, pair, i, g); i++) {
                 int64_t i0, j0;
                 wgrad_place(a, g.tile, i0, j0);
                 const int x = (int)(i0 + rank * 128), c = (int)j0 + rank * (wgrad_width(a, j0) / 2);
                 const int e = (int)a.wide + (c / 32 & ~15);
-                for (int t = g.s0; t < g.s1; t++) {
-                    if (issued >= ZERO_WG_STAGES && !pair_wait(smem_u32(&sh.empty[s]), ph ^ 1u, dead, a.err)) {
+                for (int y = g.s0 * ZERO_WG_TOK, end = g.s1 * ZERO_WG_TOK; y < end; y += ZERO_WG_TOK, n++) {
+                    if (n >= ring && !pair_wait(frees + 8 * s, ph ^ 1u, dead, a.err)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t at = base + s * ZERO_WG_STAGE, bar = smem_u32(&sh.full[s]);
-                    const int y = t * ZERO_WG_TOK;
-                    mbar_expect_tx(bar, ZERO_WG_A + ZERO_WG_C + ZERO_WG_E);
-                    tma_box(at, &map_y, x, y, bar);
-                    tma_box(at + 8192, &map_y, x + 64, y, bar);
-                    tma_box(at + ZERO_WG_A, &map_c, c, y, bar);
-                    tma_box(at + ZERO_WG_A + ZERO_WG_C, &map_e, e, y, bar);
-                    issued++;
-                    if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
+                    const uint32_t bar = loads + 8 * l;
+                    if (codes) {
+                        const uint32_t at = base_c + s * (ZERO_WG_C + ZERO_WG_E);
+                        mbar_expect_tx(bar, ZERO_WG_C + ZERO_WG_E);
+                        tma_box(at, &map_c, c, y, bar);
+                        tma_box(at + ZERO_WG_C, &map_e, e, y, bar);
+                    } else {
+                        const uint32_t at = base + s * ZERO_WG_A;
+                        mbar_expect_tx(bar, ZERO_WG_A);
+                        tma_box(at, &map_y, x, y, bar);
+                        tma_box(at + 8192, &map_y, x + 64, y, bar);
+                    }
+                    if (++s == ring) { s = 0; ph ^= 1u; }
+                    if (++l == bars) l = 0;
                 }
             }
-            // the last stages: their copies have landed and their products are done before
-            // this SM's shared memory is given back
-            for (int64_t q = issued > ZERO_WG_STAGES ? issued - ZERO_WG_STAGES : 0; q < issued; q++) {
-                const int k = (int)(q % ZERO_WG_STAGES);
-                const uint32_t parity = (uint32_t)(q / ZERO_WG_STAGES & 1);
-                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(smem_u32(&sh.full[k]), parity); it++) {
+            // before this SM's shared memory is given back: the last copies have landed, and the
+            // last products are done, as all barriers that they arrive on say
+            for (uint32_t q = n > ring ? n - ring : 0; q < n; q++) {
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(loads + 8 * (q % bars), q / bars & 1); it++) {
                 }
-                if (!*dead) pair_wait(smem_u32(&sh.empty[k]), parity, dead, a.err);
+                if (!codes && !*dead) pair_wait(frees + 8 * (q % ring), q / ring & 1, dead, a.err);
             }
+            const uint32_t places = ZERO_WG_WIDE * ZERO_WG_GROUPS;
+            for (uint32_t q = n > ZERO_WG_WIDE ? n - ZERO_WG_WIDE : 0; codes && q < n; q++)
+                if (!*dead) pair_wait(smem_u32(&sh.done[q % places]), q / places & 1, dead, a.err);
         }
     } else if (warp == 1) {
         // ---- products (the first SM's thread, for both) ----
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elected()) {
             // fp32 sums of fp16/bf16 operands, both with the contracted axis strided, 256 x width
             const uint32_t kind = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | 1u << 15 | 1u << 16 |
                                   (uint32_t)(ZERO_WG_TILE >> 4) << 24;
-            int s = 0, b = 0;
-            uint32_t ph = 0;
+            uint32_t s = 0, b = 0, f = 0, ph = 0;            // slot, place, the place's barrier, turn
             bool ok = true;
             int i = 0;
             for (; ok && wgrad_segment(a, pair, i, g); i++) {
@@ -494,19 +517,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                 const uint32_t what = kind | (uint32_t)(wgrad_width(a, j0) >> 3) << 17;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int t = g.s0; t < g.s1; t++) {
-                    if (!pair_wait(smem_u32(&sh.ready[s]), ph, dead, a.err)) {
+                    if (!pair_wait(smem_u32(&sh.ready[b]), ph, dead, a.err)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t da = operand(base + s * ZERO_WG_STAGE), db = operand(wide + b * ZERO_WG_A);
+                    const uint64_t da = operand(base + s * ZERO_WG_A), db = operand(wide + b * ZERO_WG_A);
 #pragma unroll
                     for (int q = 0; q < ZERO_WG_TOK / 16; q++)
                         product(tmem + acc * ZERO_WG_TILE, da + q * (2048 >> 4), db + q * (2048 >> 4), what,
                                 t > g.s0 || q > 0);
+                    commit_both(smem_u32(&sh.done[f]));
                     commit_both(smem_u32(&sh.empty[s]));
-                    if (++s == ZERO_WG_STAGES) { s = 0; ph ^= 1u; }
-                    if (++b == ZERO_WG_WIDE) b = 0;
+                    if (++s == ZERO_WG_STAGES) s = 0;
+                    if (++b == ZERO_WG_WIDE) { b = 0; ph ^= 1u; }
+                    if (++f == ZERO_WG_WIDE * ZERO_WG_GROUPS) f = 0;
                 }
                 if (ok) commit_both(smem_u32(&sh.sum_full[acc]));
             }
@@ -515,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             for (int q = i > 2 ? i - 2 : 0; ok && q < i; q++)
                 ok = pair_wait(smem_u32(&sh.sum_empty[q & 1]), (uint32_t)(q >> 1) & 1u, dead, a.err);
             if (*dead) {                                     // let the products in flight finish
-                commit_both(smem_u32(&sh.drain));
+                commit_both(smem_u32(&sh.drain), 1);
                 for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(smem_u32(&sh.drain), 0); it++) {
                 }
             }
@@ -527,15 +552,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
         // thread takes a token's block of 32 columns, and further tokens of the stage.  The
         // order in which it takes a block's halves (h) makes the eight lanes of each shared-
         // memory access fall on different 16-byte columns, reading and writing.
-        constexpr int GROUPS = ZERO_WG_GROUPS, TOKENS = ZERO_WG_TOK / GROUPS;
-        const int w = (threadIdx.x - 256) % (256 / GROUPS), group = (threadIdx.x - 256) / (256 / GROUPS);
+        constexpr int GROUPS = ZERO_WG_GROUPS, GROUP = ZERO_WG_WIDENERS / GROUPS, TOKENS = GROUP / 4, EACH = ZERO_WG_TOK / TOKENS;
+        const int w = (threadIdx.x - 256) % GROUP, group = (threadIdx.x - 256) / GROUP;
         const int blk = w & 3, tok = w >> 2, h = (blk >> 1) ^ (tok & 1);
         const uint32_t from = tok * 128 + blk * 32 + 16 * h, row = (blk >> 1) * 8192 + tok * 128;
         const uint32_t col = (uint32_t)(((blk & 1) * 4 + 2 * h) ^ (tok & 7)) * 16;
-        int s = group, b = group % ZERO_WG_WIDE, skip = group;
-        int f = (group - ZERO_WG_WIDE + ZERO_WG_STAGES) % ZERO_WG_STAGES;   // stage whose products free the place
-        uint32_t ph = 0, fph = group < ZERO_WG_WIDE;        // parity 1 of an unused barrier does not wait
-        // column sums of dy, for the tiles that need them: eight columns (chunk) of every fourth token
+        // this group's stage: its place, slots and barriers, and their turns; the stage whose
+        // products free the place
+        uint32_t b = group % ZERO_WG_WIDE, cs = group % ZERO_WG_CODES, cl = group, rs = group % ZERO_WG_STAGES, rl = group;
+        uint32_t cph = 0, rph = 0, fph = 0;
+        int f = group - ZERO_WG_WIDE;                       // below 0: the place is new
+        int skip = group;
+        // column sums of dy, for the tiles that need them: eight columns (chunk) of every few tokens
         const int chunk = w & 15, tok0 = w >> 4;
         int summed = 0;
         bool ok = true;
@@ -548,54 +576,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             for (int c = 0; c < 4; c++) total[c] = pack2(0.0f, 0.0f);
             const int half = wgrad_width(a, j0) / 2;          // this SM's columns
             const uint32_t eat = tok * 16 + (uint32_t)((j0 + rank * half) / 32 & 15) + blk;
+            const bool mine = blk * 32 < half;
             const int len = g.s1 - g.s0;
             int t = skip;
             for (; t < len; t += GROUPS) {
-                // The place is free once the stage ZERO_WG_WIDE before this one has been multiplied.
-                // This wait comes first: a group meets a stage's barrier every other time round
-                // (six stages, four groups), so it may look at `full` only when the use before
-                // is over, which those products tell; and that stage's `full`, which this group
-                // has seen, told that the use of `empty` before it was.
-                if (!pair_wait(smem_u32(&sh.empty[f]), fph, dead, a.err) ||
-                    !pair_wait(smem_u32(&sh.full[s]), ph, dead, a.err)) {
+                if (!pair_wait(smem_u32(&sh.codes[cl]), cph, dead, a.err)) {
                     ok = false;
                     break;
                 }
-                const uint32_t codes = base + s * ZERO_WG_STAGE + ZERO_WG_A, to = wide + b * ZERO_WG_A + row;
-                uint32_t e[GROUPS], q[GROUPS][2][4];
+                const uint32_t codes = base_c + cs * (ZERO_WG_C + ZERO_WG_E), to = wide + b * ZERO_WG_A + row;
+                uint32_t e[EACH], q[EACH][2][4];
+                if (mine) {
 #pragma unroll
-                for (int u = 0; u < GROUPS; u++) {
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[u]) : "r"(codes + ZERO_WG_C + eat + u * TOKENS * 16));
+                    for (int u = 0; u < EACH; u++) {
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[u]) : "r"(codes + ZERO_WG_C + eat + u * TOKENS * 16));
 #pragma unroll
-                    for (int c = 0; c < 2; c++)
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(q[u][c][0]), "=r"(q[u][c][1]), "=r"(q[u][c][2]), "=r"(q[u][c][3])
-                                     : "r"(codes + u * TOKENS * 128 + (from ^ 16 * c)));
+                        for (int c = 0; c < 2; c++)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(q[u][c][0]), "=r"(q[u][c][1]), "=r"(q[u][c][2]), "=r"(q[u][c][3])
+                                         : "r"(codes + u * TOKENS * 128 + (from ^ 16 * c)));
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.read[cs]));
+                if (f >= 0 && !pair_wait(smem_u32(&sh.done[f]), fph, dead, a.err)) {
+                    ok = false;
+                    break;
+                }
+                if (mine) {
 #pragma unroll
-                for (int u = 0; u < GROUPS; u++) {
-                    const uint32_t sc = code_scale<DT>(e[u]);
+                    for (int u = 0; u < EACH; u++) {
+                        const uint32_t sc = code_scale<DT>(e[u]);
 #pragma unroll
-                    for (int c = 0; c < 2; c++)
+                        for (int c = 0; c < 2; c++)
 #pragma unroll
-                        for (int p = 0; p < 2; p++) {          // eight codes -> 16 bytes
-                            uint32_t r[4];
+                            for (int p = 0; p < 2; p++) {          // eight codes -> 16 bytes
+                                uint32_t r[4];
 #pragma unroll
-                            for (int d = 0; d < 4; d++) {
-                                const uint32_t x = q[u][c][2 * p + d / 2];
-                                r[d] = widen_codes<DT>(DT == 1 ? x : x ^ 0x80808080u, d & 1 ? 0x4342 : 0x4140, sc);
+                                for (int d = 0; d < 4; d++) {
+                                    const uint32_t x = q[u][c][2 * p + d / 2];
+                                    r[d] = widen_codes<DT>(DT == 1 ? x : x ^ 0x80808080u, d & 1 ? 0x4342 : 0x4140, sc);
+                                }
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                             ::"r"(to + u * TOKENS * 128 + (col ^ (2 * c + p) * 16)), "r"(r[0]), "r"(r[1]),
+                                             "r"(r[2]), "r"(r[3]) : "memory");
                             }
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                                         ::"r"(to + u * TOKENS * 128 + (col ^ (2 * c + p) * 16)), "r"(r[0]), "r"(r[1]),
-                                         "r"(r[2]), "r"(r[3]) : "memory");
-                        }
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (!pair_wait(smem_u32(&sh.rows[rl]), rph, dead, a.err)) {
+                    ok = false;
+                    break;
+                }
                 if (sums) {
-                    const uint32_t at = base + s * ZERO_WG_STAGE + (chunk >> 3) * 8192;
-                    constexpr int EACH = 256 / GROUPS / 16;    // tokens a step
+                    const uint32_t at = base + rs * ZERO_WG_A + (chunk >> 3) * 8192;
 #pragma unroll 4
-                    for (int k = tok0; k < ZERO_WG_TOK; k += EACH) {
+                    for (int k = tok0; k < ZERO_WG_TOK; k += GROUP / 16) {
                         uint32_t v[4];
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -609,32 +645,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) arrive_first(smem_u32(&sh.ready[s]));
-                s += GROUPS;
-                if (s >= ZERO_WG_STAGES) { s -= ZERO_WG_STAGES; ph ^= 1u; }
-                f += GROUPS;
-                if (f >= ZERO_WG_STAGES) { f -= ZERO_WG_STAGES; fph ^= 1u; }
+                if (lane == 0) arrive_first(smem_u32(&sh.ready[b]));
                 b = (b + GROUPS) % ZERO_WG_WIDE;
+                f += GROUPS;
+                if (f >= ZERO_WG_WIDE * GROUPS) { f -= ZERO_WG_WIDE * GROUPS; fph ^= 1u; }
+                cs = (cs + GROUPS) % ZERO_WG_CODES;
+                cl += GROUPS;
+                if (cl >= ZERO_WG_CODES * ZERO_WG_GROUPS) { cl -= ZERO_WG_CODES * ZERO_WG_GROUPS; cph ^= 1u; }
+                rs = (rs + GROUPS) % ZERO_WG_STAGES;
+                rl += GROUPS;
+                if (rl >= ZERO_WG_STAGES * ZERO_WG_GROUPS) { rl -= ZERO_WG_STAGES * ZERO_WG_GROUPS; rph ^= 1u; }
             }
             skip = t - len;
             if (sums && ok) {
                 // the two lanes of a warp with the same columns, then a row of 128 from each warp
-                const int buf = summed & 1;
-                if (summed >= 2 && !pair_wait(smem_u32(&sh.col_empty[buf]), (uint32_t)((summed >> 1) - 1) & 1u, dead, a.err)) break;
+                if (summed >= 1 && !pair_wait(smem_u32(&sh.col_empty), (uint32_t)(summed - 1) & 1u, dead, a.err)) break;
                 float v[8];
 #pragma unroll
                 for (int c = 0; c < 4; c++) unpack2(total[c], v[2 * c], v[2 * c + 1]);
 #pragma unroll
                 for (int c = 0; c < 8; c++) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], 16);
                 if (lane < 16) {
-                    const uint32_t to = cols + buf * ZERO_WG_SUMS + (warp - 8) * 512 + chunk * 32;
+                    const uint32_t to = cols + (warp - 8) * 512 + chunk * 32;
 #pragma unroll
                     for (int c = 0; c < 8; c += 4)
                         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * c), "f"(v[c]), "f"(v[c + 1]),
                                      "f"(v[c + 2]), "f"(v[c + 3]) : "memory");
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.col_full[buf]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.col_full));
                 summed++;
             }
         }
@@ -655,18 +694,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             float* kept = part ? part : a.slots + (int64_t)(2 * ZERO_WG_PAIRS + pair) * ZERO_WG_SLOT;
             if (g.first) sum = part ? 0.0f : column_sum(a, r);
             if (adds_sums(a, j0)) {
-                const int buf = summed & 1;
-                have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.col_full[buf]), (uint32_t)(summed >> 1) & 1u, dead, a.err)) && have;
+                have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.col_full), (uint32_t)summed & 1u, dead, a.err)) && have;
 #pragma unroll
-                for (int w = 0; w < 8; w++) {
+                for (int w = 0; w < ZERO_WG_WIDENERS / 32; w++) {
                     float x;
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x)
-                                 : "r"(cols + buf * ZERO_WG_SUMS + w * 512 + ((warp - 4) * 32 + lane) * 4));
+                                 : "r"(cols + w * 512 + ((warp - 4) * 32 + lane) * 4));
                     sum += x;
                 }
                 if (!have) sum = __uint_as_float(0x7FC00000u);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.col_empty[buf]));
+                if (lane == 0) mbar_arrive(smem_u32(&sh.col_empty));
                 summed++;
             }
             if (g.last && part && adds_sums(a, j0))

@@ -260,6 +260,14 @@ def test_wgrad_workspace_serves_calls_of_other_sizes(env):
         seen[s] = (dw, db)
 
 
+@pytest.mark.parametrize("tokens,n,k,grad,affine", [(300, 4200, 5200, R.BF16, False), (130, 5000, 6272, R.BF16, True),
+                                                    (1020, 2500, 9000, R.FP32, False)])
+def test_wgrad_of_many_tiles(env, tokens, n, k, grad, affine):
+    """More tiles than the device takes at a time, so that buffers stay full while a tile is written
+    out and the next one's operands wait."""
+    wgrad_case(env, tokens, n, k, R.BF16, grad, affine=affine)
+
+
 @pytest.mark.parametrize("tokens,n,k,grad", [(30011, 776, 771, R.FP32), (8192, 1024, 1024, R.BF16), (700, 40, 100, R.BF16)])
 def test_wgrad_gives_equal_bits_over_many_calls(env, tokens, n, k, grad):
     """Loads that land in another order must not be taken for one another: the same call, with other

@@ -293,6 +293,10 @@ static __device__ __forceinline__ void arrive_first(uint32_t bar)
     asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
                  " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
 }
+// A lane to arrive for the warp, known once every lane has its x.  An arrival that hands a
+// buffer back must not be made while loads from it are under way, and the barrier unit does not
+// wait for loads before it: x is made of the loaded values.
+static __device__ __forceinline__ int lane_with(uint32_t x) { return __any_sync(0xFFFFFFFFu, x == 0) ? 0 : 1; }
 // Bounded wait: false when it gave up (here or in another warp of this SM).
 static __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
@@ -585,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     break;
                 }
                 const uint32_t codes = base_c + cs * (ZERO_WG_C + ZERO_WG_E), to = wide + b * ZERO_WG_A + row;
-                uint32_t e[EACH], q[EACH][2][4];
+                uint32_t e[EACH], q[EACH][2][4], all = 0;
                 if (mine) {
 #pragma unroll
                     for (int u = 0; u < EACH; u++) {
@@ -597,8 +601,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                                          : "r"(codes + u * TOKENS * 128 + (from ^ 16 * c)));
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.read[cs]));
+                if (mine)
+#pragma unroll
+                    for (int u = 0; u < EACH; u++) all |= e[u] | q[u][0][0] | q[u][1][0];
+                if (lane == lane_with(all)) mbar_arrive(smem_u32(&sh.read[cs]));
                 if (f >= 0 && !pair_wait(smem_u32(&sh.done[f]), fph, dead, a.err)) {
                     ok = false;
                     break;
@@ -644,8 +650,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) arrive_first(smem_u32(&sh.ready[b]));
+                uint32_t last = 0;
+                if (sums)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        float lo, hi;
+                        unpack2(total[c], lo, hi);
+                        last |= __float_as_uint(lo);
+                    }
+                if (lane == lane_with(last)) arrive_first(smem_u32(&sh.ready[b]));
                 b = (b + GROUPS) % ZERO_WG_WIDE;
                 f += GROUPS;
                 if (f >= ZERO_WG_WIDE * GROUPS) { f -= ZERO_WG_WIDE * GROUPS; fph ^= 1u; }
@@ -703,8 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     sum += x;
                 }
                 if (!have) sum = __uint_as_float(0x7FC00000u);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.col_empty));
+                if (lane == lane_with(__float_as_uint(sum))) mbar_arrive(smem_u32(&sh.col_empty));
                 summed++;
             }
             if (g.last && part && adds_sums(a, j0))

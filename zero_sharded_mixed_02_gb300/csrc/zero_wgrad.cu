@@ -50,8 +50,9 @@ namespace zero {
 #define ZERO_WG_C 8192
 #define ZERO_WG_E 1024
 #define ZERO_WG_SUMS (ZERO_WG_WIDENERS / 32 * 512)
+#define ZERO_WG_OUT 2048                    // rows that an output warp writes
 #define ZERO_WG_SMEM \
-    (ZERO_WG_STAGES * ZERO_WG_A + ZERO_WG_CODES * (ZERO_WG_C + ZERO_WG_E) + ZERO_WG_WIDE * ZERO_WG_A + ZERO_WG_SUMS + 1024)
+    (ZERO_WG_STAGES * ZERO_WG_A + ZERO_WG_CODES * (ZERO_WG_C + ZERO_WG_E) + ZERO_WG_WIDE * ZERO_WG_A + ZERO_WG_SUMS + 4 * ZERO_WG_OUT + 1024)
 #define ZERO_WG_SLOT (ZERO_WG_TILE * (ZERO_WG_TILE + 1))  // floats of a part: its sums, its rows' sums of dy
 
 struct WgradArgs {
@@ -177,11 +178,11 @@ static __device__ __forceinline__ void eight(const uint16_t* p, float (&w)[8])
     widen2<DT>(q.w, w[6], w[7]);
 }
 
-// N columns from j of row i; s the row's column sum of dy.
+// N columns from j of a row: times the norm's weight, plus its bias times s, the row's column
+// sum of dy.
 template <int DT, int N>
-static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, int64_t j, float (&v)[N], float s)
+static __device__ __forceinline__ void affine(const WgradArgs& a, int64_t j, float (&v)[N], float s)
 {
-    if (i >= a.n || j >= a.k) return;
     const int m = a.k - j < N ? (int)(a.k - j) : N;
     if ((a.scale || a.shift) && a.vec_s && m == N) {
 #pragma unroll
@@ -206,6 +207,15 @@ static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, in
                 if (a.shift) v[c] = __fmaf_rn(s, widen1<DT>(__ldg(a.shift + j + c)), v[c]);
             }
     }
+}
+
+// N columns from j of row i, a lane its own row.
+template <int DT, int N>
+static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, int64_t j, float (&v)[N], float s)
+{
+    if (i >= a.n || j >= a.k) return;
+    const int m = a.k - j < N ? (int)(a.k - j) : N;
+    affine<DT, N>(a, j, v, s);
     const int64_t at = i * a.ldw + j;
     if (a.vec && m == N) {
         if (a.grad_dtype == 2) {
@@ -243,6 +253,117 @@ static __device__ __forceinline__ void put_row(const WgradArgs& a, int64_t i, in
 #pragma unroll
     for (int c = 0; c < N; c++)
         if (c < m) put_grad(a.dw, at + c, v[c], a.grad_dtype, a.accumulate);
+}
+
+// A warp's 32 rows of 64 bytes (of 16 or 32 columns from j) between dw and shared memory, a lane
+// a column.  16-byte word q of row r lies at q ^ (r >> 1 & 3), so that lanes that each take a row
+// meet all banks too.
+template <bool IN>
+static __device__ __forceinline__ void move_rows(const WgradArgs& a, int64_t i0, int64_t j, uint32_t stage)
+{
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    if (a.grad_dtype == 2) {
+#pragma unroll 8
+        for (int p = 0; p < 16; p++) {
+            const int r = 2 * p + half, c = lane & 15;
+            const uint32_t s = stage + r * 64 + ((c >> 2) ^ (r >> 1 & 3)) * 16 + (c & 3) * 4;
+            float* g = static_cast<float*>(a.dw) + (i0 + r) * a.ldw + j + c;
+            if (i0 + r >= a.n || j + c >= a.k) continue;
+            if (IN) {
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(s), "f"(*g) : "memory");
+            } else {
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s));
+                *g = x;
+            }
+        }
+        return;
+    }
+#pragma unroll 8
+    for (int r = 0; r < 32; r++) {
+        const uint32_t s = stage + r * 64 + ((lane >> 3) ^ (r >> 1 & 3)) * 16 + (lane & 7) * 2;
+        uint16_t* g = static_cast<uint16_t*>(a.dw) + (i0 + r) * a.ldw + j + lane;
+        if (i0 + r >= a.n || j + lane >= a.k) continue;
+        if (IN) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(s), "h"(*g) : "memory");
+        } else {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(s));
+            *g = x;
+        }
+    }
+}
+
+// put_row() for rows of dw that are not aligned to vectors: 32 columns from j of the warp's rows
+// from i0, through 2 KB of shared memory, so that an access of the warp is a run of a row and not
+// an element of each of 32 rows (4095 x 4095 over 128 tokens: 171 -> 40 us, 440 -> 134 us when
+// added to what is there).  Aligned rows are faster written by the lanes that have them: 21
+// against 31 us at 4096 x 4096.
+template <int DT>
+static __device__ __forceinline__ void put_rows(const WgradArgs& a, int64_t i0, int64_t j, float (&v)[32], float s, uint32_t stage)
+{
+    const int lane = threadIdx.x & 31;
+    if (j >= a.k || i0 >= a.n) return;                       // all lanes
+    if (i0 + lane < a.n) affine<DT, 32>(a, j, v, s);
+    const uint32_t own = stage + lane * 64;
+    auto word = [&](int q) { return own + (q ^ (lane >> 1 & 3)) * 16; };
+    auto get = [&](int q) {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(word(q)));
+        return x;
+    };
+    auto put = [&](int q, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(word(q)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+    };
+    if (a.grad_dtype == 2) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (j + 16 * h >= a.k) break;
+            if (a.accumulate) {
+                move_rows<true>(a, i0, j + 16 * h, stage);
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const uint4 x = get(q);
+                    v[16 * h + 4 * q] += __uint_as_float(x.x);
+                    v[16 * h + 4 * q + 1] += __uint_as_float(x.y);
+                    v[16 * h + 4 * q + 2] += __uint_as_float(x.z);
+                    v[16 * h + 4 * q + 3] += __uint_as_float(x.w);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                put(q, __float_as_uint(v[16 * h + 4 * q]), __float_as_uint(v[16 * h + 4 * q + 1]),
+                    __float_as_uint(v[16 * h + 4 * q + 2]), __float_as_uint(v[16 * h + 4 * q + 3]));
+            __syncwarp();
+            move_rows<false>(a, i0, j + 16 * h, stage);
+            __syncwarp();
+        }
+        return;
+    }
+    if (a.accumulate) {
+        move_rows<true>(a, i0, j, stage);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint4 x = get(q);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float lo, hi;
+                widen2<DT>(w[e], lo, hi);
+                v[8 * q + 2 * e] += lo;
+                v[8 * q + 2 * e + 1] += hi;
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        put(q, narrow2<DT>(v[8 * q], v[8 * q + 1]), narrow2<DT>(v[8 * q + 2], v[8 * q + 3]),
+            narrow2<DT>(v[8 * q + 4], v[8 * q + 5]), narrow2<DT>(v[8 * q + 6], v[8 * q + 7]));
+    __syncwarp();
+    move_rows<false>(a, i0, j, stage);
+    __syncwarp();
 }
 
 // Whether a tile adds its rows' sums of dy: for db, in the first column of tiles, unless
@@ -744,7 +865,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                         v[4 * e + 3] += p.w;
                     }
                 if (g.last && !part) {
-                    put_row<DT, 32>(a, r, j0 + c * 32, v, sum);
+                    if (a.vec) put_row<DT, 32>(a, r, j0 + c * 32, v, sum);
+                    else put_rows<DT>(a, r - lane, j0 + c * 32, v, sum, cols + ZERO_WG_SUMS + (warp - 4) * ZERO_WG_OUT);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e++) o[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);

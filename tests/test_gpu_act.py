@@ -260,6 +260,14 @@ def test_wgrad_workspace_serves_calls_of_other_sizes(env):
         seen[s] = (dw, db)
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 31, 32, 33, 64, 65])
+@pytest.mark.parametrize("n,k,pad,shift", [(64, 128, 0, 0), (130, 257, 1, 1), (1, 33, 3, 1), (768, 768, 0, 0)])
+@pytest.mark.parametrize("dtype,grad,accumulate", [(R.BF16, R.BF16, 0), (R.FP16, R.FP32, 1), (R.FP16, R.FP16, 1)])
+def test_wgrad_of_few_tokens(env, tokens, n, k, pad, shift, dtype, grad, accumulate):
+    wgrad_case(env, tokens, n, k, dtype, grad, pad=pad, shift=shift, affine=tokens % 2 == 1, dw_pad=pad, dw_shift=shift,
+               accumulate=accumulate)
+
+
 @pytest.mark.parametrize("tokens,n,k,grad,affine", [(300, 4200, 5200, R.BF16, False), (130, 5000, 6272, R.BF16, True),
                                                     (1020, 2500, 9000, R.FP32, False)])
 def test_wgrad_of_many_tiles(env, tokens, n, k, grad, affine):

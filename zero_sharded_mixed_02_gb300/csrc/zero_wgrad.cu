@@ -42,6 +42,9 @@ namespace zero {
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
 #define ZERO_WG_RUN 64                      // stages an accumulator adds for an fp32 gradient
+#define ZERO_WG_FEW 64                      // most tokens that k_wgrad_few takes,
+#define ZERO_WG_FEW_WORK (60ll << 20)       // and most products
+#define ZERO_WG_FEW_TOK 32                  // tokens it adds at a time
 #define ZERO_WG_RANGES 32                   // most token ranges that k_wgrad_columns adds
 
 // bytes of a stage in one SM: dy rows, codes, exponents; and of widened codes (as dy rows); the
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ Wgra
 // A first pass over dy where one is needed: its columns added over ZERO_WG_RANGES token
 // ranges (blockIdx.y) for the norm's bias, which every tile's output needs (adding them in
 // every tile would read each dy operand from shared memory once more, the product kernel's
-// bound: 23 us more at 8192 x 6400 x 1600, this pass xx us), and rows that are not aligned to
+// bound: 23 us more at 8192 x 6400 x 1600, this pass 18 us), and rows that are not aligned to
 // 16 bytes copied to rows that are, so that TMA can read them.  A warp takes 256 columns.
 template <int DT, bool COPY>
 __global__ void __launch_bounds__(256) k_wgrad_columns(const __grid_constant__ WgradArgs a, uint16_t* out, int64_t pitch)
@@ -970,6 +973,117 @@ __global__ void __launch_bounds__(256) k_wgrad_columns(const __grid_constant__ W
     float v = 0.0f;
     for (int w = 0; w < 8; w++) v += part[w][threadIdx.x];
     if (i0 + threadIdx.x < a.n) a.sums[blockIdx.y * a.n + i0 + threadIdx.x] = v;
+}
+
+// ---- few tokens ----------------------------------------------------------------------
+// A small product of few tokens is a matter of latency, of which the machinery above has 10 us:
+// here a block takes 64 rows and 128 columns of dw, widens the tokens' codes and gradients to
+// fp32 in shared memory, and each thread adds 8 rows of 4 columns in registers.  dy is read
+// element by element, in any alignment.  768 x 768: 4.1 us for 16 tokens and 8.8 for 64, against
+// 10.2; 1600 x 1600: 7.9 for 16 and 17.7 for 64, against 10; 4096 x 4096: 18 for one and 28 for
+// 16, against 20.  So it is taken for up to ZERO_WG_FEW tokens and ZERO_WG_FEW_WORK products.
+template <int DT>
+__global__ void __launch_bounds__(256) k_wgrad_few(const __grid_constant__ WgradArgs a)
+{
+    __shared__ __align__(16) float ys[ZERO_WG_FEW_TOK][64], xs[ZERO_WG_FEW_TOK][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i0 = (int64_t)blockIdx.x * 64, stride = act_stride(a.k);
+    for (int64_t j0 = (int64_t)blockIdx.y * 128; j0 < a.k; j0 += (int64_t)gridDim.y * 128) {
+        f32x2_t v[8][2];
+        float sum = 0.0f;                                   // lane r (of eight): row r's sum of dy
+#pragma unroll
+        for (int r = 0; r < 8; r++) v[r][0] = v[r][1] = pack2(0.0f, 0.0f);
+        for (int t0 = 0; t0 < (int)a.tokens; t0 += ZERO_WG_FEW_TOK) {
+            const int m = (int)a.tokens - t0 < ZERO_WG_FEW_TOK ? (int)a.tokens - t0 : ZERO_WG_FEW_TOK;
+            __syncthreads();                                // the previous tokens' reads are done
+            for (int e = threadIdx.x; e < m * 64; e += 256) {
+                const int t = e >> 6, c = e & 63;
+                ys[t][c] = i0 + c < a.n ? widen1<DT>(__ldg(a.dy + (t0 + t) * a.ldy + i0 + c)) : 0.0f;
+            }
+            for (int e = threadIdx.x; e < m * 16; e += 256) {
+                const int t = e >> 4;
+                const int64_t j = j0 + (e & 15) * 8;
+                f32x2_t x[4];
+#pragma unroll
+                for (int c = 0; c < 4; c++) x[c] = pack2(0.0f, 0.0f);
+                if (j < a.wide) {
+                    const uint8_t* p = a.ckpt + (t0 + t) * stride;
+                    const uint32_t b = __ldg(p + a.wide + (j >> 5));
+                    act_values(__ldg(reinterpret_cast<const uint2*>(p + j)), b, x);
+                    if (DT == 0 && (b < 103 || b > 136))    // fp16 has no such block
+                        for (int c = 0; c < 4; c++) x[c] = both(__uint_as_float(0x7FC00000u));
+                }
+                float4* o = reinterpret_cast<float4*>(&xs[t][(e & 15) * 8]);
+                float w[8];
+#pragma unroll
+                for (int c = 0; c < 4; c++) unpack2(x[c], w[2 * c], w[2 * c + 1]);
+                o[0] = make_float4(w[0], w[1], w[2], w[3]);
+                o[1] = make_float4(w[4], w[5], w[6], w[7]);
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int t = 0; t < m; t++) {
+                const float4 x = *reinterpret_cast<const float4*>(&xs[t][4 * lane]);
+                const f32x2_t x0 = pack2(x.x, x.y), x1 = pack2(x.z, x.w);
+                const float4 y0 = *reinterpret_cast<const float4*>(&ys[t][8 * warp]);
+                const float4 y1 = *reinterpret_cast<const float4*>(&ys[t][8 * warp + 4]);
+                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int r = 0; r < 8; r++) {
+                    v[r][0] = fma2(both(y[r]), x0, v[r][0]);
+                    v[r][1] = fma2(both(y[r]), x1, v[r][1]);
+                }
+            }
+            for (int t = 0; t < m; t++) sum += ys[t][8 * warp + (lane & 7)];
+        }
+        const int64_t j = j0 + 4 * lane;
+        if (a.db && j0 == 0 && lane < 8 && i0 + 8 * warp + lane < a.n)
+            put_grad(a.db, i0 + 8 * warp + lane, sum, a.grad_dtype, a.accumulate);
+        float scale[4], shift[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            scale[c] = a.scale && j + c < a.k ? widen1<DT>(__ldg(a.scale + j + c)) : 1.0f;
+            shift[c] = a.shift && j + c < a.k ? widen1<DT>(__ldg(a.shift + j + c)) : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 8; r++) {
+            const float s = __shfl_sync(0xFFFFFFFFu, sum, r);
+            const int64_t i = i0 + 8 * warp + r;
+            if (i >= a.n || j >= a.k) continue;
+            float w[4];
+            unpack2(v[r][0], w[0], w[1]);
+            unpack2(v[r][1], w[2], w[3]);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                if (a.scale) w[c] *= scale[c];
+                if (a.shift) w[c] = __fmaf_rn(s, shift[c], w[c]);
+            }
+            const int64_t at = i * a.ldw + j;
+            if (!a.vec || j + 4 > a.k) {
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    if (j + c < a.k) put_grad(a.dw, at + c, w[c], a.grad_dtype, a.accumulate);
+            } else if (a.grad_dtype == 2) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
+                if (a.accumulate) {
+                    const float4 p = *o;
+                    w[0] += p.x; w[1] += p.y; w[2] += p.z; w[3] += p.w;
+                }
+                *o = make_float4(w[0], w[1], w[2], w[3]);
+            } else {
+                uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at);
+                if (a.accumulate) {
+                    const uint2 p = *o;
+                    float lo, hi;
+                    widen2<DT>(p.x, lo, hi);
+                    w[0] += lo; w[1] += hi;
+                    widen2<DT>(p.y, lo, hi);
+                    w[2] += lo; w[3] += hi;
+                }
+                *o = make_uint2(narrow2<DT>(w[0], w[1]), narrow2<DT>(w[2], w[3]));
+            }
+        }
+    }
 }
 
 }  // namespace zero
@@ -1106,6 +1220,13 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.vec_s = aligned_to(col_scale, 16) && aligned_to(col_shift, 16);
     const bool half = dtype == ZERO_FP16;
     void* args[] = {&a, nullptr, nullptr, nullptr};
+    if (tokens <= ZERO_WG_FEW && tokens * n * k <= ZERO_WG_FEW_WORK) {
+        const int64_t wide = up(k, 128);
+        return launch(half ? (const void*)k_wgrad_few<0> : (const void*)k_wgrad_few<1>,
+                      dim3((unsigned)up(n, 64), (unsigned)(wide < 32768 ? wide : 32768)), 256, 0, args, stream)
+                   ? ZERO_OK
+                   : ZERO_ECUDA;
+    }
     a.pairs = device_pairs();
     if (a.pairs == 0 || !encode()) return ZERO_ECUDA;
     a.steps = (int)steps_of(tokens);

@@ -241,6 +241,18 @@ def test_backward_strides(env, pad, shift, res):  # noqa: F811
     run_backward(env, params(21, 200, R.RMS, R.LAYER, group=4), R.BF16, res, R.BF16, pad, shift)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 9), (5, 249), (11, 250), (700, 255), (3, 4081), (40, 4088), (9, 4090), (3, 4096), (2, 8177),
+                                       (2, 8190), (2000, 33)])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (0, 5), (7, 7)])
+@pytest.mark.parametrize("dtype,res,post,pre,bias", [(R.BF16, R.BF16, 1, 1, False), (R.FP16, R.FP32, 2, 2, True),
+                                                     (R.FP16, R.FP16, 0, 2, True), (R.BF16, R.FP32, 0, 1, False)])
+def test_backward_rows_of_any_alignment(env, rows, cols, pad, shift, dtype, res, post, pre, bias):  # noqa: F811
+    """Rows whose words and chunks do not coincide: every shift, rows of one warp, rows that fill
+    the threads, and the matrices' first and last words."""
+    run_backward(env, params(rows, cols, post, pre, group=3, bias=bias), dtype, res, R.FP32, pad=pad, shift=shift,
+                 in_place=rows == 40)
+
+
 @pytest.mark.parametrize("accumulate", [0, 1])
 def test_backward_accumulates(env, accumulate):  # noqa: F811
     run_backward(env, params(90, 160, R.LAYER, R.RMS, group=40), R.FP16, R.FP16, R.FP16, accumulate=accumulate)

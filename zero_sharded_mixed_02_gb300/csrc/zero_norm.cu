@@ -338,10 +338,22 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         const bool whole = d.cols % 8 == 0 && dy && (!dh_out || whole_rows(dh_out, lddho, d.res_dtype)) &&
                            (!dx || a.vec_dx) && (!dh || whole_rows(dh, lddh, d.res_dtype)) && a.vec_dy && a.vec_w &&
                            (!d.gate || a.vec_g);
+        // other rows can be copied ahead too if their words, one more than chunks, have threads
+        bool copied = !whole && dx && dy;
+        if (copied) {
+            int cv = 1, ct = 32;
+            row_shape(((2 * a.cols + 13) / 16 + 1) * 8, cv, ct);
+            copied = cv <= 2 && (int64_t)cv * ct * norm_ring_bytes(d.res_dtype) + 18 * 1024 <= 227 * 1024 &&
+                     (d.pre == ZERO_NORM_LAYER || !two) && (d.post == ZERO_NORM_NONE || d.post == d.pre);
+            if (copied) {
+                v = cv;
+                threads = ct;
+            }
+        }
         int smem = 0;
         const void* fn = d.dtype == ZERO_FP16
-                             ? norm_backward_fp16(d.res_dtype, v, d.post, d.pre, whole, two, smem)
-                             : norm_backward_bf16(d.res_dtype, v, d.post, d.pre, whole, two, smem);
+                             ? norm_backward_fp16(d.res_dtype, v, d.post, d.pre, whole, copied, two, smem)
+                             : norm_backward_bf16(d.res_dtype, v, d.post, d.pre, whole, copied, two, smem);
         smem *= threads;
         int sms = 0;
         blocks = resident(fn, threads, smem, sms);

@@ -3,11 +3,11 @@
 
 namespace zero {
 
-const void* norm_backward_bf16_fp32(int, int v, int post, int pre, bool whole, bool& two, int& smem)
+const void* norm_backward_bf16_fp32(int, int v, int post, int pre, bool whole, bool copied, bool& two, int& smem)
 {
-    return v == 1   ? norm_backward_of<1, 2, 1>(post, pre, whole, two, smem)
-           : v == 2 ? norm_backward_of<1, 2, 2>(post, pre, whole, two, smem)
-                    : norm_backward_of<1, 2, 4>(post, pre, whole, two, smem);
+    return v == 1   ? norm_backward_of<1, 2, 1>(post, pre, whole, copied, two, smem)
+           : v == 2 ? norm_backward_of<1, 2, 2>(post, pre, whole, copied, two, smem)
+                    : norm_backward_of<1, 2, 4>(post, pre, whole, copied, two, smem);
 }
 
 }  // namespace zero

@@ -193,6 +193,21 @@ static __device__ __forceinline__ uint32_t load_bits(const void* p, uint32_t i)
     return T == 2 ? __ldg(static_cast<const uint32_t*>(p) + i) : (uint32_t)__ldg(static_cast<const uint16_t*>(p) + i);
 }
 
+// Sixteen bytes from `sh` (even) of the 32 in q and n.
+static __device__ __forceinline__ uint4 shifted(uint4 q, uint4 n, uint32_t sh)
+{
+    const uint32_t w[7] = {q.x, q.y, q.z, q.w, n.x, n.y, n.z};
+    uint32_t x[6], y[5];
+#pragma unroll
+    for (int i = 0; i < 5; i++) x[i] = sh & 8 ? w[i + 2] : w[i];
+    x[5] = sh & 8 ? n.w : w[5];
+#pragma unroll
+    for (int i = 0; i < 5; i++) y[i] = sh & 4 ? x[i + 1] : x[i];
+    const uint32_t bits = (sh & 2) * 8;
+    return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
+                      __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
+}
+
 // Columns i .. i+8 of a row, those at or past n (of the eight) read as 0.  Unless `vec`, a
 // lane has columns lane + 32 k of its warp's 256, for unstage().
 template <int T, bool WHOLE = false>
@@ -309,6 +324,11 @@ static __device__ __forceinline__ void store_chunk(const void* row, uint32_t i, 
     if ((WHOLE || vec) && n >= 8) {
         uint4* o = T == 2 ? reinterpret_cast<uint4*>(static_cast<float*>(p) + i)
                           : reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i);
+        if (T == 2 && (reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+            asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "f"(x[0]), "f"(x[1]),
+                         "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]) : "memory");
+            return;
+        }
         __stcs(o, q[0]);
         if (T == 2) __stcs(o + 1, q[T == 2]);
     } else if (!WHOLE && vec) {

@@ -728,21 +728,6 @@ template <int RT, int V, bool ANY> struct NormRing {
 // With rows of any alignment: bytes of a thread and chunk.
 static inline int64_t norm_ring_bytes(int res) { return res == 2 ? NormRing<2, 1, true>::bytes : NormRing<0, 1, true>::bytes; }
 
-// Sixteen bytes from `sh` (even, the same in all threads) of the 32 in q and n.
-static __device__ __forceinline__ uint4 shifted(uint4 q, uint4 n, uint32_t sh)
-{
-    const uint32_t w[7] = {q.x, q.y, q.z, q.w, n.x, n.y, n.z};
-    uint32_t x[6], y[5];
-#pragma unroll
-    for (int i = 0; i < 5; i++) x[i] = sh & 8 ? w[i + 2] : w[i];
-    x[5] = sh & 8 ? n.w : w[5];
-#pragma unroll
-    for (int i = 0; i < 5; i++) y[i] = sh & 4 ? x[i + 1] : x[i];
-    const uint32_t bits = (sh & 2) * 8;
-    return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
-                      __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
-}
-
 template <int DT, int RT, int V, int POST, int PRE, bool TWO, bool ANY>
 __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 : 1)
     k_norm_backward_whole(const __grid_constant__ NormBwdArgs a)

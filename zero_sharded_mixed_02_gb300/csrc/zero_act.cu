@@ -127,9 +127,8 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_load(const __grid_constant
 template <int T>
 __global__ void __launch_bounds__(ZERO_THREADS) k_act_save_any(const __grid_constant__ ActArgs a)
 {
-    constexpr int WORDS = T == 2 ? 3 : 2, SIZE = T == 2 ? 4 : 2;
     const uint32_t first = blockIdx.x * (ZERO_ACT_UNROLL * ZERO_THREADS) + threadIdx.x;
-    uint4 q[ZERO_ACT_UNROLL][WORDS];
+    Words<T> w[ZERO_ACT_UNROLL];
     uint32_t sh[ZERO_ACT_UNROLL];
     int64_t row[ZERO_ACT_UNROLL];
     int col[ZERO_ACT_UNROLL];
@@ -138,43 +137,12 @@ __global__ void __launch_bounds__(ZERO_THREADS) k_act_save_any(const __grid_cons
         const uint32_t at = first + u * ZERO_THREADS;
         act_place(a, at, row[u], col[u]);
         if (at >= a.chunks) col[u] = a.wide;                 // nothing to read or write
-        sh[u] = 0;
-#pragma unroll
-        for (int w = 0; w < WORDS; w++) q[u][w] = make_uint4(0, 0, 0, 0);
-        if (col[u] >= a.cols) continue;
-        const void* line = row_of<T>(a.x, row[u], a.ld);
-        const char* from = static_cast<const char*>(line) + (int64_t)col[u] * SIZE;
-        sh[u] = (uint32_t)reinterpret_cast<uintptr_t>(from) & 15;
-        from -= sh[u];
-        if (from >= static_cast<const char*>(a.x) && from + 16 * (WORDS - (sh[u] == 0)) <= a.stop) {
-#pragma unroll
-            for (int w = 0; w < WORDS; w++)
-                if (w + 1 < WORDS || sh[u]) q[u][w] = __ldg(reinterpret_cast<const uint4*>(from) + w);
-        } else {
-            Raw<T> r;
-            load_chunk<T>(r, line, col[u], a.cols - col[u] < 8 ? a.cols - col[u] : 7, true);
-            const bool eight = a.cols - col[u] >= 8;         // the last of eight elements
-            const uint32_t b = eight ? load_bits<T>(line, col[u] + 7) : 0;
-            if (T == 2) r.w[T == 2 ? 7 : 0] |= b;
-            else r.w[3] |= b << 16;
-            sh[u] = 0;
-            q[u][0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-            if (T == 2) q[u][1] = make_uint4(r.w[T == 2 ? 4 : 0], r.w[T == 2 ? 5 : 0], r.w[T == 2 ? 6 : 0], r.w[T == 2 ? 7 : 0]);
-        }
+        load_words<T>(w[u], sh[u], row_of<T>(a.x, row[u], a.ld), col[u], a.cols - col[u], a.x, a.stop);
     }
 #pragma unroll
     for (int u = 0; u < ZERO_ACT_UNROLL; u++) {
         Raw<T> r;
-#pragma unroll
-        for (int w = 0; w < WORDS - 1; w++) {
-            const uint4 x = shifted(q[u][w], q[u][w + 1], sh[u]);
-            r.w[4 * w] = x.x; r.w[4 * w + 1] = x.y; r.w[4 * w + 2] = x.z; r.w[4 * w + 3] = x.w;
-        }
-        const int n = a.cols - col[u];
-        if (n < 8)
-#pragma unroll
-            for (int k = 0; k < (T == 2 ? 8 : 4); k++)
-                r.w[k] = T == 2 ? (k < n ? r.w[k] : 0u) : 2 * k + 1 < n ? r.w[k] : 2 * k < n ? r.w[k] & 0xFFFFu : 0u;
+        from_words<T>(r, w[u], sh[u], a.cols - col[u]);
         act_save_chunk<T>(a, row[u], col[u], r);
     }
 }

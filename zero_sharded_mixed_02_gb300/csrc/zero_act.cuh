@@ -208,6 +208,53 @@ static __device__ __forceinline__ uint4 shifted(uint4 q, uint4 n, uint32_t sh)
                       __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
 }
 
+// The aligned 16-byte words in which columns i .. i+8 of a row of any alignment lie, the first
+// `sh` bytes before them.  Words may reach into the neighbouring rows; those that would reach
+// out of the matrix [begin, stop) are put together element by element.  n as below.
+template <int T> struct Words { uint4 q[T == 2 ? 3 : 2]; };
+template <int T>
+static __device__ __forceinline__ void load_words(Words<T>& w, uint32_t& sh, const void* row, uint32_t i, int n,
+                                                  const void* begin, const char* stop)
+{
+    constexpr int WORDS = T == 2 ? 3 : 2;
+    sh = 0;
+#pragma unroll
+    for (int k = 0; k < WORDS; k++) w.q[k] = make_uint4(0, 0, 0, 0);
+    if (n <= 0) return;
+    const char* from = static_cast<const char*>(row) + (uint64_t)i * (T == 2 ? 4 : 2);
+    const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(from) & 15;
+    from -= s;
+    if (from >= static_cast<const char*>(begin) && from + 16 * (WORDS - (s == 0)) <= stop) {
+        sh = s;
+#pragma unroll
+        for (int k = 0; k < WORDS; k++)
+            if (k + 1 < WORDS || s) w.q[k] = __ldg(reinterpret_cast<const uint4*>(from) + k);
+        return;
+    }
+    uint32_t e[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) e[k] = k < n ? load_bits<T>(row, i + k) : 0;
+    if (T == 2) {
+        w.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
+        w.q[1] = make_uint4(e[4], e[5], e[6], e[7]);
+    } else {
+        w.q[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    }
+}
+template <int T>
+static __device__ __forceinline__ void from_words(Raw<T>& r, const Words<T>& w, uint32_t sh, int n)
+{
+#pragma unroll
+    for (int k = 0; k < (T == 2 ? 2 : 1); k++) {
+        const uint4 x = shifted(w.q[k], w.q[k + 1], sh);
+        r.w[4 * k] = x.x; r.w[4 * k + 1] = x.y; r.w[4 * k + 2] = x.z; r.w[4 * k + 3] = x.w;
+    }
+    if (n < 8)
+#pragma unroll
+        for (int k = 0; k < (T == 2 ? 8 : 4); k++)
+            r.w[k] = T == 2 ? (k < n ? r.w[k] : 0u) : 2 * k + 1 < n ? r.w[k] : 2 * k < n ? r.w[k] & 0xFFFFu : 0u;
+}
+
 // Columns i .. i+8 of a row, those at or past n (of the eight) read as 0.  Unless `vec`, a
 // lane has columns lane + 32 k of its warp's 256, for unstage().
 template <int T, bool WHOLE = false>

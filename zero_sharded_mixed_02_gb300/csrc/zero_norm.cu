@@ -251,6 +251,8 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.post = d.post; a.pre = d.pre;
     a.eps = d.eps; a.alpha = d.alpha;
     a.inv_cols = 1.0f / (float)d.cols;
+    a.stop_h = static_cast<const char*>(h) + ((d.rows - 1) * ldh + d.cols) * elem(d.res_dtype);
+    a.stop_y = static_cast<const char*>(y) + (y ? ((d.rows - 1) * ldy + d.cols) * elem(d.dtype) : 0);
     a.vec_h = vec_rows(h, ldh, d.res_dtype);
     a.vec_y = vec_rows(y, ldy, d.dtype);
     a.vec_ho = vec_rows(h_out, ldho, d.res_dtype);

@@ -37,6 +37,7 @@ struct NormArgs {
     int post, pre;
     float eps, alpha, inv_cols;
     int vec_h, vec_y, vec_ho, vec_x, vec_w, vec_g;
+    const char *stop_h, *stop_y;       // ends of h and y
 };
 
 struct NormBwdArgs {
@@ -294,6 +295,12 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
     }
     Raw<RT> rh[V];
     Raw<DT> ry[V];
+    // rows that are not whole aligned chunks: 16-bit ones as words (16384 x 1601 bf16: 115 -> 105 us,
+    // 4096 x 6001: 154 -> 99; three words of an fp32 stream gain nothing: its rows are read column
+    // by column through shared memory)
+    Words<RT> wh[V];
+    Words<DT> wy[V];
+    uint32_t sh[V], sy[V];
     const uint32_t end = (uint32_t)norm_row0(blockIdx.x + 1, a.rows, gridDim.x);
     uint32_t row = (uint32_t)norm_row0(blockIdx.x, a.rows, gridDim.x);
     uint32_t grp = row / a.group, in_group = row - grp * a.group;
@@ -301,8 +308,14 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         const void *ph = row_of<RT>(a.h, at, a.ldh), *py = row_of<DT>(a.y, at, a.ldy);
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            load_chunk<RT, WHOLE>(rh[c], ph, col[c], n[c], a.vec_h);
-            if (block) load_chunk<DT, WHOLE>(ry[c], py, col[c], n[c], a.vec_y);
+            if (WHOLE) {
+                load_chunk<RT, true>(rh[c], ph, col[c], n[c], true);
+                load_chunk<DT, true>(ry[c], py, col[c], n[c], true);
+            } else {
+                if (RT == 2) load_chunk<RT>(rh[c], ph, col[c], n[c], a.vec_h);
+                else load_words<RT>(wh[c], sh[c], ph, col[c], n[c], a.h, a.stop_h);
+                if (block) load_words<DT>(wy[c], sy[c], py, col[c], n[c], a.y, a.stop_y);
+            }
         }
     };
     extern __shared__ __align__(128) unsigned char raw[];
@@ -326,8 +339,13 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 ? 2 : 1)
         f32x2_t h[V][4], y[V][4], w[4];
 #pragma unroll
         for (int c = 0; c < V; c++) {
-            widen_chunk<RT, WHOLE>(rh[c], h[c], a.vec_h, stage);
-            if (block) widen_chunk<DT, WHOLE>(ry[c], y[c], a.vec_y, stage);
+            if (!WHOLE) {
+                if (RT != 2) from_words<RT>(rh[c], wh[c], sh[c], n[c]);
+                else if (!a.vec_h) unstage<RT>(rh[c], stage);
+                if (block) from_words<DT>(ry[c], wy[c], sy[c], n[c]);
+            }
+            widen_chunk<RT>(rh[c], h[c]);
+            if (block) widen_chunk<DT>(ry[c], y[c]);
         }
         if (row + 1 < end) fetch(row + 1);
         float mu2 = 0.0f, r2 = 1.0f, mu1 = 0.0f, r1 = 1.0f;

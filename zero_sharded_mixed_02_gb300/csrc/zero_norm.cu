@@ -14,7 +14,7 @@ struct NormSumArgs {
     void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
     int64_t rows, group, groups;
     int cols, wide, blocks, sums, dtype, grad_dtype, accumulate;
-    int col_jobs, flat;
+    int flat;
     float alpha;
 };
 
@@ -42,11 +42,13 @@ static __device__ __forceinline__ void add4(float4& v, const float* p)
     v.x += s.x; v.y += s.y; v.z += s.z; v.w += s.w;
 }
 
-#define ZERO_NORM_STRIPS 16
+#define ZERO_NORM_SUM_THREADS 512       // of a job: strips of 32 or 8 threads
 
-__host__ __device__ inline int64_t norm_sum_jobs(const NormSumArgs& a)
+__host__ __device__ inline int64_t norm_sum_jobs(const NormSumArgs& a, int lanes)
 {
-    return a.col_jobs * (2 + (!a.dgate ? 0 : a.flat ? (a.groups + ZERO_NORM_STRIPS - 1) / ZERO_NORM_STRIPS : a.groups));
+    const int strips = ZERO_NORM_SUM_THREADS / lanes;
+    const int64_t col_jobs = (a.cols + 4 * lanes - 1) / (4 * lanes);
+    return col_jobs * (2 + (!a.dgate ? 0 : a.flat ? (a.groups + strips - 1) / strips : a.groups));
 }
 
 // The sums of a group's rows at column c: its blocks' slots from the group's block `first` by step.
@@ -70,22 +72,27 @@ static __device__ __forceinline__ void gate_out(const NormSumArgs& a, int64_t g,
     grad_out(a.dgate, g * a.cols + c, a.alpha * v0, a.grad_dtype, a.accumulate);
 }
 
-// Adds the blocks' partial sums.  A job is 128 columns (four a thread) of the pre-norm's
-// sums, of the post-norm's, or of a gate group's; the strips of threads take every
-// 16th block's part, and the strips are added in order.  Where a group spans few blocks
-// (flat), a gate job is 128 columns of 16 groups instead, a strip each.
-__global__ void __launch_bounds__(32 * ZERO_NORM_STRIPS) k_norm_sums(const __grid_constant__ NormSumArgs a)
+// Adds the blocks' partial sums.  A job is 128 or 32 columns (four a thread) of the pre-norm's
+// sums, of the post-norm's, or of a gate group's; the strips of LANES threads take every 16th or
+// 64th block's part, and the strips are added in order.  Where a group spans few blocks (flat), a
+// gate job is these columns of as many groups instead, a strip each.  The parts lie in L2.  Few
+// jobs are a matter of latency and are made narrow: 29.1 -> 24.9 us a backward pass at 8192 x 768
+// (60 wide jobs), where many would come in waves: 87 -> 99 us at 8192 x 4096 (576).
+template <int LANES>
+__global__ void __launch_bounds__(ZERO_NORM_SUM_THREADS) k_norm_sums(const __grid_constant__ NormSumArgs a)
 {
-    __shared__ float4 s0[ZERO_NORM_STRIPS][32], s1[ZERO_NORM_STRIPS][32];
+    constexpr int STRIPS = ZERO_NORM_SUM_THREADS / LANES, WIDTH = 4 * LANES, PARTS = ZERO_NORM_SUM_THREADS / WIDTH;
+    __shared__ float4 s0[STRIPS][LANES], s1[STRIPS][LANES];
+    __shared__ float r0[STRIPS > 16 ? PARTS : 1][WIDTH], r1[STRIPS > 16 ? PARTS : 1][WIDTH];
     asm volatile("griddepcontrol.wait;" ::: "memory");       // the pass whose sums these are
     const int strip = threadIdx.y;
-    const int64_t jobs = norm_sum_jobs(a);
+    const int64_t jobs = norm_sum_jobs(a, LANES), col_jobs = (a.cols + WIDTH - 1) / WIDTH;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         float4 v0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v1 = v0;
-        const int64_t what = job / a.col_jobs;
+        const int64_t what = job / col_jobs;
         if (what >= 2 && a.flat) {
-            const int64_t g = (what - 2) * ZERO_NORM_STRIPS + strip;
-            const int c = (int)(job - what * a.col_jobs) * 128 + 4 * threadIdx.x;
+            const int64_t g = (what - 2) * STRIPS + strip;
+            const int c = (int)(job - what * col_jobs) * WIDTH + 4 * threadIdx.x;
             if (g >= a.groups || c >= a.wide) continue;
             add_group(a, g, c, 0, 1, v0, v1);
 #pragma unroll
@@ -93,12 +100,12 @@ __global__ void __launch_bounds__(32 * ZERO_NORM_STRIPS) k_norm_sums(const __gri
                 if (c + e < a.cols) gate_out(a, g, c + e, (&v0.x)[e], (&v1.x)[e]);
             continue;
         }
-        const int c = (int)(job - what * a.col_jobs) * 128 + 4 * threadIdx.x;
+        const int c = (int)(job - what * col_jobs) * WIDTH + 4 * threadIdx.x;
         if (what >= 2) {
-            if (c < a.wide) add_group(a, what - 2, c, strip, ZERO_NORM_STRIPS, v0, v1);
+            if (c < a.wide) add_group(a, what - 2, c, strip, STRIPS, v0, v1);
         } else if (const float* p = what == 0 ? a.pre_part : a.post_part; p && c < a.wide) {
 #pragma unroll 8
-            for (int b = strip; b < a.blocks; b += ZERO_NORM_STRIPS) {
+            for (int b = strip; b < a.blocks; b += STRIPS) {
                 add4(v0, p + (int64_t)b * a.sums * a.wide + c);
                 if (a.sums == 2) add4(v1, p + (int64_t)b * a.sums * a.wide + a.wide + c);
             }
@@ -107,14 +114,30 @@ __global__ void __launch_bounds__(32 * ZERO_NORM_STRIPS) k_norm_sums(const __gri
         s0[strip][threadIdx.x] = v0;
         s1[strip][threadIdx.x] = v1;
         __syncthreads();
-        if (strip >= 4) continue;                            // the first four finish 32 columns each
-        const int own = (int)(job - what * a.col_jobs) * 128 + strip * 32 + threadIdx.x;
-        if (own >= a.cols) continue;
+        // a thread a column; with many strips their sums by parts first
+        const int at = strip * LANES + threadIdx.x, part = at / WIDTH, w = at % WIDTH;
+        const float *p0 = reinterpret_cast<const float*>(s0), *p1 = reinterpret_cast<const float*>(s1);
+        constexpr int LEFT = STRIPS > 16 ? PARTS : STRIPS;
+        if (STRIPS > 16) {
+            float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < STRIPS / PARTS; i++) {
+                t0 += p0[(part * (STRIPS / PARTS) + i) * WIDTH + w];
+                t1 += p1[(part * (STRIPS / PARTS) + i) * WIDTH + w];
+            }
+            r0[part][w] = t0;
+            r1[part][w] = t1;
+            __syncthreads();
+            p0 = r0[0];
+            p1 = r1[0];
+        }
+        const int own = (int)(job - what * col_jobs) * WIDTH + w;
+        if (part > 0 || own >= a.cols) continue;
         float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < ZERO_NORM_STRIPS; i++) {
-            t0 += reinterpret_cast<const float*>(s0[i])[strip * 32 + threadIdx.x];
-            t1 += reinterpret_cast<const float*>(s1[i])[strip * 32 + threadIdx.x];
+        for (int i = 0; i < LEFT; i++) {
+            t0 += p0[i * WIDTH + w];
+            t1 += p1[i * WIDTH + w];
         }
         if (what == 0) {
             if (a.dpre_w) grad_out(a.dpre_w, own, t0, a.grad_dtype, a.accumulate);
@@ -392,18 +415,18 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     a.dtype = d.dtype; a.grad_dtype = grad_dtype; a.accumulate = accumulate != 0;
     a.alpha = d.alpha;
     a.wide = (int)act_wide(d.cols);
-    a.col_jobs = (int)((d.cols + 127) / 128);
     a.flat = a.groups * 4 > blocks;
-    const int64_t jobs = norm_sum_jobs(a);
+    const bool narrow = norm_sum_jobs(a, 32) <= 76 && blocks >= 128;
+    const int64_t jobs = norm_sum_jobs(a, narrow ? 8 : 32);
     // placed while the pass drains; it waits for the pass's sums itself
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)(jobs < (1 << 30) ? jobs : 1 << 30));
-    c.blockDim = dim3(32, ZERO_NORM_STRIPS);
+    c.blockDim = narrow ? dim3(8, ZERO_NORM_SUM_THREADS / 8) : dim3(32, ZERO_NORM_SUM_THREADS / 32);
     c.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     c.attrs = &at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, k_norm_sums, a) == cudaSuccess ? ZERO_OK : ZERO_ECUDA;
+    return cudaLaunchKernelEx(&c, narrow ? k_norm_sums<8> : k_norm_sums<32>, a) == cudaSuccess ? ZERO_OK : ZERO_ECUDA;
 }

@@ -350,3 +350,49 @@ def test_wgrad_against_differences(env):
         slope = ((dyv * (xq @ (w + u).T)).sum() - (dyv * (xq @ (w - u).T)).sum()) / 2
         room = (tokens + 8) * 2.0 ** -23 * ((np.abs(dyv).T @ np.abs(xq)) * np.abs(u)).sum()
         assert abs(slope - (got * u).sum()) <= room
+
+
+# ---- offsets past 32 bits -------------------------------------------------------------
+
+def test_checkpoints_past_32_bits(env):
+    """4.6 G elements: rows at both ends against the same rows alone."""
+    torch, z = env
+    rows, cols = 70001, 65536
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:3].normal_(), x[-3:].normal_()
+    ckpt = save(torch, z, x.data_ptr(), R.BF16, rows, cols, cols)
+    for part in (slice(0, 3), slice(rows - 3, rows)):
+        alone = save(torch, z, x[part].data_ptr(), R.BF16, 3, cols, cols)
+        assert torch.equal(ckpt[part], alone)
+    assert not ckpt[3:6, :cols].any()
+    out = torch.full((rows, cols + 1), 7.0, dtype=torch.bfloat16, device="cuda")          # unaligned rows
+    z.zero_act_load(R.BF16, ckpt, rows, cols, out, cols + 1, stream(torch))
+    want = torch.empty(3, cols, dtype=torch.bfloat16, device="cuda")
+    z.zero_act_load(R.BF16, ckpt[-3:], 3, cols, want, cols, stream(torch))
+    assert torch.equal(out[-3:, :cols], want) and bool((out[-5:, cols] == 7.0).all()) and not out[3:6, :cols].any()
+    again = save(torch, z, out.data_ptr(), R.BF16, rows, cols, cols + 1)
+    assert torch.equal(again[-3:], ckpt[-3:])
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_wgrad_past_32_bits(env, shift):
+    """dy of 2.2 G elements, zero but for its first and last tokens."""
+    torch, z = env
+    tokens, n, k = (1 << 21) + 5, 1040, 40
+    rng = np.random.default_rng(1)
+    store = torch.zeros(tokens * n + 8, dtype=torch.bfloat16, device="cuda")
+    dy = store[shift:shift + tokens * n].view(tokens, n)
+    x = torch.randn(tokens, k, device="cuda").to(torch.bfloat16)
+    ckpt = save(torch, z, x.data_ptr(), R.BF16, tokens, k, k)
+    pick = [0, 1, 70, tokens - 66, tokens - 2, tokens - 1]
+    for t in pick:
+        dy[t] = torch.from_numpy(rng.standard_normal(n)).to(torch.bfloat16).cuda()
+    dw, db = torch.empty(n, k, device="cuda"), torch.empty(n, device="cuda")
+    work = torch.zeros(z.zero_act_wgrad_workspace(tokens, n, k), dtype=torch.uint8, device="cuda")
+    z.zero_act_wgrad(R.BF16, dy.data_ptr(), tokens, n, n, ckpt, k, None, None, R.FP32, dw, k, db, 0, work, stream(torch))
+    assert int(work[:4].view(torch.int32)[0]) == 0
+    xq = R.values(ckpt[pick].cpu().numpy(), k)
+    d = dy[pick].double().cpu().numpy()
+    # six terms and zeros: a few units in the last place of the magnitudes
+    assert np.all(np.abs(dw.double().cpu().numpy() - d.T @ xq) <= 2.0 ** -20 * (np.abs(d).T @ np.abs(xq)) + 1e-30)
+    assert np.all(np.abs(db.double().cpu().numpy() - d.sum(0)) <= 2.0 ** -20 * np.abs(d).sum(0) + 1e-30)

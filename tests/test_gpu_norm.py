@@ -330,3 +330,38 @@ def test_forward_and_backward_against_differences(env):  # noqa: F811
             # each term off by 2^-6 of its magnitude (times the largest |normalised| value, below 5), in
             # random directions: five standard deviations
             assert abs(slope - have) <= 5 * 2.0 ** -6 * 5 * np.sqrt((m.reshape(v.shape) ** 2).sum()) + 1e-6, name
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+def test_rows_past_32_bits(env, pad):  # noqa: F811
+    """2.3 G elements: the last rows of both passes against a call on those rows alone."""
+    torch, z = env
+    rows, cols, last = 140000, 16384 - 8, 3
+    ld = cols + pad
+    new = lambda *shape, dtype=torch.bfloat16: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    h, y, x = new(rows, ld), new(rows, ld), new(rows, ld)
+    h[-last:].normal_(), y[-last:].normal_()
+    size = z.zero_act_row_bytes(cols)
+    cy, cx = new(rows, size, dtype=torch.uint8), new(rows, size, dtype=torch.uint8)
+    st = new(rows, 4, dtype=torch.float32)
+
+    def forward(n, h, y, x, cy, cx, st):
+        z.zero_norm_forward(z.norm(R.BF16, n, cols, post=R.RMS, pre=R.RMS), h.data_ptr(), ld, y.data_ptr(), ld, h.data_ptr(), ld,
+                            x.data_ptr(), ld, cy.data_ptr(), cx.data_ptr(), st.data_ptr(), stream(torch))
+
+    tail = [t[-last:].clone() for t in (h, y, x, cy, cx, st)]
+    forward(rows, h, y, x, cy, cx, st)
+    forward(last, *tail)
+    for a, b in zip((h, y, x, cy, cx, st), tail):
+        assert torch.equal(a[-last:], b)
+
+    def backward(n, dh, dx, cy, cx, st, dy):
+        norm = z.norm(R.BF16, n, cols, post=R.RMS, pre=R.RMS)
+        z.zero_norm_backward(norm, dh.data_ptr(), ld, dx.data_ptr(), ld, cy.data_ptr(), cx.data_ptr(), st.data_ptr(), dh.data_ptr(), ld,
+                             dy.data_ptr(), ld, R.BF16, stream=stream(torch))
+
+    tail = [t[-last:].clone() for t in (h, x, cy, cx, st, y)]
+    backward(rows, h, x, cy, cx, st, y)
+    backward(last, *tail)
+    for a, b in zip((h, x, cy, cx, st, y), tail):
+        assert torch.equal(a[-last:], b)

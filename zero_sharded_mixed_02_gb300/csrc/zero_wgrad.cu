@@ -593,12 +593,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                 wgrad_place(a, g.tile, i0, j0);
                 const int x = (int)(i0 + rank * 128), c = (int)j0 + rank * (wgrad_width(a, j0) / 2);
                 const int e = (int)a.wide + (c / 32 & ~15);
-                for (int y = g.s0 * ZERO_WG_TOK, end = g.s1 * ZERO_WG_TOK; y < end; y += ZERO_WG_TOK, n++) {
+                for (int t = g.s0; t < g.s1; t++, n++) {
                     if (n >= ring && !pair_wait(frees + 8 * s, ph ^ 1u, dead, a.err)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = loads + 8 * l;
+                    const int y = t * ZERO_WG_TOK;           // below 2^31
                     if (codes) {
                         const uint32_t at = base_c + s * (ZERO_WG_C + ZERO_WG_E);
                         mbar_expect_tx(bar, ZERO_WG_C + ZERO_WG_E);

@@ -42,6 +42,7 @@ namespace zero {
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
 #define ZERO_WG_RUN 64                      // stages an accumulator adds for an fp32 gradient
+#define ZERO_WG_DEEP 4                      // parts a tile from which eight warps share them
 #define ZERO_WG_FEW 64                      // most tokens that k_wgrad_few takes,
 #define ZERO_WG_FEW_WORK (60ll << 20)       // and most products
 #define ZERO_WG_FEW_TOK 32                  // tokens it adds at a time
@@ -369,9 +370,12 @@ static __device__ __forceinline__ void put_rows(const WgradArgs& a, int64_t i0, 
     __syncwarp();
 }
 
-// Whether a tile adds its rows' sums of dy: for db, in the first column of tiles, unless
-// k_wgrad_columns has added them all.
-static __device__ __forceinline__ bool adds_sums(const WgradArgs& a, int64_t j0) { return a.db && j0 == 0 && !a.sums; }
+// Whether a tile adds its rows' sums of dy: for db (and for the norm's bias if there are no
+// other columns of tiles), in the first column, unless k_wgrad_columns has added them all.
+static __device__ __forceinline__ bool adds_sums(const WgradArgs& a, int64_t j0)
+{
+    return (a.db || a.shift) && j0 == 0 && !a.sums;
+}
 
 // Row i's sum of dy from k_wgrad_columns.
 static __device__ __forceinline__ float column_sum(const WgradArgs& a, int64_t i)
@@ -887,27 +891,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
     cluster_sync();                          // the two SMs give the tensor memory back together
 }
 
-// Adds the parts of the cut tiles in token order and writes them out: a warp takes 32
-// rows and 16 columns of a tile.
-template <int DT>
+// Adds the parts of the cut tiles in token order and writes them out: a warp takes 32 rows and 16
+// columns of a tile, or (DEEP) the eight warps of a block share their parts, add them and the
+// eight sums in order.  That is for tiles of many parts, where a warp alone would wait for one
+// load after another (a call on 41245 tokens, 64 x 128, 76 parts: 23 us instead of 41; with two
+// parts a tile it costs 6 us at 8192 x 6400 x 1600).
+template <int DT, bool DEEP>
 __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ WgradArgs a, const __grid_constant__ WgradJoin of)
 {
-    const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    __shared__ __align__(16) float4 sums_of[DEEP ? 8 : 1][4][32];
+    __shared__ float rows_of[DEEP ? 8 : 1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t unit = DEEP ? blockIdx.x : blockIdx.x * 8 + warp;
     const int q = unit >> 7;
     const int strip = (unit >> 4) & 7, c = unit & 15;               // (SM, warp) of the rows; 16 columns
-    const int p0 = of.p0[q], p1 = of.p1[q], first = of.second[q];
+    const int first = of.second[q];
+    int p0 = of.p0[q], p1 = of.p1[q];
     int64_t i0, j0;
     wgrad_place(a, (uint32_t)(a.waves * a.pairs + q), i0, j0);
     const int64_t r = i0 + strip * 32 + lane;
     if (p0 == p1 || j0 + c * 16 >= a.k) return;                     // not cut, or past the right edge
     const bool sums = adds_sums(a, j0);
-    float v[16], sum = column_sum(a, r);
+    const int begin = p0;
+    if (DEEP) {
+        const int each = (p1 - p0 + 8) / 8;
+        p0 += warp * each;
+        p1 = p1 < p0 + each - 1 ? p1 : p0 + each - 1;
+    }
+    float v[16], sum = DEEP ? 0.0f : column_sum(a, r);
 #pragma unroll
     for (int e = 0; e < 16; e++) v[e] = 0.0f;
 #pragma unroll 4
     for (int p = p0; p <= p1; p++) {
-        const float* part = a.slots + (int64_t)(2 * p + (p == p0 ? first : 0)) * ZERO_WG_SLOT;
+        const float* part = a.slots + (int64_t)(2 * p + (p == begin ? first : 0)) * ZERO_WG_SLOT;
         const float4* s = reinterpret_cast<const float4*>(part) + (strip * 64 + c * 4) * 32 + lane;
         if (sums) sum += __ldcg(part + ZERO_WG_TILE * ZERO_WG_TILE + strip * 32 + lane);
 #pragma unroll
@@ -917,6 +933,28 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const __grid_constant__ Wgra
             v[4 * e + 1] += f.y;
             v[4 * e + 2] += f.z;
             v[4 * e + 3] += f.w;
+        }
+    }
+    if (DEEP) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) sums_of[warp][e][lane] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        rows_of[warp][lane] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+        sum = column_sum(a, r);
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+            sum += rows_of[w][lane];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float4 f = sums_of[w][e][lane];
+                v[4 * e] += f.x;
+                v[4 * e + 1] += f.y;
+                v[4 * e + 2] += f.z;
+                v[4 * e + 3] += f.w;
+            }
         }
     }
     if (a.db && j0 == 0 && c == 0 && r < a.n) put_grad(a.db, r, sum, a.grad_dtype, a.accumulate);
@@ -982,7 +1020,8 @@ __global__ void __launch_bounds__(256) k_wgrad_columns(const __grid_constant__ W
 // fp32 in shared memory, and each thread adds 8 rows of 4 columns in registers.  dy is read
 // element by element, in any alignment.  768 x 768: 4.1 us for 16 tokens and 8.8 for 64, against
 // 10.2; 1600 x 1600: 7.9 for 16 and 17.7 for 64, against 10; 4096 x 4096: 18 for one and 28 for
-// 16, against 20.  So it is taken for up to ZERO_WG_FEW tokens and ZERO_WG_FEW_WORK products.
+// 16, against 20.  So it is taken for up to ZERO_WG_FEW tokens and ZERO_WG_FEW_WORK products, and
+// for up to four tokens and 32 M elements of dw.
 template <int DT>
 __global__ void __launch_bounds__(256) k_wgrad_few(const __grid_constant__ WgradArgs a)
 {
@@ -1209,7 +1248,7 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.db = db;
     a.err = static_cast<int32_t*>(work);
     char* at = static_cast<char*>(work) + 256;
-    if (col_shift) a.sums = reinterpret_cast<float*>(at);
+    if (col_shift && k > ZERO_WG_TILE) a.sums = reinterpret_cast<float*>(at);
     at += sums_bytes(n);
     a.slots = reinterpret_cast<float*>(at);
     at += parts_bytes(tokens);
@@ -1221,7 +1260,7 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     a.vec_s = aligned_to(col_scale, 16) && aligned_to(col_shift, 16);
     const bool half = dtype == ZERO_FP16;
     void* args[] = {&a, nullptr, nullptr, nullptr};
-    if (tokens <= ZERO_WG_FEW && tokens * n * k <= ZERO_WG_FEW_WORK) {
+    if ((tokens <= ZERO_WG_FEW && tokens * n * k <= ZERO_WG_FEW_WORK) || (tokens <= 4 && n * k <= 32 << 20)) {
         const int64_t wide = up(k, 128);
         return launch(half ? (const void*)k_wgrad_few<0> : (const void*)k_wgrad_few<1>,
                       dim3((unsigned)up(n, 64), (unsigned)(wide < 32768 ? wide : 32768)), 256, 0, args, stream)
@@ -1287,9 +1326,12 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
     if (!launch(half ? (const void*)k_wgrad<0> : (const void*)k_wgrad<1>, dim3(2 * run), ZERO_WG_THREADS, ZERO_WG_SMEM, args,
                 stream))
         return ZERO_ECUDA;
-    void* last[] = {&a, &join};
-    if (a.rest_pairs > a.rest &&
-        !launch(half ? (const void*)k_wgrad_join<0> : (const void*)k_wgrad_join<1>, dim3(a.rest * 16), 256, 0, last, stream))
-        return ZERO_ECUDA;
+    if (a.rest_pairs > a.rest) {
+        const bool deep = a.rest_pairs >= ZERO_WG_DEEP * a.rest;
+        const void* const joins[2][2] = {{(const void*)k_wgrad_join<1, false>, (const void*)k_wgrad_join<1, true>},
+                                         {(const void*)k_wgrad_join<0, false>, (const void*)k_wgrad_join<0, true>}};
+        void* last[] = {&a, &join};
+        if (!launch(joins[half][deep], dim3(a.rest * (deep ? 128 : 16)), 256, 0, last, stream)) return ZERO_ECUDA;
+    }
     return ZERO_OK;
 }

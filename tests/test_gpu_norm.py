@@ -245,12 +245,21 @@ def test_backward_strides(env, pad, shift, res):  # noqa: F811
                                        (2, 8190), (2000, 33)])
 @pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (0, 5), (7, 7)])
 @pytest.mark.parametrize("dtype,res,post,pre,bias", [(R.BF16, R.BF16, 1, 1, False), (R.FP16, R.FP32, 2, 2, True),
-                                                     (R.FP16, R.FP16, 0, 2, True), (R.BF16, R.FP32, 0, 1, False)])
+                                                     (R.FP16, R.FP16, 0, 2, True), (R.BF16, R.FP32, 0, 1, False),
+                                                     (R.BF16, R.BF16, 1, 1, True), (R.FP16, R.FP32, 1, 0, True),
+                                                     (R.FP16, R.FP16, 1, 0, False), (R.BF16, R.FP32, 0, 1, True)])
 def test_backward_rows_of_any_alignment(env, rows, cols, pad, shift, dtype, res, post, pre, bias):  # noqa: F811
     """Rows whose words and chunks do not coincide: every shift, rows of one warp, rows that fill
     the threads, and the matrices' first and last words."""
     run_backward(env, params(rows, cols, post, pre, group=3, bias=bias), dtype, res, R.FP32, pad=pad, shift=shift,
                  in_place=rows == 40)
+
+
+@pytest.mark.parametrize("rows,cols", [(7, 64), (700, 1600), (30, 4096), (9, 8192)])
+@pytest.mark.parametrize("post,pre,bias", [(1, 1, True), (0, 1, True), (1, 0, True), (1, 0, False)])
+@pytest.mark.parametrize("res", [R.BF16, R.FP32])
+def test_backward_aligned_rows_of_other_kinds(env, rows, cols, post, pre, bias, res):  # noqa: F811
+    run_backward(env, params(rows, cols, post, pre, group=4, bias=bias), R.BF16, res, R.FP32)
 
 
 @pytest.mark.parametrize("accumulate", [0, 1])

@@ -364,12 +364,11 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
                            (!dx || a.vec_dx) && (!dh || whole_rows(dh, lddh, d.res_dtype)) && a.vec_dy && a.vec_w &&
                            (!d.gate || a.vec_g);
         // other rows can be copied ahead too if their words, one more than chunks, have threads
-        bool copied = !whole && dx && dy;
+        bool copied = !whole && dy && norm_kinds_copied(d.post, d.pre);
         if (copied) {
             int cv = 1, ct = 32;
             row_shape(((2 * a.cols + 13) / 16 + 1) * 8, cv, ct);
-            copied = cv <= 2 && (int64_t)cv * ct * norm_ring_bytes(d.res_dtype) + 18 * 1024 <= 227 * 1024 &&
-                     (d.pre == ZERO_NORM_LAYER || !two) && (d.post == ZERO_NORM_NONE || d.post == d.pre);
+            copied = cv <= 2 && (int64_t)cv * ct * norm_ring_bytes(d.res_dtype) + 18 * 1024 <= 227 * 1024;
             if (copied) {
                 v = cv;
                 threads = ct;

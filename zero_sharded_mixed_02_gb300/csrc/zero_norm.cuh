@@ -811,13 +811,13 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
             for (int c = 0; c < V; c++) {
                 const uint32_t at = part + slot + c * threads * PART, k = chunk(c);
                 if (in(c)) {
-                    if (!ANY) copy16(at, lx + 16 * k);
-                    copy8(at + T16, qx + 8 * k);
+                    if (PRE && !ANY) copy16(at, lx + 16 * k);
+                    if (PRE) copy8(at + T16, qx + 8 * k);
                     if (a.ckpt_y) copy8(at + T16 + 8, qy + 8 * k);
                     if (!ANY && !WIDE && a.dh_out) copy16(at + 2 * T16, ld + 16 * k);
                 }
                 if (ANY) {
-                    word(at, lx, k, a.dx, lx_step);
+                    if (PRE) word(at, lx, k, a.dx, lx_step);
                     if (!WIDE && a.dh_out) word(at + 2 * T16, ld, k, a.dh_out, ld_step);
                 }
                 if (ANY && WIDE && a.dh_out) {
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
         for (int c = 0; c < V; c++) {
             ex[c] = ey[c] = 0;
             if (in(c)) {
-                ex[c] = __ldg(lex + (chunk(c) >> 2));
+                if (PRE) ex[c] = __ldg(lex + (chunk(c) >> 2));
                 if (a.ckpt_y) ey[c] = __ldg(ley + (chunk(c) >> 2));
             }
         }
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
     };
     auto scales = [&](int c, f32x2_t (&u)[4]) { get_chunk(weights + c * threads * PART, T16, u); };
     auto widen16 = [&](uint32_t at, f32x2_t (&v)[4]) { get16<DT>(at, v); };
-    if (a.pre_w)
+    if (PRE && a.pre_w)
 #pragma unroll
         for (int c = 0; c < V; c++)
             put_pre<DT, !ANY>(weights + c * threads * PART + 2 * T16, a.pre_w, 8 * chunk(c), left_of(c), ANY ? a.vec_w : 1, stage);
@@ -956,27 +956,32 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
 #pragma unroll
         for (int c = 0; c < V; c++) {
             const uint32_t p = part + at + c * threads * PART;
-            if (ANY) {
-                const uint4 x = shifted(shared16(p), shared16(p + next(c)), (shift_x + row * (uint32_t)lx_step) & 15);
-                Raw<DT> r;
-                r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
-                widen_chunk<DT>(r, b[c]);
-                end_of_row(b[c], left_of(c));
-            } else {
-                widen16(p, b[c]);                            // dx, then g, then B
-            }
             const uint4 q = shared16(p + T16);
-            act_values(make_uint2(q.x, q.y), ex[c], xh);
             fx[c] = ex[c];
             fy[c] = ey[c];
+            if (PRE) {
+                if (ANY) {
+                    const uint4 x = shifted(shared16(p), shared16(p + next(c)), (shift_x + row * (uint32_t)lx_step) & 15);
+                    Raw<DT> r;
+                    r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+                    widen_chunk<DT>(r, b[c]);
+                    end_of_row(b[c], left_of(c));
+                } else {
+                    widen16(p, b[c]);                            // dx, then g, then B
+                }
+                act_values(make_uint2(q.x, q.y), ex[c], xh);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                pw[c][j] = fma2(b[c][j], xh[j], pw[c][j]);
-                if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
-            }
-            if (a.pre_w) {
-                widen16(weights + c * threads * PART + 2 * T16, w);
-                times(b[c], w);
+                for (int j = 0; j < 4; j++) {
+                    pw[c][j] = fma2(b[c][j], xh[j], pw[c][j]);
+                    if (TWO) pb[c][j] = add2(pb[c][j], b[c][j]);
+                }
+                if (a.pre_w) {
+                    widen16(weights + c * threads * PART + 2 * T16, w);
+                    times(b[c], w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++) b[c][j] = xh[j] = both(0.0f);
             }
             if (WIDE) {
                 const uint32_t m = mine + at + c * threads * 32;
@@ -996,13 +1001,13 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                s2[0] = fma2(b[c][j], xh[j], s2[0]);
+                if (PRE) s2[0] = fma2(b[c][j], xh[j], s2[0]);
                 if (PRE == ZERO_NORM_LAYER) s2[3] = add2(s2[3], b[c][j]);
-                b[c][j] = fma2(both(k1), b[c][j], w[j]);
+                b[c][j] = PRE ? fma2(both(k1), b[c][j], w[j]) : w[j];
                 if (POST) {
                     const f32x2_t uy = mul2(u[j], yh[j]);
                     s2[1] = fma2(uy, b[c][j], s2[1]);
-                    s2[2] = fma2(uy, xh[j], s2[2]);
+                    if (PRE) s2[2] = fma2(uy, xh[j], s2[2]);
                     if (LAYER) s2[4] = add2(s2[4], uy);
                 }
                 if (POST == ZERO_NORM_LAYER) {
@@ -1033,7 +1038,7 @@ __global__ void __launch_bounds__(ZERO_NORM_THREADS, V == 1 && !TWO && !ANY ? 2 
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 if (PRE == ZERO_NORM_LAYER) b[c][j] = sub2(b[c][j], both(p0));
-                b[c][j] = fma2(both(-p1), xh[j], b[c][j]);
+                if (PRE) b[c][j] = fma2(both(-p1), xh[j], b[c][j]);
             }
             if (a.dh) store_chunk<RT, !ANY>(sd, 8 * k, left_of(c), ANY ? a.vec_dh : true, stage, b[c]);
             act_values(make_uint2(q.z, q.w), fy[c], yh);
@@ -1084,21 +1089,28 @@ static const void* norm_forward_of(int post, int pre, bool whole)
     }
     return (const void*)k_norm_forward<DT, RT, V, -1, -1>;
 }
+// The kinds whose rows are copied ahead: the same norm on both sides, only the one before the next
+// block, or only an RMS norm after this one.
+static inline bool norm_kinds_copied(int post, int pre) { return pre == 0 ? post == 1 : post == 0 || post == pre; }
+
 // `two`: both sums are wanted; set where the kernel keeps both all the same.  `smem`: bytes of
 // shared memory a thread of the kernel needs.  `copied`: whether the rows can be copied ahead
-// (there are dx and dy, and with rows that are not whole a word more fits into the threads).
+// (there is dy, and with rows that are not whole a word more fits into the threads).
 template <int DT, int RT, int V, bool ANY>
 static const void* norm_backward_copied(int post, int pre, bool& two, int& smem)
 {
     smem = NormRing<RT, V, ANY>::bytes;
-    if (post == 0 && pre == 1 && !two) return (const void*)k_norm_backward_whole<DT, RT, V, 0, 1, false, ANY>;
-    if (post == 1 && pre == 1 && !two) return (const void*)k_norm_backward_whole<DT, RT, V, 1, 1, false, ANY>;
-    if (pre == 2 && (post == 0 || post == 2)) {
-        two = true;
-        return post == 0 ? (const void*)k_norm_backward_whole<DT, RT, V, 0, 2, true, ANY>
-                         : (const void*)k_norm_backward_whole<DT, RT, V, 2, 2, true, ANY>;
-    }
-    return nullptr;
+    if (!norm_kinds_copied(post, pre)) return nullptr;
+    if (pre == 1 && !two)
+        return post == 0 ? (const void*)k_norm_backward_whole<DT, RT, V, 0, 1, false, ANY>
+                         : (const void*)k_norm_backward_whole<DT, RT, V, 1, 1, false, ANY>;
+    two = true;
+    if (pre == 0) return (const void*)k_norm_backward_whole<DT, RT, V, 1, 0, true, ANY>;
+    if (pre == 1)
+        return post == 0 ? (const void*)k_norm_backward_whole<DT, RT, V, 0, 1, true, ANY>
+                         : (const void*)k_norm_backward_whole<DT, RT, V, 1, 1, true, ANY>;
+    return post == 0 ? (const void*)k_norm_backward_whole<DT, RT, V, 0, 2, true, ANY>
+                     : (const void*)k_norm_backward_whole<DT, RT, V, 2, 2, true, ANY>;
 }
 template <int DT, int RT, int V>
 static const void* norm_backward_of(int post, int pre, bool whole, bool copied, bool& two, int& smem)

@@ -41,7 +41,7 @@ namespace zero {
 #define ZERO_WG_THREADS (256 + ZERO_WG_WIDENERS)    // warps 0 and 2 TMA, 1 products, 4-7 output, from 8 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
-#define ZERO_WG_RUN 64                      // stages an accumulator adds for an fp32 gradient
+#define ZERO_WG_RUN 12                      // stages an accumulator adds for an fp32 gradient
 #define ZERO_WG_DEEP 4                      // parts a tile from which eight warps share them
 #define ZERO_WG_FEW 64                      // most tokens that k_wgrad_few takes,
 #define ZERO_WG_FEW_WORK (60ll << 20)       // and most products
@@ -79,8 +79,9 @@ struct WgradArgs {
 // A run of stages whose products one accumulator adds.  The tensor cores cut each sum off
 // rather than round it, so an accumulator's relative error grows by about 1.6e-8 a step of
 // 16 tokens (6.4e-6 after 400, at random inputs): fp32 gradients, whose type would show it,
-// are summed in runs of 64 stages (256 steps, 4e-6) that are added in fp32.  Writing the runs
-// out costs 10 % of the time at 8192 x 4096 x 4096 (173 -> 190 us).
+// are summed in runs of 12 stages (48 steps) that are added in fp32.  At 30011 tokens,
+// 776 x 771, runs of 64 stages take 59.6 us and are off by 3.8e-6, runs of 12 take 77.9 us and
+// are off by 7.4e-7 (an fp32 product without tensor cores: 2.9e-7).
 struct WgradSegment {
     uint32_t tile;
     int32_t s0, s1;                         // stages [s0, s1) of a tile

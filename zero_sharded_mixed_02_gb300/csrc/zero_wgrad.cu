@@ -41,7 +41,7 @@ namespace zero {
 #define ZERO_WG_THREADS (256 + ZERO_WG_WIDENERS)    // warps 0 and 2 TMA, 1 products, 4-7 output, from 8 widening
 #define ZERO_WG_PAIRS 80                    // most pairs that share a launch's work
 #define ZERO_WG_PART 8                      // least stages of a part of a cut tile
-#define ZERO_WG_RUN 12                      // stages an accumulator adds for an fp32 gradient
+#define ZERO_WG_RUN 12                      // stages an accumulator adds for an fp32 gradient (from 16 stages)
 #define ZERO_WG_DEEP 4                      // parts a tile from which eight warps share them
 #define ZERO_WG_FEW 64                      // most tokens that k_wgrad_few takes,
 #define ZERO_WG_FEW_WORK (60ll << 20)       // and most products
@@ -57,7 +57,9 @@ namespace zero {
 #define ZERO_WG_OUT 2048                    // rows that an output warp writes
 #define ZERO_WG_SMEM \
     (ZERO_WG_STAGES * ZERO_WG_A + ZERO_WG_CODES * (ZERO_WG_C + ZERO_WG_E) + ZERO_WG_WIDE * ZERO_WG_A + ZERO_WG_SUMS + 4 * ZERO_WG_OUT + 1024)
-#define ZERO_WG_SLOT (ZERO_WG_TILE * (ZERO_WG_TILE + 1))  // floats of a part: its sums, its rows' sums of dy
+// Slots of the workspace for sums: two for each pair's parts of cut tiles, one for its runs.
+#define ZERO_WG_SLOTS (3 * ZERO_WG_PAIRS)
+#define ZERO_WG_SLOT (ZERO_WG_TILE * (ZERO_WG_TILE + 1))  // floats of one: a tile's sums, its rows' sums of dy
 
 struct WgradArgs {
     const uint16_t* dy;
@@ -79,7 +81,7 @@ struct WgradArgs {
 // A run of stages whose products one accumulator adds.  The tensor cores cut each sum off
 // rather than round it, so an accumulator's relative error grows by about 1.6e-8 a step of
 // 16 tokens (6.4e-6 after 400, at random inputs): fp32 gradients, whose type would show it,
-// are summed in runs of 12 stages (48 steps) that are added in fp32.  At 30011 tokens,
+// are summed in runs of 12 stages (48 steps; from 16 stages) that are added in fp32.  At 30011 tokens,
 // 776 x 771, runs of 64 stages take 59.6 us and are off by 3.8e-6, runs of 12 take 77.9 us and
 // are off by 7.4e-7 (an fp32 product without tensor cores: 2.9e-7).
 struct WgradSegment {
@@ -134,6 +136,17 @@ static __host__ __device__ __forceinline__ bool wgrad_segment(const WgradArgs& a
         i -= n;
     }
     return false;
+}
+
+// The slot that a segment's sums go to where they are kept, and whether they are: those of a
+// part, and of a whole tile's run that others come before or after.
+static __host__ __device__ __forceinline__ int wgrad_slot(const WgradSegment& g, uint32_t pair)
+{
+    return g.slot >= 0 ? g.slot : 2 * ZERO_WG_PAIRS + (int)pair;
+}
+static __host__ __device__ __forceinline__ bool wgrad_kept(const WgradSegment& g)
+{
+    return g.slot >= 0 || !g.first || !g.last;
 }
 
 // Tiles in an order that keeps a wave's panels few: bands of eight tiles along n.
@@ -834,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             float* part = g.slot < 0 ? nullptr : a.slots + (int64_t)g.slot * ZERO_WG_SLOT;
             // where the sums of a tile's or part's earlier runs are kept
-            float* kept = part ? part : a.slots + (int64_t)(2 * ZERO_WG_PAIRS + pair) * ZERO_WG_SLOT;
+            float* kept = wgrad_kept(g) ? a.slots + (int64_t)wgrad_slot(g, pair) * ZERO_WG_SLOT : nullptr;
             if (g.first) sum = part ? 0.0f : column_sum(a, r);
             if (adds_sums(a, j0)) {
                 have = __all_sync(0xFFFFFFFFu, pair_wait(smem_u32(&sh.col_full), (uint32_t)summed & 1u, dead, a.err)) && have;
@@ -1144,14 +1157,43 @@ bool sizes_ok(int64_t tokens, int64_t n, int64_t k)
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t steps_of(int64_t tokens) { return up(tokens, ZERO_WG_TOK); }
 
+// Whether a call on so many stages keeps sums in the workspace: only then are tiles cut into parts,
+// or their stages into runs, and only then does the workspace have slots.  Below, one run of at
+// most 15 stages (60 steps) is off by about 1e-6 where runs of 12 would be by 8e-7.
+bool keeps_sums(int64_t steps) { return steps >= 2 * ZERO_WG_PART; }
+
 // Workspace: the status word (256 bytes), the columns' sums, the parts and runs' sums, dy's copy.
 int64_t round_bytes(int64_t b) { return up(b, 256) * 256; }
 int64_t sums_bytes(int64_t n) { return round_bytes(ZERO_WG_RANGES * n * 4); }
 int64_t parts_bytes(int64_t tokens)
 {
-    return steps_of(tokens) < 2 * ZERO_WG_PART ? 0 : round_bytes(3ll * ZERO_WG_PAIRS * ZERO_WG_SLOT * 4);
+    return keeps_sums(steps_of(tokens)) ? round_bytes((int64_t)ZERO_WG_SLOTS * ZERO_WG_SLOT * 4) : 0;
 }
 int64_t copy_bytes(int64_t tokens, int64_t n) { return round_bytes(tokens * up(n, 8) * 16); }
+
+// The division of a.tokens, a.n and a.k among `pairs` pairs of SMs (units of the last wave: below
+// 80 * 2^25).
+void divide(WgradArgs& a, int pairs)
+{
+    a.pairs = pairs;
+    a.steps = (int)steps_of(a.tokens);
+    a.run = a.grad_dtype == ZERO_FP32 && keeps_sums(a.steps) ? ZERO_WG_RUN : (uint32_t)a.steps;
+    a.tiles_n = (uint32_t)up(a.n, ZERO_WG_TILE);
+    a.tiles_k = (uint32_t)up(a.k, ZERO_WG_TILE);
+    const int64_t tiles = (int64_t)a.tiles_n * a.tiles_k;
+    a.waves = (int)(tiles / a.pairs);
+    a.rest = (int)(tiles % a.pairs);
+    a.rest_pairs = a.rest;
+    const int64_t units = (int64_t)a.rest * a.steps;
+    if (a.rest > 0 && keeps_sums(a.steps)) {
+        const int64_t parts = units / ZERO_WG_PART;
+        a.rest_pairs = (int)(parts < a.rest ? a.rest : parts < a.pairs ? parts : a.pairs);
+    }
+    if (a.rest > 0) {
+        a.share = (uint32_t)(units / a.rest_pairs);
+        a.extra = (uint32_t)(units % a.rest_pairs);
+    }
+}
 
 decltype(&cuTensorMapEncodeTiled) encode()
 {
@@ -1268,25 +1310,11 @@ extern "C" zero_status_t zero_act_wgrad(zero_dtype_t dtype, const void* dy, int6
                    ? ZERO_OK
                    : ZERO_ECUDA;
     }
-    a.pairs = device_pairs();
-    if (a.pairs == 0 || !encode()) return ZERO_ECUDA;
-    a.steps = (int)steps_of(tokens);
-    a.run = grad_dtype == ZERO_FP32 ? ZERO_WG_RUN : (uint32_t)a.steps;
-    a.tiles_n = (uint32_t)up(n, ZERO_WG_TILE);
-    a.tiles_k = (uint32_t)up(k, ZERO_WG_TILE);
-    const int64_t tiles = (int64_t)a.tiles_n * a.tiles_k;
-    a.waves = (int)(tiles / a.pairs);
-    a.rest = (int)(tiles % a.pairs);
-    a.rest_pairs = a.rest;
-    const int64_t units = (int64_t)a.rest * a.steps;        // below 80 * 2^25
-    if (a.rest > 0 && a.steps >= 2 * ZERO_WG_PART) {
-        const int64_t parts = units / ZERO_WG_PART;
-        a.rest_pairs = (int)(parts < a.rest ? a.rest : parts < a.pairs ? parts : a.pairs);
-    }
+    const int pairs = device_pairs();
+    if (pairs == 0 || !encode()) return ZERO_ECUDA;
+    divide(a, pairs);
     WgradJoin join{};
     if (a.rest > 0) {
-        a.share = (uint32_t)(units / a.rest_pairs);
-        a.extra = (uint32_t)(units % a.rest_pairs);
         for (int p = a.rest_pairs - 1; p >= 0; p--) {       // backwards: a tile's first pair is written last
             const uint32_t t0 = wgrad_share(a, p) / a.steps, t1 = (wgrad_share(a, p + 1) - 1) / a.steps;
             for (uint32_t t = t0; t <= t1; t++) {

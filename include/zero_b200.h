@@ -530,7 +530,9 @@ zero_status_t zero_act_load(zero_dtype_t dtype, const void* ckpt, int64_t rows, 
  * the checkpoint of its input.  With xh the checkpoint's values [tokens][k],
  *   dw[i][j] = sum_t dy[t][i] * (xh[t][j] * col_scale[j] + col_shift[j])
  *   db[i]    = sum_t dy[t][i]
- * summed in fp32.  col_scale and col_shift (dtype, [k]; NULL: 1 and 0) are the
+ * summed in fp32: on the tensor cores, whose accumulators cut a sum off at each
+ * step of 16 tokens, over at most 65536 tokens (fp32 gradients: 960), and by
+ * rounded additions beyond.  col_scale and col_shift (dtype, [k]; NULL: 1 and 0) are the
  * weight and bias of a norm whose normalised rows were checkpointed, so one
  * checkpoint serves the norm's backward pass and every layer it feeds.
  *   dtype       fp16 or bf16: dy, col_scale, col_shift.  An fp16 dy needs a

@@ -54,3 +54,12 @@ def test_sums_are_kept_inside_the_workspace(lib, n, k, grad):
                 # dy's copy comes after the slots: up to eight columns' worth of two bytes a token
                 copy = up(tokens * up(n, 8) * 16, 256) * 256
                 assert used + copy <= lib.zero_act_wgrad_workspace(tokens, n, k), (tokens, pairs)
+
+
+def test_an_accumulator_adds_a_bounded_number_of_stages(lib):
+    """12 stages for fp32 gradients (15 where there is one run), 1024 for 16-bit ones."""
+    for n, k in SIZES:
+        for stages in (1, 12, 13, 15, 16, 17, 469, 1024, 1025, 5000, 1 << 16):
+            for pairs in (1, 76):
+                most = {grad: reach(lib, STAGE * stages, n, k, grad, pairs)[2] for grad in (BF16, FP32)}
+                assert most[FP32] <= (stages if stages < 16 else 12) and most[BF16] <= 1024, (stages, pairs, most)

@@ -48,6 +48,9 @@ namespace zero {
 #define ZERO_WG_FEW_WORK (60ll << 20)       // and most products
 #define ZERO_WG_FEW_TOK 32                  // tokens it adds at a time
 #define ZERO_WG_RANGES 32                   // most token ranges that k_wgrad_columns adds
+#ifndef ZERO_WG_WAIT_LIMIT                  // polls before a wait gives up (not those for what is in flight)
+#define ZERO_WG_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
+#endif
 
 // bytes of a stage in one SM: dy rows, codes, exponents; and of widened codes (as dy rows); the
 // column sums of a tile (a row of 128 from each widening warp)
@@ -442,15 +445,31 @@ static __device__ __forceinline__ void arrive_first(uint32_t bar)
 // buffer back must not be made while loads from it are under way, and the barrier unit does not
 // wait for loads before it: x is made of the loaded values.
 static __device__ __forceinline__ int lane_with(uint32_t x) { return __any_sync(0xFFFFFFFFu, x == 0) ? 0 : 1; }
-// Bounded wait: false when it gave up (here or in another warp of this SM).
+// Bounded wait of a lane: false when it gave up (here or in another warp of this SM).
 static __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
-    for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT; it++) {
+    for (uint32_t it = 0; it < ZERO_WG_WAIT_LIMIT; it++) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*dead) return false;
     }
     *dead = 1;
     atomicExch(err, ZERO_ETIMEOUT);
+    return false;
+}
+// The same for a whole warp, whose lanes go on or stop together (votes and shuffles of all lanes
+// follow), so every poll is voted on.  A vote after lanes that polled by themselves took 154 us
+// instead of 146 at 8192 x 6400 x 1600, a loop without a first poll of its own 151.
+static __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
+{
+    if (ZERO_WG_WAIT_LIMIT > 0 && __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+#pragma unroll 1
+    for (uint32_t it = 0; it < ZERO_WG_WAIT_LIMIT; it++) {
+        if (__any_sync(0xFFFFFFFFu, *dead)) return false;
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    }
+    *dead = 1;
+    atomicExch(err, ZERO_ETIMEOUT);
+    __syncwarp();
     return false;
 }
 static __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
@@ -730,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             const int len = g.s1 - g.s0;
             int t = skip;
             for (; t < len; t += GROUPS) {
-                if (!pair_wait(smem_u32(&sh.codes[cl]), cph, dead, a.err)) {
+                if (!warp_wait(smem_u32(&sh.codes[cl]), cph, dead, a.err)) {
                     ok = false;
                     break;
                 }
@@ -751,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
 #pragma unroll
                     for (int u = 0; u < EACH; u++) all |= e[u] | q[u][0][0] | q[u][1][0];
                 if (lane == lane_with(all)) mbar_arrive(smem_u32(&sh.read[cs]));
-                if (f >= 0 && !pair_wait(smem_u32(&sh.done[f]), fph, dead, a.err)) {
+                if (f >= 0 && !warp_wait(smem_u32(&sh.done[f]), fph, dead, a.err)) {
                     ok = false;
                     break;
                 }
@@ -776,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                if (!pair_wait(smem_u32(&sh.rows[rl]), rph, dead, a.err)) {
+                if (!warp_wait(smem_u32(&sh.rows[rl]), rph, dead, a.err)) {
                     ok = false;
                     break;
                 }
@@ -818,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
             skip = t - len;
             if (sums && ok) {
                 // the two lanes of a warp with the same columns, then a row of 128 from each warp
-                if (summed >= 1 && !pair_wait(smem_u32(&sh.col_empty), (uint32_t)(summed - 1) & 1u, dead, a.err)) break;
+                if (summed >= 1 && !warp_wait(smem_u32(&sh.col_empty), (uint32_t)(summed - 1) & 1u, dead, a.err)) break;
                 float v[8];
 #pragma unroll
                 for (int c = 0; c < 4; c++) unpack2(total[c], v[2 * c], v[2 * c + 1]);

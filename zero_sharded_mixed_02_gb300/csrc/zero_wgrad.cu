@@ -815,15 +815,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_WG_THREADS, 1)
                         }
                     }
                 }
-                uint32_t last = 0;
-                if (sums)
+                int one = 0;
+                if (sums) {
+                    uint32_t last = 0;
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         float lo, hi;
                         unpack2(total[c], lo, hi);
                         last |= __float_as_uint(lo);
                     }
-                if (lane == lane_with(last)) arrive_first(smem_u32(&sh.ready[b]));
+                    one = lane_with(last);
+                }
+                // one lane arrives for all: their stores and proxy fences come before (a vote orders
+                // no memory)
+                __syncwarp();
+                if (lane == one) arrive_first(smem_u32(&sh.ready[b]));
                 b = (b + GROUPS) % ZERO_WG_WIDE;
                 f += GROUPS;
                 if (f >= ZERO_WG_WIDE * GROUPS) { f -= ZERO_WG_WIDE * GROUPS; fph ^= 1u; }

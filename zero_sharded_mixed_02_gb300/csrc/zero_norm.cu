@@ -171,9 +171,15 @@ bool matrix_ok(const void* p, int64_t ld, int64_t cols, int dtype)
     return p && aligned_to(p, elem(dtype)) && ld >= cols && ld <= (1ll << 31);
 }
 
+// Rows of a gate group, at most all of them (and at least one), and the number of groups.
+int64_t group_of(const zero_norm_t& d)
+{
+    const int64_t rows = d.rows > 0 ? d.rows : 1;
+    return d.group_rows == 0 || d.group_rows > rows ? rows : d.group_rows;
+}
 int64_t groups_of(const zero_norm_t& d)
 {
-    return d.group_rows == 0 || d.rows == 0 ? 1 : (d.rows + d.group_rows - 1) / d.group_rows;
+    return d.rows == 0 ? 1 : (d.rows + group_of(d) - 1) / group_of(d);
 }
 
 bool description_ok(const zero_norm_t* d)
@@ -265,7 +271,7 @@ extern "C" zero_status_t zero_norm_forward(const zero_norm_t* norm, const void* 
     a.stats = stats;
     a.rows = (uint32_t)d.rows;
     a.ldh = (uint32_t)ldh; a.ldy = (uint32_t)ldy; a.ldho = (uint32_t)ldho; a.ldx = (uint32_t)ldx;
-    a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
+    a.group = (uint32_t)group_of(d);
     a.cols = (int)d.cols;
     a.wide = (uint32_t)act_wide(d.cols);
     a.stride = (uint32_t)act_stride(d.cols);
@@ -345,7 +351,7 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
         a.stats = stats;
         a.rows = (uint32_t)d.rows;
         a.lddho = (uint32_t)lddho; a.lddx = (uint32_t)lddx; a.lddh = (uint32_t)lddh; a.lddy = (uint32_t)lddy;
-        a.group = (uint32_t)(d.group_rows == 0 || d.group_rows > d.rows ? d.rows : d.group_rows);
+        a.group = (uint32_t)group_of(d);
         a.cols = (int)d.cols;
         a.wide = (uint32_t)act_wide(d.cols);
         a.stride = (uint32_t)act_stride(d.cols);
@@ -406,7 +412,7 @@ extern "C" zero_status_t zero_norm_backward(const zero_norm_t* norm, const void*
     a.post_w = d.post_w; a.post_b = d.post_b;
     a.dpost_w = dpost_w; a.dpost_b = dpost_b; a.dgate = dgate; a.dpre_w = dpre_w; a.dpre_b = dpre_b;
     a.rows = d.rows;
-    a.group = d.group_rows ? d.group_rows : d.rows > 0 ? d.rows : 1;
+    a.group = group_of(d);
     a.groups = groups_of(d);
     a.cols = (int)d.cols;
     a.blocks = (int)blocks;

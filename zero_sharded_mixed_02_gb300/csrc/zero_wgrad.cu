@@ -564,6 +564,8 @@ static __device__ __forceinline__ uint32_t code_scale(uint32_t e)
 // of five stages 13 %).  A stage's way through them takes about 2300 cycles (850 for the loads,
 // 1100 to widen, the arrivals), its products 512.
 static_assert((ZERO_WG_WIDENERS / ZERO_WG_GROUPS / 4) % 8 == 0, "a thread's tokens keep their swizzle");
+static_assert(ZERO_WG_GROUPS <= ZERO_WG_CODES && ZERO_WG_GROUPS <= ZERO_WG_STAGES && ZERO_WG_GROUPS <= ZERO_WG_WIDE,
+              "every group's stage has a place in each ring");
 
 struct WgradShared {
     uint64_t rows[ZERO_WG_STAGES * ZERO_WG_GROUPS];     // a stage's dy rows have come

@@ -645,6 +645,104 @@ zero_status_t zero_norm_backward(const zero_norm_t* norm, const void* dh_out, in
 /* Workspace bytes of zero_norm_backward; 0 on an invalid description. */
 uint64_t zero_norm_workspace(const zero_norm_t* norm);
 
+/* ---- losses over the vocabulary ----------------------------------------------- */
+
+/* Most rows, columns, vocabulary and teacher's entries a row of the head's losses. */
+#define ZERO_HEAD_MAX_ROWS 65536
+#define ZERO_HEAD_MAX_COLS 16384
+#define ZERO_HEAD_MAX_VOCAB (1 << 24)
+#define ZERO_HEAD_MAX_TOP 256
+
+/* The end of a model: the last norm's rows x [rows][cols], the head's weights w
+ * [vocab][cols], the logits z = x w^T and a loss of each row's softmax.  The logits
+ * are computed tile by tile and never kept, neither by the forward pass nor by the
+ * backward pass, which computes them once more, a piece of the vocabulary at a time;
+ * its gradients go where they are wanted (dw: e.g. the tensor's place in a rank's
+ * gradient row).
+ *   dtype        fp16 or bf16: x, w, dx, dw.
+ *   piece        columns of the vocabulary that the backward pass keeps the logits'
+ *                gradient of at a time (2 rows piece bytes of workspace), rounded up
+ *                to 256, at most 65536; 0: the library's choice (about 512 MB).
+ *   z_loss       weight of the squared log-sum-exp (0: none).
+ *   top, top_dtype, temperature, hard, soft   zero_distill_* only: the teacher's
+ *                entries of a row, the type of its logits (fp16, bf16, fp32), the
+ *                temperature (> 0) and the weights of the two parts of the loss. */
+typedef struct {
+    int32_t dtype, top, top_dtype;
+    float   temperature, hard, soft, z_loss;
+    int64_t rows, cols, vocab, piece;
+} zero_head_t;
+
+/* Softmax cross entropy.  With l = log sum_j exp(z_j) of row i and y its label,
+ *   loss[i] = l - z_y + z_loss l^2,   lse[i] = l.
+ * A row with a negative label takes no part: its x is not read, its loss and lse are
+ * 0.  A label >= vocab gives NaN (loss and lse; the backward pass then gives NaN in
+ * the row's dx and all of dw).
+ *   labels   [rows] int32.     loss, lse   [rows] fp32.
+ *   sums     two fp32 (NULL: not wanted): the sum of the losses, and the number of
+ *            rows that take part.
+ *   work     zero_head_workspace(head) bytes, 16-byte aligned, contents ignored; calls
+ *            whose executions overlap need one each.
+ * Rows of x and w lie ldx and ldw elements apart and need the alignment of their
+ * element; rows of w that are not 16-byte aligned are first copied to the workspace,
+ * a piece at a time.  The logits are fp32 sums of exact products, added by the tensor
+ * cores in runs of at most 768 columns that are then added in fp32.  Sums are taken
+ * in a fixed order: equal inputs give equal bits.  Asynchronous.  rows = 0 is accepted
+ * (sums are 0).  A bounded device wait that gives up (none should) sets the first
+ * int32 of `work` to ZERO_ETIMEOUT and gives NaN.
+ * Errors: ZERO_EINVAL (description: types; rows in [0, ZERO_HEAD_MAX_ROWS], cols in [1,
+ * ZERO_HEAD_MAX_COLS], vocab in [1, ZERO_HEAD_MAX_VOCAB], piece >= 0, top in [0,
+ * ZERO_HEAD_MAX_TOP]; weights that are not finite, temperature not > 0; strides below cols
+ * or above 2^31; null or misaligned pointer), ZERO_ECUDA. */
+zero_status_t zero_ce_forward(const zero_head_t* head, const void* x, int64_t ldx, const void* w,
+                              int64_t ldw, const int32_t* labels, float* loss, float* lse,
+                              float* sums, void* work, void* stream);
+
+/* Its gradients: with g_i = scale * row_grad[i] / *divisor (row_grad [rows] fp32, NULL: 1;
+ * divisor one fp32 on the device, e.g. sums + 1 for a mean, NULL: 1; g_i = 0 if it is 0),
+ *   dz_ij = g_i (p_ij (1 + 2 z_loss l_i) - [j = y_i]),   p_ij = exp(z_ij - lse[i])
+ *   dx_i  = sum_j dz_ij w_j,   dw_j = sum_i dz_ij x_i.
+ * lse is what the forward pass wrote.  Rows that take no part, and rows with g_i = 0,
+ * have dx = 0 and are not read.  dz is rounded once to dtype, relative to its row's own power of
+ * two (so neither a loss scale nor small weights cost bits), all sums are fp32, and dx
+ * and dw are rounded once.
+ *   dx, dw      rows lddx, lddw apart, aligned to their element (16-byte aligned rows are
+ *               written fastest); either may be NULL: not wanted.  dx may be x itself
+ *               (lddx = ldx).
+ *   accumulate  1: dw is added to what it holds (one rounding); 0: overwritten.
+ * rows = 0 is accepted (dw is 0, or nothing is added).  The rest as zero_ce_forward. */
+zero_status_t zero_ce_backward(const zero_head_t* head, const void* x, int64_t ldx, const void* w,
+                               int64_t ldw, const int32_t* labels, const float* lse,
+                               const float* row_grad, float scale, const float* divisor, void* dx,
+                               int64_t lddx, void* dw, int64_t lddw, int accumulate, void* work,
+                               void* stream);
+
+/* Distillation from a teacher's top logits: a row has head->top entries (top_index[i][k],
+ * top_logit[i][k]), rows ldt apart, in any order.  An entry with a negative index or a logit of
+ * -inf is none (a teacher that kept fewer); entries of one index are added.  With T the
+ * temperature, q = softmax of the row's logits / T over its entries and
+ * l_T = log sum_j exp(z_j / T),
+ *   loss[i] = soft T^2 sum_k q_k (log q_k - z_k / T + l_T) + hard (l - z_y + z_loss l^2)
+ *   lse[i]  = {l_T, l}   ([rows][2]; l is 0 without labels)
+ *   dz_ij   = g_i (soft T (exp(z_ij / T - l_T) - q_j) + hard (p_ij (1 + 2 z_loss l) - [j = y]))
+ * labels may be NULL: no second part, and a row without an entry takes no part.  With
+ * labels a row with a negative label takes no part, and one without an entry has no first
+ * part.  An index >= vocab of an entry gives NaN as such a label does.  The rest as zero_ce_forward
+ * and zero_ce_backward; also ZERO_EINVAL: head->top < 1, ldt < head->top. */
+zero_status_t zero_distill_forward(const zero_head_t* head, const void* x, int64_t ldx,
+                                   const void* w, int64_t ldw, const int32_t* top_index,
+                                   const void* top_logit, int64_t ldt, const int32_t* labels,
+                                   float* loss, float* lse, float* sums, void* work, void* stream);
+zero_status_t zero_distill_backward(const zero_head_t* head, const void* x, int64_t ldx,
+                                    const void* w, int64_t ldw, const int32_t* top_index,
+                                    const void* top_logit, int64_t ldt, const int32_t* labels,
+                                    const float* lse, const float* row_grad, float scale,
+                                    const float* divisor, void* dx, int64_t lddx, void* dw,
+                                    int64_t lddw, int accumulate, void* work, void* stream);
+
+/* Workspace bytes of the four calls above; 0 on an invalid description. */
+uint64_t zero_head_workspace(const zero_head_t* head);
+
 /* ---- memory ledger and communication volume ------------------------------- */
 
 /* Bytes of model state one rank holds ([L18] 1.2, 2.1; [Z026] 2; [L32] 2.1,

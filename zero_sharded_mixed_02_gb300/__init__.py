@@ -41,6 +41,8 @@ ENTRY_POINTS = (
     "zero_checkpoint_save", "zero_checkpoint_load", "zero_offload_step", "zero_cpu_adam",
     "zero_act_row_bytes", "zero_act_save", "zero_act_load", "zero_act_wgrad",
     "zero_act_wgrad_workspace", "zero_norm_forward", "zero_norm_backward", "zero_norm_workspace",
+    "zero_ce_forward", "zero_ce_backward", "zero_distill_forward", "zero_distill_backward",
+    "zero_head_workspace",
 )
 
 
@@ -84,6 +86,19 @@ def norm(dtype, rows, cols, res_dtype=None, post=ZERO_NORM_NONE, pre=ZERO_NORM_R
     return zero_norm_t(dtype, dtype if res_dtype is None else res_dtype, post, pre, rows, cols,
                        group_rows, eps, alpha, _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(pre_w),
                        _ptr(pre_b))
+
+
+class zero_head_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("top", ctypes.c_int32), ("top_dtype", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("hard", ctypes.c_float), ("soft", ctypes.c_float),
+                ("z_loss", ctypes.c_float), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("piece", ctypes.c_int64)]
+
+
+def head(dtype, rows, cols, vocab, piece=0, z_loss=0.0, top=0, top_dtype=ZERO_FP32, temperature=1.0,
+         hard=1.0, soft=1.0) -> zero_head_t:
+    """Description of a vocabulary head for zero_ce_* and zero_distill_*."""
+    return zero_head_t(dtype, top, top_dtype, temperature, hard, soft, z_loss, rows, cols, vocab, piece)
 
 
 _lock = threading.Lock()
@@ -156,6 +171,13 @@ def lib():
                                             ctypes.c_int, _P, _P, _P, _P, _P, ctypes.c_int, _P,
                                             _P]),
                 "zero_norm_workspace": (_U64, [_P]),
+                "zero_ce_forward": (st, [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P]),
+                "zero_ce_backward": (st, [_P, _P, _I64, _P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _I64,
+                                          _P, _I64, ctypes.c_int, _P, _P]),
+                "zero_distill_forward": (st, [_P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P]),
+                "zero_distill_backward": (st, [_P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P,
+                                               ctypes.c_float, _P, _P, _I64, _P, _I64, ctypes.c_int, _P, _P]),
+                "zero_head_workspace": (_U64, [_P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -408,6 +430,41 @@ def zero_norm_backward(norm: zero_norm_t, dh_out, lddho: int, dx, lddx: int, ckp
 
 def zero_norm_workspace(norm: zero_norm_t) -> int:
     return lib().zero_norm_workspace(ctypes.byref(norm))
+
+
+def zero_ce_forward(head: zero_head_t, x, ldx: int, w, ldw: int, labels, loss, lse, sums=None, work=None,
+                    stream=0) -> None:
+    """work: zero_head_workspace(head) bytes."""
+    _check(lib().zero_ce_forward(ctypes.byref(head), _ptr(x), ldx, _ptr(w), ldw, _ptr(labels), _ptr(loss),
+                                 _ptr(lse), _ptr(sums), _ptr(work), _ptr(stream)), "zero_ce_forward")
+
+
+def zero_ce_backward(head: zero_head_t, x, ldx: int, w, ldw: int, labels, lse, row_grad, scale: float,
+                     divisor, dx, lddx: int, dw, lddw: int, accumulate: int = 0, work=None,
+                     stream=0) -> None:
+    _check(lib().zero_ce_backward(ctypes.byref(head), _ptr(x), ldx, _ptr(w), ldw, _ptr(labels), _ptr(lse),
+                                  _ptr(row_grad), scale, _ptr(divisor), _ptr(dx), lddx, _ptr(dw), lddw,
+                                  accumulate, _ptr(work), _ptr(stream)), "zero_ce_backward")
+
+
+def zero_distill_forward(head: zero_head_t, x, ldx: int, w, ldw: int, top_index, top_logit, ldt: int,
+                         labels, loss, lse, sums=None, work=None, stream=0) -> None:
+    _check(lib().zero_distill_forward(ctypes.byref(head), _ptr(x), ldx, _ptr(w), ldw, _ptr(top_index),
+                                      _ptr(top_logit), ldt, _ptr(labels), _ptr(loss), _ptr(lse),
+                                      _ptr(sums), _ptr(work), _ptr(stream)), "zero_distill_forward")
+
+
+def zero_distill_backward(head: zero_head_t, x, ldx: int, w, ldw: int, top_index, top_logit, ldt: int,
+                          labels, lse, row_grad, scale: float, divisor, dx, lddx: int, dw, lddw: int,
+                          accumulate: int = 0, work=None, stream=0) -> None:
+    _check(lib().zero_distill_backward(ctypes.byref(head), _ptr(x), ldx, _ptr(w), ldw, _ptr(top_index),
+                                       _ptr(top_logit), ldt, _ptr(labels), _ptr(lse), _ptr(row_grad),
+                                       scale, _ptr(divisor), _ptr(dx), lddx, _ptr(dw), lddw, accumulate,
+                                       _ptr(work), _ptr(stream)), "zero_distill_backward")
+
+
+def zero_head_workspace(head: zero_head_t) -> int:
+    return lib().zero_head_workspace(ctypes.byref(head))
 
 
 def zero_state_bytes(psi: int, nd: int, stage: int, K: int = 12) -> int:

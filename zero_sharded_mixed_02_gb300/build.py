@@ -24,7 +24,8 @@ SOURCES = ["zero_abi.cu", "zero_step_fp16.cu", "zero_step_bf16.cu", "zero_step_q
            "zero_norm_forward_fp16.cu", "zero_norm_forward_fp16_fp32.cu",
            "zero_norm_forward_bf16.cu", "zero_norm_forward_bf16_fp32.cu",
            "zero_norm_backward_fp16.cu", "zero_norm_backward_fp16_fp32.cu",
-           "zero_norm_backward_bf16.cu", "zero_norm_backward_bf16_fp32.cu"]
+           "zero_norm_backward_bf16.cu", "zero_norm_backward_bf16_fp32.cu",
+           "zero_head.cu", "zero_head_fp16.cu", "zero_head_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,1247 @@
+// zero_head.cuh -- kernels of the vocabulary head's losses (include/zero_b200.h).
+//
+// The logits z = x w^T (rows x vocab) are never kept.  All products run on the tensor cores, a
+// pair of SMs (a cluster of two) on a 256 x 256 tile, 64 steps of the contracted axis a stage:
+//   LOGITS    z tile by tile; each tile leaves a row's maximum and sum of exponentials
+//   GRADIENT  the same tiles again; each leaves its gradient dz (16 bits, scaled by a power of
+//             two a row) in the workspace, a piece of the vocabulary at a time
+//   INPUT     dx += dz w of a piece, summed over pieces in fp32
+//   WEIGHT    dw = dz^T x of a piece
+// Rows that take no part are left out before the first product: a pass over the rows packs the
+// others (aligned, padded with zeros to a whole stage), so what their x holds is not read, and
+// every product's rows are the counted ones.
+#pragma once
+
+#include <cuda.h>
+
+#include "zero_b200.h"
+#include "zero_common.cuh"
+#include "zero_pair.cuh"
+
+namespace zero {
+
+#define ZERO_HD_TILE 256                     // rows and columns of a pair's tile
+#define ZERO_HD_STEP 64                      // contracted elements of a stage
+#define ZERO_HD_STAGES 6
+#define ZERO_HD_SIDE 16384                   // bytes of a stage's operand in one SM
+#define ZERO_HD_WRITERS 8                    // warps that read the accumulators
+#define ZERO_HD_THREADS (128 + 32 * ZERO_HD_WRITERS)    // warp 0 loads, 1 products, from 4 output
+#define ZERO_HD_ROWS 2048                    // bytes in which an output warp turns its rows
+#define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + ZERO_HD_WRITERS * ZERO_HD_ROWS + 1024)
+#define ZERO_HD_PAIRS 80                     // most pairs that share a launch's work
+#define ZERO_HD_PART 8                       // least stages of a part of a cut tile
+#define ZERO_HD_RUN 12                       // stages an accumulator adds for the loss
+#define ZERO_HD_CHUNK 1024                   // rows whose counted ones are numbered by one block
+#define ZERO_HD_SLOT (ZERO_HD_TILE * ZERO_HD_TILE)      // floats of a tile's sums
+#define ZERO_HD_SCALE 14                     // dz is kept times 2^14 over its row's power of two
+#define ZERO_HD_NONE 0x7FFFFFFF              // column of no target
+#ifndef ZERO_HD_WAIT_LIMIT                   // polls before a wait gives up
+#define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
+#endif
+
+enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT = 3 };
+
+// What the passes over the rows leave for the rest, at the head of the workspace.
+struct HeadState {
+    int32_t err;                             // ZERO_ETIMEOUT once a wait gave up
+    uint32_t ticket;
+    int32_t rows;                            // counted rows
+    int32_t top;                             // largest exponent of their gradients' scales
+};
+
+// A counted row.  Gradients: dz = c1 2^(k1 z - l1) + c2 2^(k2 z - l2) - weight at the targets.
+struct __align__(16) HeadRow {
+    float c1, l1, c2, l2;
+};
+
+struct HeadArgs {
+    int64_t rows, ldx, ldw, ldt, lddx, lddw;
+    int cols, vocab, top, slots;             // slots: targets of a row (top, and one for the label)
+    int top_dtype, two, backward;            // two: both log-sum-exps are needed
+    float temperature, hard, soft, z_loss, k1, k2, scale;
+    const uint16_t *x, *w;
+    const int32_t *labels, *index;
+    const void* logit;
+    const float *weight, *divisor, *kept;    // the backward pass's row weights, divisor, log-sum-exps
+    float *loss, *lse, *sums;
+    uint16_t *dx, *dw;
+    int accumulate, vec;
+    // workspace
+    HeadState* st;
+    uint32_t* mask;                          // counted rows, a bit each
+    int32_t *count, *most;                   // of a chunk of rows: how many; their largest exponent
+    int32_t *map, *exponent;                 // counted row -> row, its scale's exponent
+    HeadRow* info;                           // (forward: c1 is the loss's constant part, c2 the teacher's share)
+    int32_t* column;                         // targets of a counted row, ascending, and their weights
+    float *target, *found;                   // found: their logits
+    double* partial;
+    float2* part;                            // [tiles of the vocabulary][npad]: maximum, sum
+    float* part2;                            // the sum at the temperature
+    uint16_t *xp, *xs, *wp, *dz;             // packed rows, the same scaled, weights where repacked, dz
+    float *acc, *parts;
+    int64_t npad, pitch;                     // packed rows, columns of dz
+    int wide;                                // columns of packed rows
+    // this launch
+    int pairs, v0, count_v, wy;              // first column of the piece, columns, its first row in the weights' map
+    int first, last;                         // piece
+    int band;                                // row tiles that are taken together
+};
+
+// ---- the division of the work ------------------------------------------------------
+struct HeadShape {
+    uint32_t tm, tn, steps, runs, run, waves, rest, rest_pairs, share, extra;
+};
+struct HeadSegment {
+    uint32_t tile;
+    int32_t s0, s1;
+    int slot;                                // of a part of a cut tile, else -1
+    bool first, last;                        // run of the tile
+};
+
+static __host__ __device__ __forceinline__ uint32_t head_up(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+
+// Tiles along the left operand's rows (tm) and the right one's (tn), and how `pairs` pairs share
+// them: whole waves, then the rest, whose tiles are cut along the contracted axis into equal parts
+// where that is long enough to pay for joining them (INPUT, WEIGHT).
+template <int PASS>
+static __host__ __device__ __forceinline__ HeadShape head_shape(const HeadArgs& a, int counted)
+{
+    HeadShape s;
+    const uint32_t n = counted > 0 ? counted : 1;
+    const uint32_t rows = head_up(n, ZERO_HD_TILE), words = head_up(a.count_v, ZERO_HD_TILE), wide = head_up(a.cols, ZERO_HD_TILE);
+    s.tm = PASS == HEAD_WEIGHT ? words : rows;
+    s.tn = PASS <= HEAD_GRADIENT ? words : wide;
+    s.steps = head_up(PASS <= HEAD_GRADIENT ? a.cols : PASS == HEAD_INPUT ? a.count_v : n, ZERO_HD_STEP);
+    s.runs = PASS == HEAD_LOGITS ? head_up(s.steps, ZERO_HD_RUN) : 1;
+    s.run = head_up(s.steps, s.runs);
+    s.runs = head_up(s.steps, s.run);
+    const uint32_t tiles = s.tm * s.tn;
+    s.waves = tiles / a.pairs;
+    s.rest = tiles % a.pairs;
+    s.rest_pairs = s.rest;
+    s.share = s.extra = 0;
+    if (s.rest > 0) {
+        const uint32_t units = s.rest * s.steps;
+        if (PASS >= HEAD_INPUT && s.steps >= 2 * ZERO_HD_PART) {
+            const uint32_t parts = units / ZERO_HD_PART;
+            s.rest_pairs = parts < s.rest ? s.rest : parts < (uint32_t)a.pairs ? parts : a.pairs;
+        }
+        s.share = units / s.rest_pairs;
+        s.extra = units % s.rest_pairs;
+    }
+    return s;
+}
+
+// First unit (stage of a tile of the last wave) of a pair's share, and the pair that has a unit.
+static __host__ __device__ __forceinline__ uint32_t head_share(const HeadShape& s, uint32_t pair)
+{
+    return pair * s.share + (pair < s.extra ? pair : s.extra);
+}
+static __host__ __device__ __forceinline__ uint32_t head_owner(const HeadShape& s, uint32_t unit)
+{
+    const uint32_t large = s.extra * (s.share + 1);
+    return unit < large ? unit / (s.share + 1) : s.extra + (unit - large) / s.share;
+}
+
+// Segment i of a pair; false past its last.
+template <int PASS>
+static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, const HeadShape& s, uint32_t pair, uint32_t i,
+                                                             HeadSegment& g)
+{
+    if (i < s.waves * s.runs) {
+        const uint32_t w = s.runs == 1 ? i : i / s.runs, r = i - w * s.runs;
+        g.tile = w * a.pairs + pair;
+        g.s0 = r * s.run;
+        g.last = r + 1 == s.runs;
+        g.s1 = g.last ? s.steps : g.s0 + s.run;
+        g.first = r == 0;
+        g.slot = -1;
+        return true;
+    }
+    i -= s.waves * s.runs;
+    if (pair >= s.rest_pairs) return false;
+    if (PASS <= HEAD_GRADIENT) {             // whole tiles
+        if (i >= s.runs) return false;
+        g.tile = s.waves * a.pairs + pair;
+        g.s0 = i * s.run;
+        g.last = i + 1 == s.runs;
+        g.s1 = g.last ? s.steps : g.s0 + s.run;
+        g.first = i == 0;
+        g.slot = -1;
+        return true;
+    }
+    const uint32_t u0 = head_share(s, pair), u1 = head_share(s, pair + 1), t = u0 / s.steps + i;
+    uint32_t b = t * s.steps, e = b + s.steps;
+    if (b >= u1) return false;               // a share lies in two tiles at most
+    b = b > u0 ? b : u0;
+    e = e < u1 ? e : u1;
+    g.tile = s.waves * a.pairs + t;
+    g.slot = e - b == s.steps ? -1 : (int)(2 * pair + i);
+    g.s0 = b - t * s.steps;
+    g.s1 = e - t * s.steps;
+    g.first = g.last = true;
+    return true;
+}
+
+// Tiles of the logits: bands of row tiles that stay in L2 while the weights pass by once a band;
+// of the products: bands of eight, which keep a wave's panels few.
+static __host__ __device__ __forceinline__ void head_place(uint32_t band, const HeadShape& s, uint32_t tile, uint32_t& i, uint32_t& j)
+{
+    const uint32_t b = tile / (band * s.tn), in = tile - b * band * s.tn;
+    const uint32_t high = s.tm - b * band < band ? s.tm - b * band : band;
+    j = in / high;
+    i = b * band + (in - j * high);
+}
+template <int PASS>
+static __host__ __device__ __forceinline__ uint32_t head_band(const HeadArgs& a) { return PASS <= HEAD_GRADIENT ? a.band : 8; }
+
+// Columns that are multiplied of a products' tile at column tile j: half a tile at the right edge where that is
+// enough (each SM's part is then one whole 64-column group of the operand's layout).
+template <int PASS>
+static __device__ __forceinline__ int head_width(const HeadArgs& a, uint32_t j)
+{
+    return PASS <= HEAD_GRADIENT || a.cols - (int)j * ZERO_HD_TILE > ZERO_HD_TILE / 2 ? ZERO_HD_TILE : ZERO_HD_TILE / 2;
+}
+
+// ---- scalars -------------------------------------------------------------------------
+static __device__ __forceinline__ float power2(int e)       // 2^e, 0 below the normal range
+{
+    return e < -126 ? 0.0f : __uint_as_float((uint32_t)(e + 127) << 23);
+}
+static __device__ __forceinline__ float exp2_fast(float x)  // within 2 ulp
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+static __device__ __forceinline__ float teacher_logit(const HeadArgs& a, int64_t row, int k)
+{
+    const int64_t i = row * a.ldt + k;
+    if (a.top_dtype == 2) return __ldg(static_cast<const float*>(a.logit) + i);
+    const uint16_t u = __ldg(static_cast<const uint16_t*>(a.logit) + i);
+    return a.top_dtype == 0 ? widen1<0>(u) : widen1<1>(u);
+}
+static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row, int k)
+{
+    return __ldg(a.index + row * a.ldt + k) >= 0 && teacher_logit(a, row, k) != __uint_as_float(0xFF800000u);
+}
+
+// The scale of a row's gradient: scale * weight / divisor (0 where the divisor is).
+static __device__ __forceinline__ float row_scale(const HeadArgs& a, int64_t row)
+{
+    float s = a.scale * (a.weight ? __ldg(a.weight + row) : 1.0f);
+    if (a.divisor) {
+        const float d = __ldg(a.divisor);
+        s = d == 0.0f ? 0.0f : s / d;
+    }
+    return s;
+}
+// Factors of the two softmaxes in a row's gradient before the row's power of two, and a bound of |dz|.
+static __device__ __forceinline__ void row_factors(const HeadArgs& a, int64_t row, float& s, float& hard, float& soft)
+{
+    s = row_scale(a, row);
+    hard = 0.0f;
+    if (a.labels) {
+        const float l = a.index ? __ldg(a.kept + 2 * row + 1) : __ldg(a.kept + row);
+        hard = s * a.hard * (1.0f + 2.0f * a.z_loss * l);
+    }
+    soft = a.index ? s * a.soft * a.temperature : 0.0f;
+}
+static __device__ __forceinline__ float factors_bound(const HeadArgs& a, float s, float hard, float soft)
+{
+    return fabsf(hard) + fabsf(soft) + fabsf(s) * ((a.labels ? fabsf(a.hard) : 0.0f) + (a.index ? fabsf(a.soft) * a.temperature : 0.0f));
+}
+// Exponent of a bound, kept where 2^(14 - e) and its inverse are normal; of an inf or a NaN, 0.
+static __device__ __forceinline__ int bound_exponent(float b)
+{
+    const int e = (int)(__float_as_uint(b) >> 23) - 127;
+    return e == 128 ? 0 : e < -112 ? -112 : e;
+}
+
+// ---- the rows ------------------------------------------------------------------------
+// Which rows are counted, and their gradients' largest power of two: a block takes a chunk of
+// 1024 rows, a warp 32 of them.
+static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant__ HeadArgs a)
+{
+    __shared__ int32_t counts[32], tops[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * ZERO_HD_CHUNK + threadIdx.x;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.st->err = 0;
+        a.st->ticket = 0;
+    }
+    bool in = row < a.rows;
+    if (a.labels) {
+        in = in && __ldg(a.labels + row) >= 0;
+    } else {                                 // rows of which the teacher has kept something
+        uint32_t any = 0;
+        for (int r = 0; r < 32; r++) {
+            const int64_t of = row - lane + r;
+            bool has = false;
+            for (int k = lane; of < a.rows && k < a.top; k += 32) has = has || has_entry(a, of, k);
+            any |= (uint32_t)(__any_sync(0xFFFFFFFFu, has) != 0) << r;
+        }
+        in = any >> lane & 1;
+    }
+    int e = -1000;
+    if (in && a.backward) {
+        float s, hard, soft;
+        row_factors(a, row, s, hard, soft);
+        const float b = factors_bound(a, s, hard, soft);
+        in = !(b == 0.0f);
+        if (in && b - b == 0.0f) e = bound_exponent(b);
+    }
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+    e = __reduce_max_sync(0xFFFFFFFFu, e);
+    if (lane == 0) {
+        a.mask[row >> 5] = m;
+        counts[warp] = __popc(m);
+        tops[warp] = e;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int c = __reduce_add_sync(0xFFFFFFFFu, counts[lane]), t = __reduce_max_sync(0xFFFFFFFFu, tops[lane]);
+        if (lane == 0) {
+            a.count[blockIdx.x] = c;
+            a.most[blockIdx.x] = t;
+        }
+    }
+}
+
+// The targets of a row, ascending and without repetitions: the teacher's entries and the label.
+// A warp's; `cols` and `vals` are its shared memory.  An entry leads if none before it has its
+// column, and takes the weights of all that have it; its place is the number of leaders of smaller columns.
+static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t at, int* cols, float* vals)
+{
+    const int lane = threadIdx.x & 31, n = a.slots;
+    uint32_t leads = 0;                                      // bit i: this lane's i-th entry
+    int leaders = 0;
+    for (int e = lane, i = 0; e < n; e += 32, i++) {
+        const int col = cols[e];
+        bool first = col != ZERO_HD_NONE;
+        for (int f = 0; f < e; f++) first = first && cols[f] != col;
+        leads |= (uint32_t)first << i;
+    }
+    __syncwarp();
+    for (int e = lane, i = 0; e < n; e += 32, i++) {
+        if (!(leads >> i & 1)) continue;
+        const int col = cols[e];
+        float w = 0.0f;
+        for (int f = e; f < n; f++)
+            if (cols[f] == col) w += vals[f];
+        vals[n + e] = w;
+    }
+    __syncwarp();
+    for (int e = lane, i = 0; e < n; e += 32, i++)
+        if (!(leads >> i & 1)) cols[e] = ZERO_HD_NONE;
+    __syncwarp();
+    for (int e = lane, i = 0; e < n; e += 32, i++) {
+        if (!(leads >> i & 1)) continue;
+        const int col = cols[e];
+        int rank = 0;
+        for (int f = 0; f < n; f++) rank += cols[f] < col;
+        a.column[at + rank] = col;
+        a.target[at + rank] = vals[n + e];
+    }
+    leaders = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)__popc(leads));
+    for (int e = leaders + lane; e < n; e += 32) {
+        a.column[at + e] = ZERO_HD_NONE;
+        a.target[at + e] = 0.0f;
+    }
+}
+
+// Packs the counted rows and what belongs to them: a warp a row, eight rows a block; rows past the
+// last counted one are zeros up to a whole tile.
+template <int DT>
+__global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadArgs a)
+{
+    extern __shared__ int32_t entries_of[];                 // a warp's targets: columns, weights, added weights
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+    const int chunks = (int)((a.rows + ZERO_HD_CHUNK - 1) / ZERO_HD_CHUNK);
+    int mine = (int)(row < a.rows ? row >> 10 : chunks), before = 0, all = 0, top = -1000;
+    for (int c = lane; c < chunks; c += 32) {
+        const int n = a.count[c];
+        all += n;
+        if (c < mine) before += n;
+        top = max(top, a.most[c]);
+    }
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.st->rows = all;
+        a.st->top = top == -1000 ? 0 : top;
+    }
+    if (top == -1000) top = 0;
+    int64_t at;                                             // packed row
+    bool counted = false;
+    if (row < a.rows) {
+        const int in = (int)(row & 1023), word = in >> 5;
+        const uint32_t w = lane <= word ? a.mask[(row >> 10 << 5) + lane] : 0;
+        const uint32_t below = lane < word ? w : w & ((1u << (in & 31)) - 1);
+        at = before + __reduce_add_sync(0xFFFFFFFFu, (uint32_t)__popc(below));
+        counted = __shfl_sync(0xFFFFFFFFu, w, word) >> (in & 31) & 1;
+        if (!counted) {
+            if (a.backward) {
+                if (a.dx)
+                    for (int c = lane; c < a.cols; c += 32) a.dx[row * a.lddx + c] = 0;
+            } else if (lane == 0) {
+                a.loss[row] = 0.0f;
+                if (a.index) a.lse[2 * row] = a.lse[2 * row + 1] = 0.0f;
+                else a.lse[row] = 0.0f;
+            }
+            return;
+        }
+    } else {
+        at = all + (row - a.rows);
+        const int64_t end = all > 0 ? ((int64_t)all + 255) / 256 * 256 : 256;
+        if (at >= end) return;
+    }
+    // the row, eight columns a lane
+    float up = 1.0f;
+    int e = 0;
+    float s = 0.0f, hard = 0.0f, soft = 0.0f;
+    if (counted && a.backward) {
+        row_factors(a, row, s, hard, soft);
+        const float b = factors_bound(a, s, hard, soft);
+        e = bound_exponent(b);
+        up = b - b == 0.0f ? power2(e - top) : 1.0f;
+        if (!(b - b == 0.0f)) e = top;
+    }
+    const uint16_t* from = a.x + row * a.ldx;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ldx % 8 == 0;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.wide; c += 256) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (counted) {
+            if (vec && c + 8 <= a.cols) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(from + c));
+                w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (c + i < a.cols) w[i / 2] |= (uint32_t)__ldg(from + c + i) << 16 * (i & 1);
+            }
+        }
+        *reinterpret_cast<uint4*>(a.xp + at * a.wide + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (a.xs != a.xp) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float lo, hi;
+                widen2<DT>(w[i], lo, hi);
+                w[i] = narrow2<DT>(lo * up, hi * up);
+            }
+            *reinterpret_cast<uint4*>(a.xs + at * a.wide + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (!counted) return;
+    // its targets and coefficients
+    int* cols = entries_of + warp * 3 * a.slots;
+    float* vals = reinterpret_cast<float*>(cols + a.slots);
+    const float nan = __uint_as_float(0x7FC00000u);
+    bool bad = false;
+    float constant = 0.0f, share = 0.0f;
+    const float fit = a.backward ? power2(ZERO_HD_SCALE - e) : 1.0f;
+    if (a.index) {
+        float m = __uint_as_float(0xFF800000u), sum = 0.0f, cross = 0.0f;
+        for (int k = lane; k < a.top; k += 32)
+            if (has_entry(a, row, k)) {
+                const float t = teacher_logit(a, row, k);
+                m = fmaxf(m, t);
+                share = 1.0f;
+            }
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        share = __any_sync(0xFFFFFFFFu, share > 0.0f) ? 1.0f : 0.0f;
+        for (int k = lane; k < a.top; k += 32) {
+            const int col = __ldg(a.index + row * a.ldt + k);
+            const bool has = has_entry(a, row, k);
+            float t = 0.0f, q = 0.0f;
+            if (has) {
+                t = (teacher_logit(a, row, k) - m) / a.temperature;
+                q = expf(t);
+                sum += q;
+                cross += q > 0.0f ? q * t : q;              // (a NaN stays one)
+                bad = bad || col >= a.vocab;
+            }
+            cols[k] = has ? col : ZERO_HD_NONE;
+            vals[k] = q;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            cross += __shfl_xor_sync(0xFFFFFFFFu, cross, o);
+        }
+        const float each = (a.backward ? s * fit : 1.0f) * a.soft * a.temperature;
+        for (int k = lane; k < a.top; k += 32) vals[k] = vals[k] / sum * each;
+        // sum q log q = sum q t - log(sum)
+        if (share > 0.0f) constant = a.soft * a.temperature * a.temperature * (cross / sum - logf(sum));
+        else soft = 0.0f;
+    }
+    if (a.labels && lane == 0) {
+        const int label = __ldg(a.labels + row);
+        bad = bad || label >= a.vocab;
+        cols[a.slots - 1] = label;
+        vals[a.slots - 1] = (a.backward ? s * fit : 1.0f) * a.hard;
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    __syncwarp();
+    if (a.slots == 1) {
+        if (lane == 0) {
+            a.column[at] = cols[0];
+            a.target[at] = vals[0];
+        }
+    } else {
+        put_targets(a, at * a.slots, cols, vals);
+    }
+    if (lane == 0) {
+        a.map[at] = (int32_t)row;
+        HeadRow h;
+        if (a.backward) {
+            a.exponent[at] = e;
+            const float log2e = 1.4426950408889634f;
+            const float soft_l = a.index ? __ldg(a.kept + 2 * row) : 0.0f;
+            const float hard_l = !a.labels ? 0.0f : a.index ? __ldg(a.kept + 2 * row + 1) : __ldg(a.kept + row);
+            h.c1 = hard * fit;
+            h.l1 = hard_l * log2e;
+            h.c2 = soft * fit;
+            h.l2 = soft_l * log2e;
+            if (!a.two) {                                    // one softmax
+                h.c1 += h.c2;
+                if (!a.labels) h.l1 = h.l2;
+            }
+            if (bad) h.c1 = nan;
+        } else {
+            h.c1 = bad ? nan : constant;
+            h.c2 = share;
+            h.l1 = h.l2 = 0.0f;
+        }
+        a.info[at] = h;
+    }
+}
+
+// Rows of the weights that are not aligned to 16 bytes, a piece of them, to rows that are.
+static __global__ void __launch_bounds__(256) k_head_weights(const __grid_constant__ HeadArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < a.count_v; r += (int64_t)gridDim.x * 8) {
+        const uint16_t* from = a.w + (a.v0 + r) * a.ldw;
+        uint16_t* to = a.wp + r * a.wide;
+#pragma unroll 8
+        for (int c = 2 * lane; c < a.wide; c += 64) {
+            uint32_t w = 0;
+            if (c < a.cols) w = __ldg(from + c);
+            if (c + 1 < a.cols) w |= (uint32_t)__ldg(from + c + 1) << 16;
+            *reinterpret_cast<uint32_t*>(to + c) = w;
+        }
+    }
+}
+
+// ---- the pair's machinery ------------------------------------------------------------
+// A box into this SM's shared memory whose bytes count on the first SM's barrier.
+static __device__ __forceinline__ void box_for_first(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %4, 0;\n"
+        " cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [r];\n}"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// Operand in shared memory with the contracted axis contiguous, 128-byte swizzle: rows of 64
+// elements, groups of eight rows 1024 bytes apart.
+static __device__ __forceinline__ uint64_t operand_rows(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+static __device__ __forceinline__ float read_one(uint32_t at)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(at) : "memory");
+    return __uint_as_float(r);
+}
+// A lane's 128 accumulators.
+static __device__ __forceinline__ void read128(uint32_t at, float (&v)[128])
+{
+    uint32_t r[128];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];"
+        "\ntcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(at) : "memory");
+#pragma unroll
+    for (int i = 0; i < 128; i++) v[i] = __uint_as_float(r[i]);
+}
+static __device__ __forceinline__ void read16(uint32_t at, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at) : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+static __device__ __forceinline__ void write16(uint32_t at, const float* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+          "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+          "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+          "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
+          "r"(at) : "memory");
+}
+
+struct HeadShared {
+    uint64_t full[ZERO_HD_STAGES];          // (first SM's) both SMs' operands of a stage have come
+    uint64_t empty[ZERO_HD_STAGES];         // its products are done
+    uint64_t sum_full[2], sum_empty[2];     // accumulators
+    uint64_t drain;
+    uint32_t tmem;
+    int dead;
+    float merge[4][32][3];                  // maxima and sums of a tile's right half
+};
+
+static __device__ __forceinline__ bool head_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
+{
+    return pair_wait<ZERO_HD_WAIT_LIMIT>(bar, parity, dead, err);
+}
+
+// ---- output --------------------------------------------------------------------------
+// N (a multiple of 8) columns from j of a row at `to`, in 16 bits.
+template <int DT, int N>
+static __device__ __forceinline__ void put_vectors(uint16_t* to, float (&v)[N], bool add)
+{
+    uint4* o = reinterpret_cast<uint4*>(to);
+#pragma unroll
+    for (int c = 0; c < N; c += 8) {
+        if (add) {
+            const uint4 p = o[c / 8];
+            const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float lo, hi;
+                widen2<DT>(w[e], lo, hi);
+                v[c + 2 * e] += lo;
+                v[c + 2 * e + 1] += hi;
+            }
+        }
+        o[c / 8] = make_uint4(narrow2<DT>(v[c], v[c + 1]), narrow2<DT>(v[c + 2], v[c + 3]), narrow2<DT>(v[c + 4], v[c + 5]),
+                              narrow2<DT>(v[c + 6], v[c + 7]));
+    }
+}
+
+// Where row i (packed, or of the piece) of an output lies and what its sums are multiplied by;
+// null if there is none.
+template <int PASS>
+static __device__ __forceinline__ uint16_t* out_row(const HeadArgs& a, int64_t i, int counted, int top, float& factor)
+{
+    if (PASS == HEAD_INPUT) {
+        if (i >= counted) return nullptr;
+        factor = power2(a.exponent[i] - ZERO_HD_SCALE);
+        return a.dx + a.map[i] * a.lddx;
+    }
+    if (i >= a.count_v) return nullptr;
+    factor = power2(top - ZERO_HD_SCALE);
+    return a.dw + (a.v0 + i) * a.lddw;
+}
+
+// N columns from j of a lane's own row.
+template <int DT, int PASS, int N>
+static __device__ __forceinline__ void put_row(const HeadArgs& a, uint16_t* to, float factor, int j, float (&v)[N])
+{
+    if (!to || j >= a.cols) return;
+    const bool add = PASS == HEAD_WEIGHT && a.accumulate;
+#pragma unroll
+    for (int c = 0; c < N; c++) v[c] *= factor;
+    if (a.vec && j + N <= a.cols) {
+        put_vectors<DT, N>(to + j, v, add);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < N; c++)
+        if (j + c < a.cols) {
+            float x = v[c];
+            if (add) x += widen1<DT>(to[j + c]);
+            to[j + c] = narrow1<DT>(x);
+        }
+}
+
+// put_row() for rows that are not aligned to vectors: 32 columns of the warp's rows through 2 KB of
+// shared memory, so that an access of the warp is a run of a row and not an element of each of 32
+// rows.  16-byte word q of row r lies at q ^ (r >> 1 & 3), so that lanes that each take a row meet all banks too.
+template <int DT, int PASS>
+static __device__ __forceinline__ void put_rows(const HeadArgs& a, uint16_t* to, float factor, int j, float (&v)[32], uint32_t stage)
+{
+    const int lane = threadIdx.x & 31;
+    if (j >= a.cols) return;                                 // all lanes
+    const bool add = PASS == HEAD_WEIGHT && a.accumulate;
+    const uint32_t own = stage + lane * 64;
+    const uint64_t mine = reinterpret_cast<uint64_t>(to);
+    if (add) {
+#pragma unroll 8
+        for (int r = 0; r < 32; r++) {
+            const uint16_t* g = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, mine, r));
+            const uint16_t x = g && j + lane < a.cols ? g[j + lane] : 0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + r * 64 + ((lane >> 3) ^ (r >> 1 & 3)) * 16 + (lane & 7) * 2),
+                         "h"(x) : "memory");
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const uint32_t word = own + (q ^ (lane >> 1 & 3)) * 16;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (add)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(word));
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float lo = 0.0f, hi = 0.0f;
+            if (add) widen2<DT>(w[e], lo, hi);
+            w[e] = narrow2<DT>(v[8 * q + 2 * e] * factor + lo, v[8 * q + 2 * e + 1] * factor + hi);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(word), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < 32; r++) {
+        uint16_t* g = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, mine, r));
+        if (g && j + lane < a.cols) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
+                         : "r"(stage + r * 64 + ((lane >> 3) ^ (r >> 1 & 3)) * 16 + (lane & 7) * 2));
+            g[j + lane] = x;
+        }
+    }
+    __syncwarp();
+}
+
+// Where a counted row's targets from column c on begin.
+static __device__ __forceinline__ int first_target(const HeadArgs& a, const int32_t* columns, int c)
+{
+    int lo = 0, hi = a.slots;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(columns + mid) < c) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// ---- the products --------------------------------------------------------------------
+template <int DT, int PASS, bool TWO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
+    k_head(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
+{
+    constexpr bool ROWS_A = PASS != HEAD_WEIGHT, ROWS_B = PASS <= HEAD_GRADIENT;    // contracted axis contiguous
+    extern __shared__ unsigned char raw[];
+    __shared__ HeadShared sh;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank(), pair = blockIdx.x >> 1;
+    volatile int* dead = &sh.dead;
+    int32_t* err = &a.st->err;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ZERO_HD_STAGES; s++) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(smem_u32(&sh.sum_full[s]), 1);
+            mbar_init(smem_u32(&sh.sum_empty[s]), 2 * ZERO_HD_WRITERS);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
+                     "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+    const int counted = a.st->rows;
+    const HeadShape shape = head_shape<PASS>(a, counted);
+    const uint32_t band = head_band<PASS>(a);
+    HeadSegment g;
+
+    if (warp == 0) {
+        // ---- loads ----
+        if (elected()) {
+            uint32_t n = 0, s = 0, ph = 0;
+            bool ok = true;
+            for (int i = 0; ok && head_segment<PASS>(a, shape, pair, i, g); i++) {
+                uint32_t ti, tj;
+                head_place(band, shape, g.tile, ti, tj);
+                const int half = head_width<PASS>(a, tj) / 2;
+                const int ra = (int)ti * ZERO_HD_TILE + rank * 128, rb = (int)tj * ZERO_HD_TILE + rank * half;
+                const uint32_t bytes = 2 * (ZERO_HD_SIDE + half * 128);
+                for (int t = g.s0; t < g.s1; t++, n++) {
+                    if (n >= ZERO_HD_STAGES && !head_wait(smem_u32(&sh.empty[s]), ph ^ 1u, dead, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&sh.full[s]), at = base + s * 2 * ZERO_HD_SIDE, bt = at + ZERO_HD_SIDE;
+                    const int k = t * ZERO_HD_STEP;
+                    if (rank == 0) mbar_expect_tx(bar, bytes);
+                    if (ROWS_A) {
+                        box_for_first(at, &map_a, k, ra, bar);
+                    } else {
+                        box_for_first(at, &map_a, ra, k, bar);
+                        box_for_first(at + 8192, &map_a, ra + 64, k, bar);
+                    }
+                    if (ROWS_B) {
+                        box_for_first(bt, &map_b, k, a.wy + rb, bar);
+                    } else {
+                        const int y = PASS == HEAD_INPUT ? a.wy + k : k;
+                        box_for_first(bt, &map_b, rb, y, bar);
+                        if (half > 64) box_for_first(bt + 8192, &map_b, rb + 64, y, bar);
+                    }
+                    if (++s == ZERO_HD_STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            // before this SM's shared memory is given back: both SMs' copies have landed (the
+            // first SM knows), and the last products are done
+            for (uint32_t q = n > ZERO_HD_STAGES ? n - ZERO_HD_STAGES : 0; q < n; q++) {
+                if (rank == 0)
+                    for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT &&
+                                          !mbar_try_wait(smem_u32(&sh.full[q % ZERO_HD_STAGES]), q / ZERO_HD_STAGES & 1); it++) {
+                    }
+                if (!*dead) head_wait(smem_u32(&sh.empty[q % ZERO_HD_STAGES]), q / ZERO_HD_STAGES & 1, dead, err);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products (the first SM's thread, for both) ----
+        if (rank == 0 && elected()) {
+            const uint32_t kind = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | (ROWS_A ? 0u : 1u << 15) |
+                                  (ROWS_B ? 0u : 1u << 16) | (uint32_t)(ZERO_HD_TILE >> 4) << 24;
+            constexpr uint32_t STEP_A = (ROWS_A ? 32 : 2048) >> 4, STEP_B = (ROWS_B ? 32 : 2048) >> 4;
+            uint32_t s = 0, ph = 0;
+            bool ok = true;
+            int i = 0;
+            for (; ok && head_segment<PASS>(a, shape, pair, i, g); i++) {
+                const int acc = i & 1;
+                if (i >= 2 && !head_wait(smem_u32(&sh.sum_empty[acc]), (uint32_t)((i >> 1) - 1) & 1u, dead, err)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t ti, tj;
+                head_place(band, shape, g.tile, ti, tj);
+                const uint32_t what = kind | (uint32_t)(head_width<PASS>(a, tj) >> 3) << 17;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int t = g.s0; t < g.s1; t++) {
+                    if (!head_wait(smem_u32(&sh.full[s]), ph, dead, err)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t at = base + s * 2 * ZERO_HD_SIDE, bt = at + ZERO_HD_SIDE;
+                    const uint64_t da = ROWS_A ? operand_rows(at) : operand(at), db = ROWS_B ? operand_rows(bt) : operand(bt);
+#pragma unroll
+                    for (int q = 0; q < ZERO_HD_STEP / 16; q++)
+                        product(tmem + acc * ZERO_HD_TILE, da + q * STEP_A, db + q * STEP_B, what, t > g.s0 || q > 0);
+                    commit_both(smem_u32(&sh.empty[s]));
+                    if (++s == ZERO_HD_STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (ok) commit_both(smem_u32(&sh.sum_full[acc]));
+            }
+            // the other SM's last arrivals are here before this SM can exit
+            for (int q = i > 2 ? i - 2 : 0; ok && q < i; q++)
+                ok = head_wait(smem_u32(&sh.sum_empty[q & 1]), (uint32_t)(q >> 1) & 1u, dead, err);
+            if (*dead) {                                     // let the products in flight finish
+                commit_both(smem_u32(&sh.drain), 1);
+                for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(smem_u32(&sh.drain), 0); it++) {
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- output: warp w reads rows 32 (w mod 4) + lane of this SM's half, 128 columns ----
+        const int quad = warp & 3, side = (warp - 4) >> 2;
+        const float nan = __uint_as_float(0x7FC00000u);
+        const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
+        const int top = a.st->top;
+        [[maybe_unused]] float z[PASS == HEAD_LOGITS ? 128 : 1];
+        for (int i = 0; head_segment<PASS>(a, shape, pair, i, g); i++) {
+            const int acc = i & 1;
+            uint32_t ti, tj;
+            head_place(band, shape, g.tile, ti, tj);
+            const int64_t r = (int64_t)ti * ZERO_HD_TILE + rank * 128 + quad * 32 + lane;
+            const uint32_t from = tmem + acc * ZERO_HD_TILE + side * 128 + ((uint32_t)quad << 21);
+            const int width = head_width<PASS>(a, tj);
+            const bool live = r < counted;
+            // what does not depend on the sums, while they are made
+            [[maybe_unused]] const int c0 = (int)tj * ZERO_HD_TILE + side * 128;      // first column, of the piece
+            [[maybe_unused]] const int end = a.count_v - c0;                          // columns there are from it
+            [[maybe_unused]] int next = 0;
+            [[maybe_unused]] int goal = ZERO_HD_NONE;                                 // the next target's column, from c0
+            [[maybe_unused]] const int32_t* columns = nullptr;
+            [[maybe_unused]] HeadRow row{};
+            [[maybe_unused]] uint16_t* to = nullptr;
+            [[maybe_unused]] float factor = 0.0f;
+            if (PASS <= HEAD_GRADIENT) {
+                if (live && g.last) {
+                    columns = a.column + r * a.slots;
+                    next = a.slots == 1 ? (__ldg(columns) < a.v0 + c0) : first_target(a, columns, a.v0 + c0);
+                    if (next < a.slots) goal = __ldg(columns + next) - a.v0 - c0;
+                    if (PASS == HEAD_GRADIENT) row = a.info[r];
+                }
+            } else if (g.slot < 0 && a.last) {
+                to = out_row<PASS>(a, r, counted, top, factor);
+            } else if (g.slot < 0 && PASS == HEAD_WEIGHT) {
+                to = out_row<PASS>(a, r, counted, top, factor);
+            }
+            const bool have = __all_sync(0xFFFFFFFFu, head_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, err));
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if constexpr (PASS == HEAD_LOGITS) {
+                // z: the tile's sums, runs of it added in fp32
+                if (g.first) {
+                    read128(from, z);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 16) {
+                        float v[16];
+                        read16(from + c, v);
+#pragma unroll
+                        for (int e = 0; e < 16; e++) z[c + e] += v[e];
+                    }
+                }
+                if (g.last) {
+                    // logits of targets in these columns: a lane's accumulators are read at a column
+                    // of the warp's choice
+                    if (__any_sync(0xFFFFFFFFu, goal < 128)) {
+                        if (!g.first) {
+#pragma unroll
+                            for (int c = 0; c < 128; c += 16) write16(from + c, z + c);
+                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        }
+                        for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < 128;) {
+                            const float v = read_one(from + c);
+                            if (goal == c) {
+                                a.found[r * a.slots + next] = have ? v : nan;
+                                next++;
+                                goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
+                if (!g.last) continue;
+                if (end < 128) {
+#pragma unroll
+                    for (int c = 0; c < 128; c++)
+                        if (c >= end) z[c] = __uint_as_float(0xFF800000u);
+                }
+                float m[4], s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int e = 0; e < 4; e++) m[e] = z[e];
+#pragma unroll
+                for (int c = 4; c < 128; c++) m[c & 3] = fmaxf(m[c & 3], z[c]);
+                float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                if (end > 0) {
+                    const float b1 = -most * a.k1, b2 = -most * a.k2;
+#pragma unroll
+                    for (int c = 0; c < 128; c++) {
+                        s[c & 3] += exp2_fast(__fmaf_rn(z[c], a.k1, b1));
+                        if (TWO) s2[c & 3] += exp2_fast(__fmaf_rn(z[c], a.k2, b2));
+                    }
+                }
+                float sum = (s[0] + s[1]) + (s[2] + s[3]), sum2 = (s2[0] + s2[1]) + (s2[2] + s2[3]);
+                if (!have) sum = sum2 = nan;
+                // the tile's two halves
+                if (side == 1) {
+                    sh.merge[quad][lane][0] = most;
+                    sh.merge[quad][lane][1] = sum;
+                    if (TWO) sh.merge[quad][lane][2] = sum2;
+                }
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                if (side == 0) {
+                    const float other = sh.merge[quad][lane][0], both = fmaxf(most, other);
+                    const float f0 = exp2_fast((most - both) * a.k1), f1 = exp2_fast((other - both) * a.k1);
+                    sum = sum * f0 + sh.merge[quad][lane][1] * f1;
+                    if (TWO) {
+                        const float h0 = exp2_fast((most - both) * a.k2), h1 = exp2_fast((other - both) * a.k2);
+                        sum2 = sum2 * h0 + sh.merge[quad][lane][2] * h1;
+                    }
+                    if (live) {
+                        const int64_t at = (int64_t)(a.v0 / ZERO_HD_TILE + tj) * a.npad + r;
+                        a.part[at] = make_float2(both, sum);
+                        if (TWO) a.part2[at] = sum2;
+                    }
+                }
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+            } else if constexpr (PASS == HEAD_GRADIENT) {
+                uint16_t* out = a.dz + r * a.pitch + c0;
+                for (int c = 0; c < 128; c += 32) {
+                    float v[32];
+                    __syncwarp();
+                    read_accumulator(from + c, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) {
+                        float d = row.c1 * exp2_fast(__fmaf_rn(v[e], a.k1, -row.l1));
+                        if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v[e], a.k2, -row.l2)), d);
+                        v[e] = d;
+                    }
+                    if (!live || c + 32 > end) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (!live || c + e >= end) v[e] = 0.0f;
+                    }
+                    if (!have) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) v[e] = nan;
+                    }
+                    put_vectors<DT, 32>(out + c, v, false);
+                }
+                // once more where the targets are
+                for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < 128;) {
+                    const float v = read_one(from + c);
+                    if (goal == c) {
+                        float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1));
+                        if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v, a.k2, -row.l2)), d);
+                        out[c] = narrow1<DT>(d - __ldg(a.target + r * a.slots + next));
+                        next++;
+                        goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
+                    }
+                    __syncwarp();
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
+            } else {
+                const int j = (int)tj * ZERO_HD_TILE;
+                // four columns of 32 rows are one run of 512 bytes
+                const int64_t own = (int64_t)((rank * 4 + quad) * 64) * 32 + lane;
+                float4* part = g.slot < 0 ? nullptr : reinterpret_cast<float4*>(a.parts + (int64_t)g.slot * ZERO_HD_SLOT) + own;
+                float4* kept = PASS == HEAD_INPUT ? reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own
+                                                  : nullptr;
+                for (int c = side * 128; c < (side + 1) * 128 && c < width; c += 32) {
+                    float v[32];
+                    __syncwarp();
+                    read_accumulator(tmem + acc * ZERO_HD_TILE + c + ((uint32_t)quad << 21), v);
+                    if (!have) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) v[e] = nan;
+                    }
+                    if (!part && PASS == HEAD_INPUT && !a.first) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float4 p = kept[(c / 4 + e) * 32];
+                            v[4 * e] += p.x;
+                            v[4 * e + 1] += p.y;
+                            v[4 * e + 2] += p.z;
+                            v[4 * e + 3] += p.w;
+                        }
+                    }
+                    if (part || (PASS == HEAD_INPUT && !a.last)) {
+                        float4* o = part ? part : kept;
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            o[(c / 4 + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    } else if (a.vec) {
+                        put_row<DT, PASS, 32>(a, to, factor, j + c, v);
+                    } else {
+                        put_rows<DT, PASS>(a, to, factor, j + c, v, stage);
+                    }
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
+            }
+        }
+    }
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    cluster_sync();
+}
+
+// Adds the parts of the cut tiles in the contracted axis's order: a warp takes 32 rows and 16 columns of a tile.
+template <int DT, int PASS>
+__global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadArgs a)
+{
+    const int counted = a.st->rows, top = a.st->top, lane = threadIdx.x & 31;
+    const HeadShape shape = head_shape<PASS>(a, counted);
+    if (shape.rest_pairs <= shape.rest) return;
+    for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < shape.rest * 128; unit += gridDim.x * 8) {
+        const uint32_t q = unit >> 7;
+        const int strip = (unit >> 4) & 7, c = unit & 15;
+        const uint32_t p0 = head_owner(shape, q * shape.steps), p1 = head_owner(shape, (q + 1) * shape.steps - 1);
+        uint32_t ti, tj;
+        head_place(head_band<PASS>(a), shape, shape.waves * a.pairs + q, ti, tj);
+        const int j = (int)tj * ZERO_HD_TILE + c * 16;
+        if (p0 == p1 || j >= a.cols) continue;
+        const uint32_t second = head_share(shape, p0) / shape.steps < q;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[e] = 0.0f;
+        const int64_t own = (int64_t)(strip * 64 + c * 4) * 32 + lane;
+#pragma unroll 4
+        for (uint32_t p = p0; p <= p1; p++) {
+            const float4* s = reinterpret_cast<const float4*>(a.parts + (int64_t)(2 * p + (p == p0 ? second : 0)) * ZERO_HD_SLOT) + own;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float4 f = __ldcg(s + e * 32);
+                v[4 * e] += f.x;
+                v[4 * e + 1] += f.y;
+                v[4 * e + 2] += f.z;
+                v[4 * e + 3] += f.w;
+            }
+        }
+        const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
+        if (PASS == HEAD_INPUT) {
+            float4* kept = reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
+            if (!a.first) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float4 f = kept[e * 32];
+                    v[4 * e] += f.x;
+                    v[4 * e + 1] += f.y;
+                    v[4 * e + 2] += f.z;
+                    v[4 * e + 3] += f.w;
+                }
+            }
+            if (!a.last) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) kept[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                continue;
+            }
+        }
+        float factor = 0.0f;
+        uint16_t* to = out_row<PASS>(a, r, counted, top, factor);
+        put_row<DT, PASS, 16>(a, to, factor, j, v);
+    }
+}
+
+// ---- the loss ------------------------------------------------------------------------
+// 32 counted rows a block, a lane a row; the 32 warps share the tiles' maxima and sums.  The
+// last block to finish adds the blocks' sums in order.
+static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
+{
+    __shared__ float ms[32][32], ss[32][32], ts[32][32], dots[32];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int counted = a.st->rows;
+    const int64_t r = (int64_t)blockIdx.x * 32 + lane;
+    const float low = __uint_as_float(0xFF800000u), nan = __uint_as_float(0x7FC00000u);
+    float m = low, s = 0.0f, t = 0.0f;
+    if (r < counted) {
+#pragma unroll 4
+        for (int v = warp; v < tiles; v += 32) {
+            const float2 p = a.part[(int64_t)v * a.npad + r];
+            const float most = fmaxf(m, p.x);
+            if (most == low) {                              // (a NaN sum of a lowest maximum is kept)
+                s += p.y;
+                continue;
+            }
+            const float f = exp2_fast((m - most) * a.k1), h = exp2_fast((p.x - most) * a.k1);
+            s = s * f + p.y * h;
+            if (a.two) t = t * exp2_fast((m - most) * a.k2) + a.part2[(int64_t)v * a.npad + r] * exp2_fast((p.x - most) * a.k2);
+            m = most;
+        }
+    }
+    ms[warp][lane] = m;
+    ss[warp][lane] = s;
+    ts[warp][lane] = t;
+    // a warp a row: its targets' logits times their weights
+    const int64_t w = (int64_t)blockIdx.x * 32 + warp;
+    float dot = 0.0f;
+    if (w < counted)
+        for (int e = lane; e < a.slots; e += 32)
+            if (a.column[w * a.slots + e] < a.vocab) dot += a.target[w * a.slots + e] * a.found[w * a.slots + e];
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    if (lane == 0) dots[warp] = dot;
+    __syncthreads();
+    if (warp == 0) {
+        double loss = 0.0;
+        if (r < counted) {
+            m = low;
+            for (int v = 0; v < 32; v++) m = fmaxf(m, ms[v][lane]);
+            s = t = 0.0f;
+            for (int v = 0; v < 32; v++) {
+                if (v >= tiles) break;
+                s += ss[v][lane] * exp2_fast((ms[v][lane] - m) * a.k1);
+                if (a.two) t += ts[v][lane] * exp2_fast((ms[v][lane] - m) * a.k2);
+            }
+            // k1 is 1/T only where there is no other log-sum-exp
+            const HeadRow h = a.info[r];
+            const float scale1 = a.labels ? 1.0f : 1.0f / a.temperature;
+            float l1 = m * scale1 + logf(s), l2 = a.two ? m / a.temperature + logf(t) : l1;
+            if (h.c1 != h.c1) l1 = l2 = nan;
+            float x = h.c1 - dots[lane];
+            if (a.index) x = __fmaf_rn(h.c2 * a.soft * a.temperature * a.temperature, l2, x);
+            if (a.labels) x = __fmaf_rn(a.hard, __fmaf_rn(a.z_loss * l1, l1, l1), x);
+            const int64_t row = a.map[r];
+            a.loss[row] = x;
+            if (a.index) {
+                a.lse[2 * row] = l2;
+                a.lse[2 * row + 1] = a.labels ? l1 : 0.0f;
+            } else {
+                a.lse[row] = l1;
+            }
+            loss = x;
+        }
+        for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+        if (lane == 0) {
+            __stcg(a.partial + blockIdx.x, loss);
+            __threadfence();
+            last = atomicAdd(&a.st->ticket, 1u) == gridDim.x - 1;
+        }
+        __syncwarp();
+        if (a.sums && last) {
+            __threadfence();
+            double all = 0.0;
+            for (unsigned b = lane; b < gridDim.x; b += 32) all += __ldcg(a.partial + b);
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            if (lane == 0) {
+                a.sums[0] = (float)all;
+                a.sums[1] = (float)counted;
+            }
+        }
+    }
+}
+
+// The kernels of a 16-bit type.
+struct HeadKernels {
+    const void *pack, *logits[2], *gradient[2], *input, *weight, *join_input, *join_weight;
+};
+HeadKernels head_kernels_fp16();
+HeadKernels head_kernels_bf16();
+
+template <int DT>
+HeadKernels head_kernels()
+{
+    return {(const void*)k_head_pack<DT>,
+            {(const void*)k_head<DT, HEAD_LOGITS, false>, (const void*)k_head<DT, HEAD_LOGITS, true>},
+            {(const void*)k_head<DT, HEAD_GRADIENT, false>, (const void*)k_head<DT, HEAD_GRADIENT, true>},
+            (const void*)k_head<DT, HEAD_INPUT, false>,
+            (const void*)k_head<DT, HEAD_WEIGHT, false>,
+            (const void*)k_head_join<DT, HEAD_INPUT>,
+            (const void*)k_head_join<DT, HEAD_WEIGHT>};
+}
+
+}  // namespace zero

@@ -26,7 +26,8 @@
 
 #include "zero_act.cuh"
 #include "zero_b200.h"
-#include "zero_tma.cuh"
+#include "zero_pair.cuh"
+#include "zero_tensor_map.h"
 #include "zero_trace.h"
 
 namespace zero {
@@ -406,113 +407,14 @@ static __device__ __forceinline__ float column_sum(const WgradArgs& a, int64_t i
     return s;
 }
 
-// ---- the pair's machinery ------------------------------------------------------------
-static __device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// True in one lane of a whole warp.  Code under it is known to run in one thread, so that the
-// operands of the copies and products it issues stay in the warp's uniform registers: issuing a
-// stage's four products or its copies took about 800 cycles with `lane == 0`, longer than the
-// products themselves (1161 -> 1048 us at 16384 x 4096 x 14336).
-static __device__ __forceinline__ bool elected()
-{
-    uint32_t r;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-    return r != 0;
-}
-// Every thread of both SMs; the warp is together again after it (what follows may be a
-// whole-warp instruction).
-static __device__ __forceinline__ void cluster_sync()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-    __syncwarp();
-}
-// Arrive on the barrier of the pair's first SM that lies at this SM's address `bar`.  What
-// the arrival announces lies in this SM's own shared or tensor memory and is ordered for the
-// tensor cores by the proxy fence or the tcgen05 fence before it, so the arrival itself
-// carries no cluster-wide release (which, with the matching acquire in the wait, cost a third of
-// the rate: 1089 against 1504 TFLOP/s at 8192 x 4096 x 4096).
-static __device__ __forceinline__ void arrive_first(uint32_t bar)
-{
-    asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
-                 " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar) : "memory");
-}
-// A lane to arrive for the warp, known once every lane has its x.  An arrival that hands a
-// buffer back must not be made while loads from it are under way, and the barrier unit does not
-// wait for loads before it: x is made of the loaded values.
-static __device__ __forceinline__ int lane_with(uint32_t x) { return __any_sync(0xFFFFFFFFu, x == 0) ? 0 : 1; }
-// Bounded wait of a lane: false when it gave up (here or in another warp of this SM).
+// ---- the pair's machinery (zero_pair.cuh), its waits with this kernel's limit ----------
 static __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
-    for (uint32_t it = 0; it < ZERO_WG_WAIT_LIMIT; it++) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*dead) return false;
-    }
-    *dead = 1;
-    atomicExch(err, ZERO_ETIMEOUT);
-    return false;
+    return pair_wait<ZERO_WG_WAIT_LIMIT>(bar, parity, dead, err);
 }
-// The same for a whole warp, whose lanes go on or stop together (votes and shuffles of all lanes
-// follow), so every poll is voted on.  A vote after lanes that polled by themselves took 154 us
-// instead of 146 at 8192 x 6400 x 1600, a loop without a first poll of its own 151.
 static __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
-    if (ZERO_WG_WAIT_LIMIT > 0 && __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-#pragma unroll 1
-    for (uint32_t it = 0; it < ZERO_WG_WAIT_LIMIT; it++) {
-        if (__any_sync(0xFFFFFFFFu, *dead)) return false;
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    }
-    *dead = 1;
-    atomicExch(err, ZERO_ETIMEOUT);
-    __syncwarp();
-    return false;
-}
-static __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-// Completion of every product issued so far arrives on `bar` in both SMs (or in those of a mask).
-static __device__ __forceinline__ void commit_both(uint32_t bar, uint16_t sms = 3)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(bar), "h"(sms) : "memory");
-}
-// Operand in shared memory with the non-contracted axis contiguous, 128-byte swizzle:
-// groups of 64 columns are 8192 bytes apart, groups of 8 tokens 1024.
-static __device__ __forceinline__ uint64_t operand(uint32_t addr)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-static __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add)
-{
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-        ::"r"(d), "l"(a), "l"(b), "r"(what), "r"((uint32_t)add) : "memory");
-}
-static __device__ __forceinline__ void read_accumulator(uint32_t at, float (&v)[32])
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at) : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+    return warp_wait<ZERO_WG_WAIT_LIMIT>(bar, parity, dead, err);
 }
 
 // Two codes (bytes 0 and 1, or 2 and 3, of w) times their block's 2^e, as a 16-bit pair.
@@ -1176,15 +1078,12 @@ using namespace zero;
 
 namespace {
 
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 bool sizes_ok(int64_t tokens, int64_t n, int64_t k)
 {
     return tokens >= 0 && tokens < (1ll << 31) && n >= 1 && n <= (1ll << 24) && k >= 1 && k <= ZERO_ACT_MAX_COLS &&
            n * k < (1ll << 46);              // tiles are counted in 32 bits
 }
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t steps_of(int64_t tokens) { return up(tokens, ZERO_WG_TOK); }
 
 // Whether a call on so many stages keeps sums in the workspace: only then are tiles cut into parts,
@@ -1225,28 +1124,6 @@ void divide(WgradArgs& a, int pairs)
     }
 }
 
-decltype(&cuTensorMapEncodeTiled) encode()
-{
-    static decltype(&cuTensorMapEncodeTiled) fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p);
-    }();
-    return fn;
-}
-
-bool tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t cols, int64_t rows, int64_t pitch,
-                int box_cols, int box_rows, CUtensorMapSwizzle swizzle)
-{
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode()(m, type, 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Pairs of SMs that run a launch's clusters at the same time; 0: a CUDA call failed.
 int device_pairs()
 {
@@ -1274,11 +1151,6 @@ int device_pairs()
         pairs[dev] = n < 1 ? 1 : n > ZERO_WG_PAIRS ? ZERO_WG_PAIRS : n;
     }
     return pairs[dev];
-}
-
-bool launch(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream)
-{
-    return cudaLaunchKernel(fn, grid, dim3(threads), args, smem, static_cast<cudaStream_t>(stream)) == cudaSuccess;
 }
 
 }  // namespace

@@ -15,6 +15,8 @@ static int check(int counted, int cols, int columns, int pairs, int band)
     a.count_v = columns;
     a.pairs = pairs;
     a.band = band;
+    uint16_t some;
+    a.dx = &some;
     const HeadShape s = head_shape<PASS>(a, counted);
     const uint32_t tiles = s.tm * s.tn, places = head_band<PASS>(a);
     std::vector<uint8_t> seen((size_t)tiles * s.steps, 0), place(tiles, 0), slots(2 * ZERO_HD_PAIRS, 0);
@@ -27,7 +29,8 @@ static int check(int counted, int cols, int columns, int pairs, int band)
     for (int p = 0; p < pairs; p++) {
         HeadSegment g;
         int within = 0;                              // runs of the tile so far
-        for (uint32_t i = 0; head_segment<PASS>(a, s, p, i, g); i++) {
+        uint32_t i = 0;
+        for (; head_segment<PASS>(a, s, p, i, g); i++) {
             if (g.tile >= tiles || g.s0 < 0 || g.s1 <= g.s0 || g.s1 > (int)s.steps) return 3;
             for (int t = g.s0; t < g.s1; t++)
                 if (seen[(size_t)g.tile * s.steps + t]++) return 4;
@@ -46,6 +49,7 @@ static int check(int counted, int cols, int columns, int pairs, int band)
             }
         }
         if (within) return 10;
+        if (PASS == HEAD_INPUT && i != head_inputs(a, s, p)) return 13;
     }
     for (uint8_t n : seen)
         if (n != 1) return 11;

@@ -72,7 +72,7 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     take(a.xs, a.npad * a.wide);              // backward
     take(a.dz, a.npad * a.pitch);
     take(a.acc, a.npad / ZERO_HD_TILE * up(h->cols, ZERO_HD_TILE) * ZERO_HD_SLOT);
-    take(a.parts, 2ll * ZERO_HD_PAIRS * ZERO_HD_SLOT);
+    take(a.parts, 4ll * ZERO_HD_PAIRS * ZERO_HD_SLOT);
     return (uint64_t)((at > forward ? at : forward) - begin);
 }
 
@@ -83,7 +83,7 @@ int device_pairs(const HeadKernels& k)
 {
     static std::mutex lock;
     static int pairs[64] = {};
-    for (const void* fn : {k.logits[0], k.logits[1], k.gradient[0], k.gradient[1], k.input, k.weight})
+    for (const void* fn : {k.logits[0], k.logits[1], k.gradient[0], k.gradient[1], k.products})
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ZERO_HD_SMEM) != cudaSuccess) return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -91,7 +91,7 @@ int device_pairs(const HeadKernels& k)
     if (pairs[dev] == 0) {
         cudaLaunchConfig_t c{};
         c.gridDim = dim3(2 * ZERO_HD_PAIRS);
-        c.blockDim = dim3(ZERO_HD_THREADS);
+        c.blockDim = dim3(head_threads(HEAD_PRODUCTS));
         c.dynamicSmemBytes = ZERO_HD_SMEM;
         cudaLaunchAttribute at{};
         at.id = cudaLaunchAttributeClusterDimension;
@@ -100,7 +100,7 @@ int device_pairs(const HeadKernels& k)
         c.attrs = &at;
         c.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, k.input, &c) != cudaSuccess) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k.products, &c) != cudaSuccess) return 0;
         pairs[dev] = n < 1 ? 1 : n > ZERO_HD_PAIRS ? ZERO_HD_PAIRS : n;
     }
     return pairs[dev];
@@ -147,12 +147,29 @@ HeadArgs arguments(const zero_head_t* h, const void* x, int64_t ldx, const void*
     return a;
 }
 
+// A launch that may begin while the kernel before it ends (which it waits for before it reads or
+// writes anything): a call's kernels follow each other without the launches' latency.
+bool launch_next(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelExC(&c, fn, args) == cudaSuccess;
+}
+
 // The passes over the rows.
 bool run_rows(const HeadArgs& a, const HeadKernels& k, void* stream)
 {
     void* args[] = {const_cast<HeadArgs*>(&a)};
     return launch((const void*)k_head_rows, dim3((unsigned)up(a.rows, ZERO_HD_CHUNK)), ZERO_HD_CHUNK, 0, args, stream) &&
-           launch(k.pack, dim3((unsigned)up(a.rows + ZERO_HD_TILE, 8)), 256, 8 * 3 * a.slots * 4, args, stream);
+           launch_next(k.pack, dim3((unsigned)up(a.rows + ZERO_HD_TILE, 8)), 256, 8 * 3 * a.slots * 4, args, stream);
 }
 
 bool map16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows)
@@ -170,13 +187,13 @@ bool copy_weights(const HeadArgs& a, int pairs, void* stream)
 {
     void* args[] = {const_cast<HeadArgs*>(&a)};
     const int64_t most = 16ll * pairs, want = up(a.count_v, 8);
-    return launch((const void*)k_head_weights, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream);
+    return launch_next((const void*)k_head_weights, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream);
 }
-bool product(const void* fn, HeadArgs& a, int64_t tiles, int pairs, CUtensorMap* ma, CUtensorMap* mb, void* stream)
+bool product(const void* fn, int pass, HeadArgs& a, int64_t tiles, int pairs, CUtensorMap* const (&maps)[5], void* stream)
 {
     a.pairs = (int)(tiles < pairs ? tiles : pairs);
-    void* args[] = {&a, ma, mb};
-    return launch(fn, dim3(2 * a.pairs), ZERO_HD_THREADS, ZERO_HD_SMEM, args, stream);
+    void* args[] = {&a, maps[0], maps[1], maps[2], maps[3], maps[4]};
+    return launch_next(fn, dim3(2 * a.pairs), head_threads(pass), ZERO_HD_SMEM, args, stream);
 }
 
 zero_status_t forward(const zero_head_t* h, const void* x, int64_t ldx, const void* w, int64_t ldw, bool distill,
@@ -205,12 +222,13 @@ zero_status_t forward(const zero_head_t* h, const void* x, int64_t ldx, const vo
         a.count_v = (int)(h->vocab - v < step ? h->vocab - v : step);
         if (copied && !copy_weights(a, pairs, stream)) return ZERO_ECUDA;
         if (!weights(a, 128, copied, &mw) ||
-            !product(k.logits[a.two], a, a.npad / ZERO_HD_TILE * up(a.count_v, ZERO_HD_TILE), pairs, &mx, &mw, stream))
+            !product(k.logits[a.two], HEAD_LOGITS, a, a.npad / ZERO_HD_TILE * up(a.count_v, ZERO_HD_TILE), pairs,
+                     {&mx, &mw, &mx, &mw, &mx}, stream))
             return ZERO_ECUDA;
     }
     int tiles = (int)up(h->vocab, ZERO_HD_TILE);
     void* args[] = {&a, &tiles};
-    return launch((const void*)k_head_loss, dim3((unsigned)up(a.rows, 32)), 1024, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
+    return launch_next((const void*)k_head_loss, dim3((unsigned)up(a.rows, 32)), 1024, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
 }
 
 zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const void* w, int64_t ldw, bool distill,
@@ -231,6 +249,8 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     HeadArgs a = arguments(h, x, ldx, w, ldw, distill, index, logit, ldt, labels, work);
     a.backward = 1;
     a.kept = lse; a.weight = row_grad; a.scale = scale; a.divisor = divisor;
+    const float parts = (labels ? fabsf(a.hard) : 0.0f) + (a.index ? fabsf(a.soft) * a.temperature : 0.0f);
+    a.unit = row_grad || parts == 0.0f || !isfinite(1.0f / parts) ? 1.0f : 1.0f / parts;
     a.dx = static_cast<uint16_t*>(dx);
     a.dw = static_cast<uint16_t*>(dw);
     a.lddx = lddx; a.lddw = lddw;
@@ -240,32 +260,31 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     const int pairs = device_pairs(k);
     if (pairs == 0 || !encode() || !run_rows(a, k, stream)) return ZERO_ECUDA;
     const bool copied = !aligned_to(w, 16) || ldw % 8 != 0;
-    const int64_t rows = a.npad / ZERO_HD_TILE, wide = up(h->cols, ZERO_HD_TILE);
-    CUtensorMap mx, ms, mz, mt, mw, mn;
+    const int64_t rows = a.npad / ZERO_HD_TILE;
+    CUtensorMap mx, ms, mz, mt, mo, md, mw, mn;
+    a.vec_x = aligned_to(dx, 16) && lddx % 8 == 0;
+    a.vec_w = aligned_to(dw, 16) && lddw % 8 == 0;
     if (!map16(&mx, a.xp, a.wide, a.npad, a.wide, 128) || !map16(&ms, a.xs, a.wide, a.npad, a.wide, 64) ||
-        !map16(&mz, a.dz, a.pitch, a.npad, a.pitch, 128) || !map16(&mt, a.dz, a.pitch, a.npad, a.pitch, 64))
+        !map16(&mz, a.dz, a.pitch, a.npad, a.pitch, 128) || !map16(&mt, a.dz, a.pitch, a.npad, a.pitch, 64) ||
+        !map16(&mo, a.dz, a.pitch, a.npad, a.pitch, 32))
         return ZERO_ECUDA;
+    if (!dw || !a.vec_w) md = mo;
+    else if (!map16(&md, dw, a.cols, a.vocab, lddw, 32)) return ZERO_ECUDA;
     for (int64_t v = 0; v < h->vocab; v += a.pitch) {
         a.v0 = (int)v;
         a.count_v = (int)(h->vocab - v < a.pitch ? h->vocab - v : a.pitch);
         a.first = v == 0;
         a.last = v + a.pitch >= h->vocab;
-        const int64_t words = up(a.count_v, ZERO_HD_TILE);
         if (copied && !copy_weights(a, pairs, stream)) return ZERO_ECUDA;
         if (!weights(a, 128, copied, &mw) || !weights(a, 64, copied, &mn) ||
-            !product(k.gradient[a.two], a, rows * words, pairs, &mx, &mw, stream))
+            !product(k.gradient[a.two], HEAD_GRADIENT, a, rows * up(a.count_v, ZERO_HD_TILE), pairs, {&mx, &mw, &mx, &mw, &mo}, stream) ||
+            !product(k.products, HEAD_PRODUCTS, a, pairs, pairs, {&mz, &mn, &mt, &ms, &md}, stream))
             return ZERO_ECUDA;
+        // tiles are cut where 16 stages or more are added
         void* args[] = {&a};
-        if (dx) {
-            a.vec = aligned_to(dx, 16) && lddx % 8 == 0;
-            if (!product(k.input, a, pairs, pairs, &mz, &mn, stream)) return ZERO_ECUDA;
-            if (a.count_v > 15 * ZERO_HD_STEP && !launch(k.join_input, dim3(4 * pairs), 256, 0, args, stream)) return ZERO_ECUDA;
-        }
-        if (dw) {
-            a.vec = aligned_to(dw, 16) && lddw % 8 == 0;
-            if (!product(k.weight, a, pairs, pairs, &mt, &ms, stream)) return ZERO_ECUDA;
-            if (a.rows > 15 * ZERO_HD_STEP && !launch(k.join_weight, dim3(4 * pairs), 256, 0, args, stream)) return ZERO_ECUDA;
-        }
+        if (((dx && a.count_v > 15 * ZERO_HD_STEP) || (dw && a.rows > 15 * ZERO_HD_STEP)) &&
+            !launch_next(k.join, dim3(4 * pairs), 256, 0, args, stream))
+            return ZERO_ECUDA;
     }
     return ZERO_OK;
 }

@@ -5,8 +5,7 @@
 //   LOGITS    z tile by tile; each tile leaves a row's maximum and sum of exponentials
 //   GRADIENT  the same tiles again; each leaves its gradient dz (16 bits, scaled by a power of
 //             two a row) in the workspace, a piece of the vocabulary at a time
-//   INPUT     dx += dz w of a piece, summed over pieces in fp32
-//   WEIGHT    dw = dz^T x of a piece
+//   PRODUCTS  dx += dz w of the piece, summed over pieces in fp32, and dw = dz^T x
 // Rows that take no part are left out before the first product: a pass over the rows packs the
 // others (aligned, padded with zeros to a whole stage), so what their x holds is not read, and
 // every product's rows are the counted ones.
@@ -24,10 +23,8 @@ namespace zero {
 #define ZERO_HD_STEP 64                      // contracted elements of a stage
 #define ZERO_HD_STAGES 6
 #define ZERO_HD_SIDE 16384                   // bytes of a stage's operand in one SM
-#define ZERO_HD_WRITERS 8                    // warps that read the accumulators
-#define ZERO_HD_THREADS (128 + 32 * ZERO_HD_WRITERS)    // warp 0 loads, 1 products, from 4 output
-#define ZERO_HD_ROWS 2048                    // bytes in which an output warp turns its rows
-#define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + ZERO_HD_WRITERS * ZERO_HD_ROWS + 1024)
+#define ZERO_HD_ROWS 4096                    // bytes in which an output warp lays 32 rows of 64 columns
+#define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + 8 * ZERO_HD_ROWS + 1024)
 #define ZERO_HD_PAIRS 80                     // most pairs that share a launch's work
 #define ZERO_HD_PART 8                       // least stages of a part of a cut tile
 #define ZERO_HD_RUN 12                       // stages an accumulator adds for the loss
@@ -39,7 +36,13 @@ namespace zero {
 #define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
 #endif
 
-enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT = 3 };
+enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT = 3, HEAD_PRODUCTS = 4 };
+
+// Warps that read the accumulators, each 32 rows of a column group of the tile.  Logits, whose runs are
+// added in registers, take 64 columns a warp (128 would spill: 6.4 against 4.96 ms without runs at 8192
+// x 128256 x 4096); the others 128.
+__host__ __device__ constexpr int head_writers(int pass) { return pass == HEAD_LOGITS ? 16 : 8; }
+__host__ __device__ constexpr int head_threads(int pass) { return 128 + 32 * head_writers(pass); }   // warp 0 loads, 1 products, from 4 output
 
 // What the passes over the rows leave for the rest, at the head of the workspace.
 struct HeadState {
@@ -58,14 +61,14 @@ struct HeadArgs {
     int64_t rows, ldx, ldw, ldt, lddx, lddw;
     int cols, vocab, top, slots;             // slots: targets of a row (top, and one for the label)
     int top_dtype, two, backward;            // two: both log-sum-exps are needed
-    float temperature, hard, soft, z_loss, k1, k2, scale;
+    float temperature, hard, soft, z_loss, k1, k2, scale, unit;
     const uint16_t *x, *w;
     const int32_t *labels, *index;
     const void* logit;
     const float *weight, *divisor, *kept;    // the backward pass's row weights, divisor, log-sum-exps
     float *loss, *lse, *sums;
     uint16_t *dx, *dw;
-    int accumulate, vec;
+    int accumulate, vec_x, vec_w;
     // workspace
     HeadState* st;
     uint32_t* mask;                          // counted rows, a bit each
@@ -96,6 +99,7 @@ struct HeadSegment {
     int32_t s0, s1;
     int slot;                                // of a part of a cut tile, else -1
     bool first, last;                        // run of the tile
+    bool input;                              // of dx (else of dw, where there are two)
 };
 
 static __host__ __device__ __forceinline__ uint32_t head_up(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
@@ -183,6 +187,26 @@ static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, 
     return true;
 }
 
+// The products' segments: dx's, then dw's.  `inputs`: how many a pair has of the first.
+static __host__ __device__ __forceinline__ uint32_t head_inputs(const HeadArgs& a, const HeadShape& s, uint32_t pair)
+{
+    if (!a.dx) return 0;
+    if (pair >= s.rest_pairs) return s.waves;
+    const uint32_t u0 = head_share(s, pair), u1 = head_share(s, pair + 1);
+    return s.waves + (u1 - 1) / s.steps - u0 / s.steps + 1;
+}
+template <int PASS>
+static __host__ __device__ __forceinline__ bool head_next(const HeadArgs& a, const HeadShape& s, const HeadShape& w, uint32_t inputs,
+                                                          uint32_t pair, uint32_t i, HeadSegment& g)
+{
+    if (PASS != HEAD_PRODUCTS) return head_segment<PASS>(a, s, pair, i, g);
+    g.input = i < inputs;
+    if (g.input) return head_segment<HEAD_INPUT>(a, s, pair, i, g);
+    if (!a.dw || !head_segment<HEAD_WEIGHT>(a, w, pair, i - inputs, g)) return false;
+    if (g.slot >= 0) g.slot += 2 * ZERO_HD_PAIRS;
+    return true;
+}
+
 // Tiles of the logits: bands of row tiles that stay in L2 while the weights pass by once a band;
 // of the products: bands of eight, which keep a wave's panels few.
 static __host__ __device__ __forceinline__ void head_place(uint32_t band, const HeadShape& s, uint32_t tile, uint32_t& i, uint32_t& j)
@@ -202,6 +226,10 @@ static __device__ __forceinline__ int head_width(const HeadArgs& a, uint32_t j)
 {
     return PASS <= HEAD_GRADIENT || a.cols - (int)j * ZERO_HD_TILE > ZERO_HD_TILE / 2 ? ZERO_HD_TILE : ZERO_HD_TILE / 2;
 }
+
+// Whether the kernel's launch may begin before the one before it has ended: this waits for that one's results.
+static __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+static __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- scalars -------------------------------------------------------------------------
 static __device__ __forceinline__ float power2(int e)       // 2^e, 0 below the normal range
@@ -226,15 +254,18 @@ static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row,
     return __ldg(a.index + row * a.ldt + k) >= 0 && teacher_logit(a, row, k) != __uint_as_float(0xFF800000u);
 }
 
-// The scale of a row's gradient: scale * weight / divisor (0 where the divisor is).
+// What all rows' gradients are multiplied with after the products: scale / divisor (0 where the divisor is), over
+// `unit`.  A row's dz is kept times its weight, or where rows have none times `unit`, one over the sum of the
+// parts' weights: a label's coefficient p - 1 then lies just below a power of two, where rounding it
+// (which is most of dz's rounding) costs least: 0.7 of a rounding at random, in all rows.
+static __device__ __forceinline__ float common_factor(const HeadArgs& a)
+{
+    const float d = a.divisor ? __ldg(a.divisor) : 1.0f;
+    return d == 0.0f ? 0.0f : a.scale / a.unit / d;
+}
 static __device__ __forceinline__ float row_scale(const HeadArgs& a, int64_t row)
 {
-    float s = a.scale * (a.weight ? __ldg(a.weight + row) : 1.0f);
-    if (a.divisor) {
-        const float d = __ldg(a.divisor);
-        s = d == 0.0f ? 0.0f : s / d;
-    }
-    return s;
+    return a.weight ? __ldg(a.weight + row) : a.unit;
 }
 // Factors of the two softmaxes in a row's gradient before the row's power of two, and a bound of |dz|.
 static __device__ __forceinline__ void row_factors(const HeadArgs& a, int64_t row, float& s, float& hard, float& soft)
@@ -266,6 +297,7 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
     __shared__ int32_t counts[32], tops[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * ZERO_HD_CHUNK + threadIdx.x;
+    let_next_begin();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.st->err = 0;
         a.st->ticket = 0;
@@ -273,22 +305,16 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
     bool in = row < a.rows;
     if (a.labels) {
         in = in && __ldg(a.labels + row) >= 0;
-    } else {                                 // rows of which the teacher has kept something
-        uint32_t any = 0;
-        for (int r = 0; r < 32; r++) {
-            const int64_t of = row - lane + r;
-            bool has = false;
-            for (int k = lane; of < a.rows && k < a.top; k += 32) has = has || has_entry(a, of, k);
-            any |= (uint32_t)(__any_sync(0xFFFFFFFFu, has) != 0) << r;
-        }
-        in = any >> lane & 1;
+    } else if (in) {                         // rows of which the teacher has kept something
+        in = false;
+        for (int k = 0; k < a.top && !in; k++) in = has_entry(a, row, k);
     }
     int e = -1000;
     if (in && a.backward) {
         float s, hard, soft;
         row_factors(a, row, s, hard, soft);
         const float b = factors_bound(a, s, hard, soft);
-        in = !(b == 0.0f);
+        in = b != 0.0f && common_factor(a) != 0.0f;
         if (in && b - b == 0.0f) e = bound_exponent(b);
     }
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
@@ -358,6 +384,8 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     extern __shared__ int32_t entries_of[];                 // a warp's targets: columns, weights, added weights
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+    let_next_begin();
+    after_previous();
     const int chunks = (int)((a.rows + ZERO_HD_CHUNK - 1) / ZERO_HD_CHUNK);
     int mine = (int)(row < a.rows ? row >> 10 : chunks), before = 0, all = 0, top = -1000;
     for (int c = lane; c < chunks; c += 32) {
@@ -523,6 +551,8 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
 static __global__ void __launch_bounds__(256) k_head_weights(const __grid_constant__ HeadArgs a)
 {
     const int lane = threadIdx.x & 31;
+    let_next_begin();
+    after_previous();
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < a.count_v; r += (int64_t)gridDim.x * 8) {
         const uint16_t* from = a.w + (a.v0 + r) * a.ldw;
         uint16_t* to = a.wp + r * a.wide;
@@ -558,37 +588,6 @@ static __device__ __forceinline__ float read_one(uint32_t at)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(at) : "memory");
     return __uint_as_float(r);
 }
-// A lane's 128 accumulators.
-static __device__ __forceinline__ void read128(uint32_t at, float (&v)[128])
-{
-    uint32_t r[128];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];"
-        "\ntcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
-          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
-          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
-        : "r"(at) : "memory");
-#pragma unroll
-    for (int i = 0; i < 128; i++) v[i] = __uint_as_float(r[i]);
-}
 static __device__ __forceinline__ void read16(uint32_t at, float (&v)[16])
 {
     uint32_t r[16];
@@ -619,7 +618,8 @@ struct HeadShared {
     uint64_t drain;
     uint32_t tmem;
     int dead;
-    float merge[4][32][3];                  // maxima and sums of a tile's right half
+    uint32_t inputs;                        // (products) a pair's segments of dx
+    HeadShape shape, shape_w;
 };
 
 static __device__ __forceinline__ bool head_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
@@ -653,28 +653,28 @@ static __device__ __forceinline__ void put_vectors(uint16_t* to, float (&v)[N], 
 
 // Where row i (packed, or of the piece) of an output lies and what its sums are multiplied by;
 // null if there is none.
-template <int PASS>
-static __device__ __forceinline__ uint16_t* out_row(const HeadArgs& a, int64_t i, int counted, int top, float& factor)
+static __device__ __forceinline__ uint16_t* out_row(const HeadArgs& a, bool input, int64_t i, int counted, int top, float common,
+                                                    float& factor)
 {
-    if (PASS == HEAD_INPUT) {
+    if (input) {
         if (i >= counted) return nullptr;
-        factor = power2(a.exponent[i] - ZERO_HD_SCALE);
+        factor = power2(a.exponent[i] - ZERO_HD_SCALE) * common;
         return a.dx + a.map[i] * a.lddx;
     }
     if (i >= a.count_v) return nullptr;
-    factor = power2(top - ZERO_HD_SCALE);
+    factor = power2(top - ZERO_HD_SCALE) * common;
     return a.dw + (a.v0 + i) * a.lddw;
 }
 
 // N columns from j of a lane's own row.
-template <int DT, int PASS, int N>
-static __device__ __forceinline__ void put_row(const HeadArgs& a, uint16_t* to, float factor, int j, float (&v)[N])
+template <int DT, int N>
+static __device__ __forceinline__ void put_row(const HeadArgs& a, bool input, uint16_t* to, float factor, int j, float (&v)[N])
 {
     if (!to || j >= a.cols) return;
-    const bool add = PASS == HEAD_WEIGHT && a.accumulate;
+    const bool add = !input && a.accumulate;
 #pragma unroll
     for (int c = 0; c < N; c++) v[c] *= factor;
-    if (a.vec && j + N <= a.cols) {
+    if ((input ? a.vec_x : a.vec_w) && j + N <= a.cols) {
         put_vectors<DT, N>(to + j, v, add);
         return;
     }
@@ -687,15 +687,42 @@ static __device__ __forceinline__ void put_row(const HeadArgs& a, uint16_t* to, 
         }
 }
 
+// 32 columns of a lane's row into the warp's 32 rows of 128 bytes, with the swizzle that TMA takes them
+// with (16-byte word q of row r at q ^ (r & 7)): its first or second half.
+template <int DT>
+static __device__ __forceinline__ void lay_half(uint32_t stage, int half, const float (&v)[32])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4)),
+                     "r"(narrow2<DT>(v[8 * q], v[8 * q + 1])), "r"(narrow2<DT>(v[8 * q + 2], v[8 * q + 3])),
+                     "r"(narrow2<DT>(v[8 * q + 4], v[8 * q + 5])), "r"(narrow2<DT>(v[8 * q + 6], v[8 * q + 7])) : "memory");
+}
+// The warp's rows on their way to column x, row y of a matrix; and the wait until they have been read.
+static __device__ __forceinline__ void send_rows(uint32_t stage, const CUtensorMap* map, int x, int y)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n"
+                     "cp.async.bulk.commit_group;" ::"l"(map), "r"(x), "r"(y), "r"(stage) : "memory");
+}
+static __device__ __forceinline__ void rows_sent()
+{
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
 // put_row() for rows that are not aligned to vectors: 32 columns of the warp's rows through 2 KB of
 // shared memory, so that an access of the warp is a run of a row and not an element of each of 32
 // rows.  16-byte word q of row r lies at q ^ (r >> 1 & 3), so that lanes that each take a row meet all banks too.
-template <int DT, int PASS>
-static __device__ __forceinline__ void put_rows(const HeadArgs& a, uint16_t* to, float factor, int j, float (&v)[32], uint32_t stage)
+template <int DT>
+static __device__ __forceinline__ void put_rows(const HeadArgs& a, bool input, uint16_t* to, float factor, int j, float (&v)[32], uint32_t stage)
 {
     const int lane = threadIdx.x & 31;
     if (j >= a.cols) return;                                 // all lanes
-    const bool add = PASS == HEAD_WEIGHT && a.accumulate;
+    const bool add = !input && a.accumulate;
     const uint32_t own = stage + lane * 64;
     const uint64_t mine = reinterpret_cast<uint64_t>(to);
     if (add) {
@@ -749,11 +776,14 @@ static __device__ __forceinline__ int first_target(const HeadArgs& a, const int3
 }
 
 // ---- the products --------------------------------------------------------------------
+// map_a, map_b: the operands of the logits or of dx; map_c, map_d: of dw; map_o: where the pass's
+// output goes by TMA (dz; dw where its rows are aligned).
 template <int DT, int PASS, bool TWO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
-    k_head(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 1)
+    k_head(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+           const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_o)
 {
-    constexpr bool ROWS_A = PASS != HEAD_WEIGHT, ROWS_B = PASS <= HEAD_GRADIENT;    // contracted axis contiguous
+    constexpr int WRITERS = head_writers(PASS), WIDE = 4 * ZERO_HD_TILE / WRITERS;      // columns of a writer
     extern __shared__ unsigned char raw[];
     __shared__ HeadShared sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -768,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(smem_u32(&sh.sum_full[s]), 1);
-            mbar_init(smem_u32(&sh.sum_empty[s]), 2 * ZERO_HD_WRITERS);
+            mbar_init(smem_u32(&sh.sum_empty[s]), 2 * WRITERS);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.dead = 0;
@@ -782,19 +812,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+    let_next_begin();
+    after_previous();
     const int counted = a.st->rows;
-    const HeadShape shape = head_shape<PASS>(a, counted);
-    const uint32_t band = head_band<PASS>(a);
-    HeadSegment g;
+    // kept in shared memory: the writers' registers hold sums
+    if (threadIdx.x == 0) {
+        sh.shape = head_shape<PASS == HEAD_PRODUCTS ? HEAD_INPUT : PASS>(a, counted);
+        if (PASS == HEAD_PRODUCTS) {
+            sh.shape_w = head_shape<HEAD_WEIGHT>(a, counted);
+            sh.inputs = head_inputs(a, sh.shape, pair);
+        }
+    }
+    __syncthreads();
+    const HeadShape &shape = sh.shape, &shape_w = sh.shape_w;
+    const uint32_t& inputs = sh.inputs;
+    HeadSegment g{};
+    // the segment's tile, and whether it is one of dw
+    auto place = [&](uint32_t& ti, uint32_t& tj) {
+        const bool w = PASS == HEAD_PRODUCTS && !g.input;
+        head_place(head_band<PASS>(a), w ? shape_w : shape, g.tile, ti, tj);
+        return w;
+    };
 
     if (warp == 0) {
         // ---- loads ----
         if (elected()) {
             uint32_t n = 0, s = 0, ph = 0;
             bool ok = true;
-            for (int i = 0; ok && head_segment<PASS>(a, shape, pair, i, g); i++) {
+            for (int i = 0; ok && head_next<PASS>(a, shape, shape_w, inputs, pair, i, g); i++) {
                 uint32_t ti, tj;
-                head_place(band, shape, g.tile, ti, tj);
+                const bool dw = place(ti, tj);
                 const int half = head_width<PASS>(a, tj) / 2;
                 const int ra = (int)ti * ZERO_HD_TILE + rank * 128, rb = (int)tj * ZERO_HD_TILE + rank * half;
                 const uint32_t bytes = 2 * (ZERO_HD_SIDE + half * 128);
@@ -806,18 +853,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     const uint32_t bar = smem_u32(&sh.full[s]), at = base + s * 2 * ZERO_HD_SIDE, bt = at + ZERO_HD_SIDE;
                     const int k = t * ZERO_HD_STEP;
                     if (rank == 0) mbar_expect_tx(bar, bytes);
-                    if (ROWS_A) {
+                    if (dw) {
+                        box_for_first(at, &map_c, ra, k, bar);
+                        box_for_first(at + 8192, &map_c, ra + 64, k, bar);
+                        box_for_first(bt, &map_d, rb, k, bar);
+                        if (half > 64) box_for_first(bt + 8192, &map_d, rb + 64, k, bar);
+                    } else {
                         box_for_first(at, &map_a, k, ra, bar);
-                    } else {
-                        box_for_first(at, &map_a, ra, k, bar);
-                        box_for_first(at + 8192, &map_a, ra + 64, k, bar);
-                    }
-                    if (ROWS_B) {
-                        box_for_first(bt, &map_b, k, a.wy + rb, bar);
-                    } else {
-                        const int y = PASS == HEAD_INPUT ? a.wy + k : k;
-                        box_for_first(bt, &map_b, rb, y, bar);
-                        if (half > 64) box_for_first(bt + 8192, &map_b, rb + 64, y, bar);
+                        if (PASS == HEAD_PRODUCTS) {
+                            box_for_first(bt, &map_b, rb, a.wy + k, bar);
+                            if (half > 64) box_for_first(bt + 8192, &map_b, rb + 64, a.wy + k, bar);
+                        } else {
+                            box_for_first(bt, &map_b, k, a.wy + rb, bar);
+                        }
                     }
                     if (++s == ZERO_HD_STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -835,21 +883,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
     } else if (warp == 1) {
         // ---- products (the first SM's thread, for both) ----
         if (rank == 0 && elected()) {
-            const uint32_t kind = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | (ROWS_A ? 0u : 1u << 15) |
-                                  (ROWS_B ? 0u : 1u << 16) | (uint32_t)(ZERO_HD_TILE >> 4) << 24;
-            constexpr uint32_t STEP_A = (ROWS_A ? 32 : 2048) >> 4, STEP_B = (ROWS_B ? 32 : 2048) >> 4;
+            // fp32 sums of fp16/bf16 operands, 256 x width; the contracted axis is strided in w and x of
+            // dx and dw and in dz of dw
+            const uint32_t kind = 1u << 4 | (DT == 1 ? 1u << 7 | 1u << 10 : 0u) | (PASS == HEAD_PRODUCTS ? 1u << 16 : 0u) |
+                                  (uint32_t)(ZERO_HD_TILE >> 4) << 24;
+            constexpr uint32_t ROWS = 32 >> 4, STRIDED = 2048 >> 4, STEP_B = PASS == HEAD_PRODUCTS ? STRIDED : ROWS;
             uint32_t s = 0, ph = 0;
             bool ok = true;
             int i = 0;
-            for (; ok && head_segment<PASS>(a, shape, pair, i, g); i++) {
+            for (; ok && head_next<PASS>(a, shape, shape_w, inputs, pair, i, g); i++) {
                 const int acc = i & 1;
                 if (i >= 2 && !head_wait(smem_u32(&sh.sum_empty[acc]), (uint32_t)((i >> 1) - 1) & 1u, dead, err)) {
                     ok = false;
                     break;
                 }
                 uint32_t ti, tj;
-                head_place(band, shape, g.tile, ti, tj);
-                const uint32_t what = kind | (uint32_t)(head_width<PASS>(a, tj) >> 3) << 17;
+                const bool dw = place(ti, tj);
+                const uint32_t what = kind | (dw ? 1u << 15 : 0u) | (uint32_t)(head_width<PASS>(a, tj) >> 3) << 17;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int t = g.s0; t < g.s1; t++) {
                     if (!head_wait(smem_u32(&sh.full[s]), ph, dead, err)) {
@@ -858,10 +908,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t at = base + s * 2 * ZERO_HD_SIDE, bt = at + ZERO_HD_SIDE;
-                    const uint64_t da = ROWS_A ? operand_rows(at) : operand(at), db = ROWS_B ? operand_rows(bt) : operand(bt);
+                    const uint64_t da = dw ? operand(at) : operand_rows(at), db = PASS == HEAD_PRODUCTS ? operand(bt) : operand_rows(bt);
+                    const uint32_t step_a = dw ? STRIDED : ROWS;
 #pragma unroll
                     for (int q = 0; q < ZERO_HD_STEP / 16; q++)
-                        product(tmem + acc * ZERO_HD_TILE, da + q * STEP_A, db + q * STEP_B, what, t > g.s0 || q > 0);
+                        product(tmem + acc * ZERO_HD_TILE, da + q * step_a, db + q * STEP_B, what, t > g.s0 || q > 0);
                     commit_both(smem_u32(&sh.empty[s]));
                     if (++s == ZERO_HD_STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -877,22 +928,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
             }
         }
     } else if (warp >= 4) {
-        // ---- output: warp w reads rows 32 (w mod 4) + lane of this SM's half, 128 columns ----
+        // ---- output: warp w reads rows 32 (w mod 4) + lane of this SM's half, WIDE columns ----
         const int quad = warp & 3, side = (warp - 4) >> 2;
-        const float nan = __uint_as_float(0x7FC00000u);
-        const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
-        const int top = a.st->top;
-        [[maybe_unused]] float z[PASS == HEAD_LOGITS ? 128 : 1];
-        for (int i = 0; head_segment<PASS>(a, shape, pair, i, g); i++) {
+        const float nan = __uint_as_float(0x7FC00000u), low = __uint_as_float(0xFF800000u);
+        [[maybe_unused]] const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
+        [[maybe_unused]] const int top = a.st->top;
+        [[maybe_unused]] const float common = PASS == HEAD_PRODUCTS ? common_factor(a) : 0.0f;
+        [[maybe_unused]] float z[PASS == HEAD_LOGITS ? WIDE : 1];
+        // maxima and sums of a tile's column groups but the first: [group][which][lane] of this quad
+        [[maybe_unused]] const auto merge = reinterpret_cast<float(*)[3][32]>(
+            raw + (base - smem_u32(raw)) + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + quad * (9 * 32 * 4));
+        for (int i = 0; head_next<PASS>(a, shape, shape_w, inputs, pair, i, g); i++) {
             const int acc = i & 1;
             uint32_t ti, tj;
-            head_place(band, shape, g.tile, ti, tj);
+            const bool dw = place(ti, tj);
             const int64_t r = (int64_t)ti * ZERO_HD_TILE + rank * 128 + quad * 32 + lane;
-            const uint32_t from = tmem + acc * ZERO_HD_TILE + side * 128 + ((uint32_t)quad << 21);
-            const int width = head_width<PASS>(a, tj);
+            const uint32_t from = tmem + acc * ZERO_HD_TILE + side * WIDE + ((uint32_t)quad << 21);
             const bool live = r < counted;
             // what does not depend on the sums, while they are made
-            [[maybe_unused]] const int c0 = (int)tj * ZERO_HD_TILE + side * 128;      // first column, of the piece
+            [[maybe_unused]] const int c0 = (int)tj * ZERO_HD_TILE + side * WIDE;     // first column, of the piece
             [[maybe_unused]] const int end = a.count_v - c0;                          // columns there are from it
             [[maybe_unused]] int next = 0;
             [[maybe_unused]] int goal = ZERO_HD_NONE;                                 // the next target's column, from c0
@@ -907,139 +961,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     if (next < a.slots) goal = __ldg(columns + next) - a.v0 - c0;
                     if (PASS == HEAD_GRADIENT) row = a.info[r];
                 }
-            } else if (g.slot < 0 && a.last) {
-                to = out_row<PASS>(a, r, counted, top, factor);
-            } else if (g.slot < 0 && PASS == HEAD_WEIGHT) {
-                to = out_row<PASS>(a, r, counted, top, factor);
+            } else if (g.slot < 0 && (dw || a.last)) {
+                to = out_row(a, !dw, r, counted, top, common, factor);
             }
             const bool have = __all_sync(0xFFFFFFFFu, head_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, err));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if constexpr (PASS == HEAD_LOGITS) {
-                // z: the tile's sums, runs of it added in fp32
-                if (g.first) {
-                    read128(from, z);
-                } else {
+                // z: the tile's sums, runs of it added in fp32.  Logits of targets in these columns: a
+                // lane's accumulators are read at a column of the warp's choice, where the added ones are put back
+                const bool sought = g.last && __any_sync(0xFFFFFFFFu, goal < WIDE);
 #pragma unroll
-                    for (int c = 0; c < 128; c += 16) {
-                        float v[16];
-                        read16(from + c, v);
+                for (int c = 0; c < WIDE; c += 16) {
+                    float v[16];
+                    read16(from + c, v);
+                    if (!g.first) {
 #pragma unroll
-                        for (int e = 0; e < 16; e++) z[c + e] += v[e];
+                        for (int e = 0; e < 16; e++) v[e] += z[c + e];
+                        if (sought) write16(from + c, v);
                     }
-                }
-                if (g.last) {
-                    // logits of targets in these columns: a lane's accumulators are read at a column
-                    // of the warp's choice
-                    if (__any_sync(0xFFFFFFFFu, goal < 128)) {
-                        if (!g.first) {
 #pragma unroll
-                            for (int c = 0; c < 128; c += 16) write16(from + c, z + c);
-                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    for (int e = 0; e < 16; e++) z[c + e] = v[e];
+                }
+                if (sought) {
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < WIDE;) {
+                        const float v = read_one(from + c);
+                        if (goal == c) {
+                            a.found[r * a.slots + next] = have ? v : nan;
+                            next++;
+                            goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
                         }
-                        for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < 128;) {
-                            const float v = read_one(from + c);
-                            if (goal == c) {
-                                a.found[r * a.slots + next] = have ? v : nan;
-                                next++;
-                                goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
-                            }
-                            __syncwarp();
-                        }
+                        __syncwarp();
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
                 if (!g.last) continue;
-                if (end < 128) {
+                if (end < WIDE) {
 #pragma unroll
-                    for (int c = 0; c < 128; c++)
-                        if (c >= end) z[c] = __uint_as_float(0xFF800000u);
+                    for (int c = 0; c < WIDE; c++)
+                        if (c >= end) z[c] = low;
                 }
                 float m[4], s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int e = 0; e < 4; e++) m[e] = z[e];
 #pragma unroll
-                for (int c = 4; c < 128; c++) m[c & 3] = fmaxf(m[c & 3], z[c]);
+                for (int c = 4; c < WIDE; c++) m[c & 3] = fmaxf(m[c & 3], z[c]);
                 float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 if (end > 0) {
                     const float b1 = -most * a.k1, b2 = -most * a.k2;
 #pragma unroll
-                    for (int c = 0; c < 128; c++) {
+                    for (int c = 0; c < WIDE; c++) {
                         s[c & 3] += exp2_fast(__fmaf_rn(z[c], a.k1, b1));
                         if (TWO) s2[c & 3] += exp2_fast(__fmaf_rn(z[c], a.k2, b2));
                     }
                 }
                 float sum = (s[0] + s[1]) + (s[2] + s[3]), sum2 = (s2[0] + s2[1]) + (s2[2] + s2[3]);
                 if (!have) sum = sum2 = nan;
-                // the tile's two halves
-                if (side == 1) {
-                    sh.merge[quad][lane][0] = most;
-                    sh.merge[quad][lane][1] = sum;
-                    if (TWO) sh.merge[quad][lane][2] = sum2;
+                // the tile's column groups
+                if (side > 0) {
+                    merge[side - 1][0][lane] = most;
+                    merge[side - 1][1][lane] = sum;
+                    if (TWO) merge[side - 1][2][lane] = sum2;
                 }
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
                 if (side == 0) {
-                    const float other = sh.merge[quad][lane][0], both = fmaxf(most, other);
-                    const float f0 = exp2_fast((most - both) * a.k1), f1 = exp2_fast((other - both) * a.k1);
-                    sum = sum * f0 + sh.merge[quad][lane][1] * f1;
-                    if (TWO) {
-                        const float h0 = exp2_fast((most - both) * a.k2), h1 = exp2_fast((other - both) * a.k2);
-                        sum2 = sum2 * h0 + sh.merge[quad][lane][2] * h1;
+                    float o[3], all = most;
+#pragma unroll
+                    for (int e = 0; e < 3; e++) {
+                        o[e] = merge[e][0][lane];
+                        all = fmaxf(all, o[e]);
+                    }
+                    sum *= exp2_fast((most - all) * a.k1);
+                    if (TWO) sum2 *= exp2_fast((most - all) * a.k2);
+#pragma unroll
+                    for (int e = 0; e < 3; e++) {
+                        sum += merge[e][1][lane] * exp2_fast((o[e] - all) * a.k1);
+                        if (TWO) sum2 += merge[e][2][lane] * exp2_fast((o[e] - all) * a.k2);
                     }
                     if (live) {
                         const int64_t at = (int64_t)(a.v0 / ZERO_HD_TILE + tj) * a.npad + r;
-                        a.part[at] = make_float2(both, sum);
+                        a.part[at] = make_float2(all, sum);
                         if (TWO) a.part2[at] = sum2;
                     }
                 }
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
             } else if constexpr (PASS == HEAD_GRADIENT) {
-                uint16_t* out = a.dz + r * a.pitch + c0;
-                for (int c = 0; c < 128; c += 32) {
-                    float v[32];
-                    __syncwarp();
-                    read_accumulator(from + c, v);
+                for (int c = 0; c < WIDE; c += 64) {
 #pragma unroll
-                    for (int e = 0; e < 32; e++) {
-                        float d = row.c1 * exp2_fast(__fmaf_rn(v[e], a.k1, -row.l1));
-                        if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v[e], a.k2, -row.l2)), d);
-                        v[e] = d;
-                    }
-                    if (!live || c + 32 > end) {
+                    for (int h = 0; h < 2; h++) {
+                        float v[32];
+                        __syncwarp();
+                        read_accumulator(from + c + 32 * h, v);
 #pragma unroll
-                        for (int e = 0; e < 32; e++)
-                            if (!live || c + e >= end) v[e] = 0.0f;
-                    }
-                    if (!have) {
+                        for (int e = 0; e < 32; e++) {
+                            float d = row.c1 * exp2_fast(__fmaf_rn(v[e], a.k1, -row.l1));
+                            if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v[e], a.k2, -row.l2)), d);
+                            v[e] = d;
+                        }
+                        if (!live || c + 32 * h + 32 > end) {
 #pragma unroll
-                        for (int e = 0; e < 32; e++) v[e] = nan;
+                            for (int e = 0; e < 32; e++)
+                                if (!live || c + 32 * h + e >= end) v[e] = 0.0f;
+                        }
+                        if (!have) {
+#pragma unroll
+                            for (int e = 0; e < 32; e++) v[e] = nan;
+                        }
+                        if (h == 0) rows_sent();
+                        lay_half<DT>(stage, h, v);
                     }
-                    put_vectors<DT, 32>(out + c, v, false);
-                }
-                // once more where the targets are
-                for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < 128;) {
-                    const float v = read_one(from + c);
-                    if (goal == c) {
-                        float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1));
-                        if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v, a.k2, -row.l2)), d);
-                        out[c] = narrow1<DT>(d - __ldg(a.target + r * a.slots + next));
-                        next++;
-                        goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
+                    // once more where the targets are
+                    for (int t; (t = __reduce_min_sync(0xFFFFFFFFu, goal)) < c + 64;) {
+                        const float v = read_one(from + t);
+                        if (goal == t) {
+                            float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1));
+                            if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v, a.k2, -row.l2)), d);
+                            d = have ? d - __ldg(a.target + r * a.slots + next) : nan;
+                            const int in = t - c;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + lane * 128 + (((in >> 3) ^ (lane & 7)) << 4) + (in & 7) * 2),
+                                         "h"(narrow1<DT>(d)) : "memory");
+                            next++;
+                            goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    send_rows(stage, &map_o, c0 + c, (int)(r - lane));
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
             } else {
-                const int j = (int)tj * ZERO_HD_TILE;
+                const int j = (int)tj * ZERO_HD_TILE, width = head_width<PASS>(a, tj);
                 // four columns of 32 rows are one run of 512 bytes
                 const int64_t own = (int64_t)((rank * 4 + quad) * 64) * 32 + lane;
                 float4* part = g.slot < 0 ? nullptr : reinterpret_cast<float4*>(a.parts + (int64_t)g.slot * ZERO_HD_SLOT) + own;
-                float4* kept = PASS == HEAD_INPUT ? reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own
-                                                  : nullptr;
-                for (int c = side * 128; c < (side + 1) * 128 && c < width; c += 32) {
+                float4* kept = dw ? nullptr : reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
+                const bool sent = dw && !part && a.vec_w && !a.accumulate;
+                for (int c = side * WIDE; c < (side + 1) * WIDE && c < width; c += 32) {
                     float v[32];
                     __syncwarp();
                     read_accumulator(tmem + acc * ZERO_HD_TILE + c + ((uint32_t)quad << 21), v);
@@ -1047,7 +1107,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] = nan;
                     }
-                    if (!part && PASS == HEAD_INPUT && !a.first) {
+                    if (!part && !dw && !a.first) {
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
                             const float4 p = kept[(c / 4 + e) * 32];
@@ -1057,15 +1117,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                             v[4 * e + 3] += p.w;
                         }
                     }
-                    if (part || (PASS == HEAD_INPUT && !a.last)) {
+                    if (part || (!dw && !a.last)) {
                         float4* o = part ? part : kept;
 #pragma unroll
                         for (int e = 0; e < 8; e++)
                             o[(c / 4 + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    } else if (a.vec) {
-                        put_row<DT, PASS, 32>(a, to, factor, j + c, v);
+                    } else if (sent) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) v[e] *= factor;
+                        if (!(c & 32)) rows_sent();
+                        lay_half<DT>(stage, c >> 5 & 1, v);
+                        if (c & 32) send_rows(stage, &map_o, j + c - 32, a.v0 + (int)(r - lane));
+                    } else if (dw ? a.vec_w : a.vec_x) {
+                        put_row<DT, 32>(a, !dw, to, factor, j + c, v);
                     } else {
-                        put_rows<DT, PASS>(a, to, factor, j + c, v, stage);
+                        put_rows<DT>(a, !dw, to, factor, j + c, v, stage);
                     }
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1073,6 +1139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                 if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
             }
         }
+        // rows on their way have been written before the kernel ends
+        if (PASS != HEAD_LOGITS && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     cluster_sync();
     if (warp == 1)
@@ -1080,60 +1148,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
     cluster_sync();
 }
 
-// Adds the parts of the cut tiles in the contracted axis's order: a warp takes 32 rows and 16 columns of a tile.
+// Adds the parts of cut tiles of one pass in the contracted axis's order: a warp takes 32 rows and 16
+// columns of a tile.
 template <int DT, int PASS>
-__global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadArgs a)
+static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& shape, uint32_t unit, int counted, int top, float common)
 {
-    const int counted = a.st->rows, top = a.st->top, lane = threadIdx.x & 31;
-    const HeadShape shape = head_shape<PASS>(a, counted);
-    if (shape.rest_pairs <= shape.rest) return;
-    for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < shape.rest * 128; unit += gridDim.x * 8) {
-        const uint32_t q = unit >> 7;
-        const int strip = (unit >> 4) & 7, c = unit & 15;
-        const uint32_t p0 = head_owner(shape, q * shape.steps), p1 = head_owner(shape, (q + 1) * shape.steps - 1);
-        uint32_t ti, tj;
-        head_place(head_band<PASS>(a), shape, shape.waves * a.pairs + q, ti, tj);
-        const int j = (int)tj * ZERO_HD_TILE + c * 16;
-        if (p0 == p1 || j >= a.cols) continue;
-        const uint32_t second = head_share(shape, p0) / shape.steps < q;
-        float v[16];
+    constexpr bool INPUT = PASS == HEAD_INPUT;
+    const int lane = threadIdx.x & 31;
+    const uint32_t q = unit >> 7;
+    const int strip = (unit >> 4) & 7, c = unit & 15;
+    const uint32_t p0 = head_owner(shape, q * shape.steps), p1 = head_owner(shape, (q + 1) * shape.steps - 1);
+    uint32_t ti, tj;
+    head_place(head_band<PASS>(a), shape, shape.waves * a.pairs + q, ti, tj);
+    const int j = (int)tj * ZERO_HD_TILE + c * 16;
+    if (p0 == p1 || j >= a.cols) return;
+    const uint32_t second = head_share(shape, p0) / shape.steps < q;
+    const float* parts = a.parts + (INPUT ? 0 : 2ll * ZERO_HD_PAIRS * ZERO_HD_SLOT);
+    float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; e++) v[e] = 0.0f;
-        const int64_t own = (int64_t)(strip * 64 + c * 4) * 32 + lane;
+    for (int e = 0; e < 16; e++) v[e] = 0.0f;
+    const int64_t own = (int64_t)(strip * 64 + c * 4) * 32 + lane;
 #pragma unroll 4
-        for (uint32_t p = p0; p <= p1; p++) {
-            const float4* s = reinterpret_cast<const float4*>(a.parts + (int64_t)(2 * p + (p == p0 ? second : 0)) * ZERO_HD_SLOT) + own;
+    for (uint32_t p = p0; p <= p1; p++) {
+        const float4* s = reinterpret_cast<const float4*>(parts + (int64_t)(2 * p + (p == p0 ? second : 0)) * ZERO_HD_SLOT) + own;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float4 f = __ldcg(s + e * 32);
+            v[4 * e] += f.x;
+            v[4 * e + 1] += f.y;
+            v[4 * e + 2] += f.z;
+            v[4 * e + 3] += f.w;
+        }
+    }
+    const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
+    if (INPUT) {
+        float4* kept = reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
+        if (!a.first) {
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const float4 f = __ldcg(s + e * 32);
+                const float4 f = kept[e * 32];
                 v[4 * e] += f.x;
                 v[4 * e + 1] += f.y;
                 v[4 * e + 2] += f.z;
                 v[4 * e + 3] += f.w;
             }
         }
-        const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
-        if (PASS == HEAD_INPUT) {
-            float4* kept = reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
-            if (!a.first) {
+        if (!a.last) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float4 f = kept[e * 32];
-                    v[4 * e] += f.x;
-                    v[4 * e + 1] += f.y;
-                    v[4 * e + 2] += f.z;
-                    v[4 * e + 3] += f.w;
-                }
-            }
-            if (!a.last) {
-#pragma unroll
-                for (int e = 0; e < 4; e++) kept[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                continue;
-            }
+            for (int e = 0; e < 4; e++) kept[e * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            return;
         }
-        float factor = 0.0f;
-        uint16_t* to = out_row<PASS>(a, r, counted, top, factor);
-        put_row<DT, PASS, 16>(a, to, factor, j, v);
+    }
+    float factor = 0.0f;
+    uint16_t* to = out_row(a, INPUT, r, counted, top, common, factor);
+    put_row<DT, 16>(a, INPUT, to, factor, j, v);
+}
+template <int DT>
+__global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadArgs a)
+{
+    let_next_begin();
+    after_previous();
+    const int counted = a.st->rows, top = a.st->top;
+    const float common = common_factor(a);
+    const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
+    const uint32_t of_x = a.dx && x.rest_pairs > x.rest ? x.rest * 128 : 0, of_w = a.dw && w.rest_pairs > w.rest ? w.rest * 128 : 0;
+    for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < of_x + of_w; unit += gridDim.x * 8) {
+        if (unit < of_x) join<DT, HEAD_INPUT>(a, x, unit, counted, top, common);
+        else join<DT, HEAD_WEIGHT>(a, w, unit - of_x, counted, top, common);
     }
 }
 
@@ -1145,6 +1226,8 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
     __shared__ float ms[32][32], ss[32][32], ts[32][32], dots[32];
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    let_next_begin();
+    after_previous();
     const int counted = a.st->rows;
     const int64_t r = (int64_t)blockIdx.x * 32 + lane;
     const float low = __uint_as_float(0xFF800000u), nan = __uint_as_float(0x7FC00000u);
@@ -1227,7 +1310,7 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
 
 // The kernels of a 16-bit type.
 struct HeadKernels {
-    const void *pack, *logits[2], *gradient[2], *input, *weight, *join_input, *join_weight;
+    const void *pack, *logits[2], *gradient[2], *products, *join;
 };
 HeadKernels head_kernels_fp16();
 HeadKernels head_kernels_bf16();
@@ -1238,10 +1321,8 @@ HeadKernels head_kernels()
     return {(const void*)k_head_pack<DT>,
             {(const void*)k_head<DT, HEAD_LOGITS, false>, (const void*)k_head<DT, HEAD_LOGITS, true>},
             {(const void*)k_head<DT, HEAD_GRADIENT, false>, (const void*)k_head<DT, HEAD_GRADIENT, true>},
-            (const void*)k_head<DT, HEAD_INPUT, false>,
-            (const void*)k_head<DT, HEAD_WEIGHT, false>,
-            (const void*)k_head_join<DT, HEAD_INPUT>,
-            (const void*)k_head_join<DT, HEAD_WEIGHT>};
+            (const void*)k_head<DT, HEAD_PRODUCTS, false>,
+            (const void*)k_head_join<DT>};
 }
 
 }  // namespace zero

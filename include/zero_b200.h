@@ -662,7 +662,7 @@ uint64_t zero_norm_workspace(const zero_norm_t* norm);
  *   dtype        fp16 or bf16: x, w, dx, dw.
  *   piece        columns of the vocabulary that the backward pass keeps the logits'
  *                gradient of at a time (2 rows piece bytes of workspace), rounded up
- *                to 256, at most 65536; 0: the library's choice (about 512 MB).
+ *                to 256, at most 65536; 0: the library's choice (up to 1 GB).
  *   z_loss       weight of the squared log-sum-exp (0: none).
  *   top, top_dtype, temperature, hard, soft   zero_distill_* only: the teacher's
  *                entries of a row, the type of its logits (fp16, bf16, fp32), the

@@ -23,20 +23,22 @@ bool described(const zero_head_t* h)
            isfinite(h->temperature) && h->temperature > 0.0f && isfinite(1.4426950408889634f / h->temperature);
 }
 
-// Columns of a piece of the vocabulary: whole tiles; by default as many as keep dz and a copy of
-// the weights' piece within 512 and 256 MB.
-int64_t piece_of(const zero_head_t* h, int64_t npad, int64_t wide)
+// Columns of a piece of the vocabulary, whole tiles: by default as many as keep dz within 1 GB, and pieces
+// of about equal lengths.  Fewer where the weights are copied: within 256 MB of them.
+int64_t even(int64_t vocab, int64_t most)
 {
-    int64_t most = MOST_PIECE;
-    if (h->piece > 0) {
-        most = h->piece < MOST_PIECE ? h->piece : MOST_PIECE;
-    } else {
-        const int64_t a = (1ll << 28) / npad, b = (1ll << 27) / wide, c = a < b ? a : b;
-        most = c < 4096 ? 4096 : c < MOST_PIECE ? c : MOST_PIECE;
-    }
     most = up(most, ZERO_HD_TILE) * ZERO_HD_TILE;
-    const int64_t pieces = up(h->vocab, most);
-    return up(up(h->vocab, pieces), ZERO_HD_TILE) * ZERO_HD_TILE;
+    return up(up(vocab, up(vocab, most)), ZERO_HD_TILE) * ZERO_HD_TILE;
+}
+int64_t piece_of(const zero_head_t* h, int64_t npad)
+{
+    const int64_t room = (1ll << 29) / npad, want = h->piece > 0 ? h->piece : room < 4096 ? 4096 : room;
+    return even(h->vocab, want < MOST_PIECE ? want : MOST_PIECE);
+}
+int64_t copied_of(int64_t piece, int64_t wide)
+{
+    const int64_t room = (1ll << 27) / wide;
+    return room < piece ? even(piece, room) : piece;
 }
 
 // Lays the workspace out from `at`; returns its bytes.
@@ -50,7 +52,7 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     const int64_t rows = h->rows > 0 ? h->rows : 1, chunks = up(rows, ZERO_HD_CHUNK), tiles = up(h->vocab, ZERO_HD_TILE);
     a.npad = up(rows, ZERO_HD_TILE) * ZERO_HD_TILE;
     a.wide = (int)(up(h->cols, ZERO_HD_STEP) * ZERO_HD_STEP);
-    a.pitch = piece_of(h, a.npad, a.wide);
+    a.pitch = piece_of(h, a.npad);
     take(a.st, 1);
     take(a.mask, chunks * 32);
     take(a.count, chunks);
@@ -58,10 +60,9 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     take(a.map, a.npad);
     take(a.exponent, a.npad);
     take(a.info, a.npad);
-    take(a.column, rows * (h->top + 1));
     take(a.target, rows * (h->top + 1));
     take(a.xp, a.npad * a.wide);
-    take(a.wp, a.pitch * a.wide);
+    take(a.wp, copied_of(a.pitch, a.wide) * a.wide);
     char* const rest = at;
     take(a.found, rows * (h->top + 1));       // forward
     take(a.partial, a.npad / 32);
@@ -91,7 +92,7 @@ int device_pairs(const HeadKernels& k)
     if (pairs[dev] == 0) {
         cudaLaunchConfig_t c{};
         c.gridDim = dim3(2 * ZERO_HD_PAIRS);
-        c.blockDim = dim3(head_threads(HEAD_PRODUCTS));
+        c.blockDim = dim3(ZERO_HD_THREADS);
         c.dynamicSmemBytes = ZERO_HD_SMEM;
         cudaLaunchAttribute at{};
         at.id = cudaLaunchAttributeClusterDimension;
@@ -169,9 +170,14 @@ bool run_rows(const HeadArgs& a, const HeadKernels& k, void* stream)
 {
     void* args[] = {const_cast<HeadArgs*>(&a)};
     return launch((const void*)k_head_rows, dim3((unsigned)up(a.rows, ZERO_HD_CHUNK)), ZERO_HD_CHUNK, 0, args, stream) &&
-           launch_next(k.pack, dim3((unsigned)up(a.rows + ZERO_HD_TILE, 8)), 256, 8 * 3 * a.slots * 4, args, stream);
+           launch_next(k.pack, dim3((unsigned)up(a.rows + ZERO_HD_TILE, 8)), 256, 8 * 2 * ((a.slots + 3) & ~3) * 4, args, stream);
 }
 
+// Rows that leave from a writer's 32 rows of 32 columns.
+bool map_out(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld)
+{
+    return tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, cols, rows, ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
 bool map16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows)
 {
     return tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, cols, rows, ld * 2, ZERO_HD_STEP, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -189,11 +195,11 @@ bool copy_weights(const HeadArgs& a, int pairs, void* stream)
     const int64_t most = 16ll * pairs, want = up(a.count_v, 8);
     return launch_next((const void*)k_head_weights, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream);
 }
-bool product(const void* fn, int pass, HeadArgs& a, int64_t tiles, int pairs, CUtensorMap* const (&maps)[5], void* stream)
+bool product(const void* fn, HeadArgs& a, int64_t tiles, int pairs, CUtensorMap* const (&maps)[5], void* stream)
 {
     a.pairs = (int)(tiles < pairs ? tiles : pairs);
     void* args[] = {&a, maps[0], maps[1], maps[2], maps[3], maps[4]};
-    return launch_next(fn, dim3(2 * a.pairs), head_threads(pass), ZERO_HD_SMEM, args, stream);
+    return launch_next(fn, dim3(2 * a.pairs), ZERO_HD_THREADS, ZERO_HD_SMEM, args, stream);
 }
 
 zero_status_t forward(const zero_head_t* h, const void* x, int64_t ldx, const void* w, int64_t ldw, bool distill,
@@ -216,13 +222,13 @@ zero_status_t forward(const zero_head_t* h, const void* x, int64_t ldx, const vo
     const bool copied = !aligned_to(w, 16) || ldw % 8 != 0;
     CUtensorMap mx, mw;
     if (!map16(&mx, a.xp, a.wide, a.npad, a.wide, 128)) return ZERO_ECUDA;
-    const int64_t step = copied ? a.pitch : h->vocab;
+    const int64_t step = copied ? copied_of(a.pitch, a.wide) : h->vocab;
     for (int64_t v = 0; v < h->vocab; v += step) {
         a.v0 = (int)v;
         a.count_v = (int)(h->vocab - v < step ? h->vocab - v : step);
         if (copied && !copy_weights(a, pairs, stream)) return ZERO_ECUDA;
         if (!weights(a, 128, copied, &mw) ||
-            !product(k.logits[a.two], HEAD_LOGITS, a, a.npad / ZERO_HD_TILE * up(a.count_v, ZERO_HD_TILE), pairs,
+            !product(k.logits[a.two], a, a.npad / ZERO_HD_TILE * up(a.count_v, ZERO_HD_TILE), pairs,
                      {&mx, &mw, &mx, &mw, &mx}, stream))
             return ZERO_ECUDA;
     }
@@ -266,19 +272,20 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     a.vec_w = aligned_to(dw, 16) && lddw % 8 == 0;
     if (!map16(&mx, a.xp, a.wide, a.npad, a.wide, 128) || !map16(&ms, a.xs, a.wide, a.npad, a.wide, 64) ||
         !map16(&mz, a.dz, a.pitch, a.npad, a.pitch, 128) || !map16(&mt, a.dz, a.pitch, a.npad, a.pitch, 64) ||
-        !map16(&mo, a.dz, a.pitch, a.npad, a.pitch, 32))
+        !map_out(&mo, a.dz, a.pitch, a.npad, a.pitch))
         return ZERO_ECUDA;
     if (!dw || !a.vec_w) md = mo;
-    else if (!map16(&md, dw, a.cols, a.vocab, lddw, 32)) return ZERO_ECUDA;
-    for (int64_t v = 0; v < h->vocab; v += a.pitch) {
+    else if (!map_out(&md, dw, a.cols, a.vocab, lddw)) return ZERO_ECUDA;
+    const int64_t step = copied ? copied_of(a.pitch, a.wide) : a.pitch;
+    for (int64_t v = 0; v < h->vocab; v += step) {
         a.v0 = (int)v;
-        a.count_v = (int)(h->vocab - v < a.pitch ? h->vocab - v : a.pitch);
+        a.count_v = (int)(h->vocab - v < step ? h->vocab - v : step);
         a.first = v == 0;
-        a.last = v + a.pitch >= h->vocab;
+        a.last = v + step >= h->vocab;
         if (copied && !copy_weights(a, pairs, stream)) return ZERO_ECUDA;
         if (!weights(a, 128, copied, &mw) || !weights(a, 64, copied, &mn) ||
-            !product(k.gradient[a.two], HEAD_GRADIENT, a, rows * up(a.count_v, ZERO_HD_TILE), pairs, {&mx, &mw, &mx, &mw, &mo}, stream) ||
-            !product(k.products, HEAD_PRODUCTS, a, pairs, pairs, {&mz, &mn, &mt, &ms, &md}, stream))
+            !product(k.gradient[a.two], a, rows * up(a.count_v, ZERO_HD_TILE), pairs, {&mx, &mw, &mx, &mw, &mo}, stream) ||
+            !product(k.products, a, pairs, pairs, {&mz, &mn, &mt, &ms, &md}, stream))
             return ZERO_ECUDA;
         // tiles are cut where 16 stages or more are added
         void* args[] = {&a};

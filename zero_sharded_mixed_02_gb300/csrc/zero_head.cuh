@@ -23,8 +23,10 @@ namespace zero {
 #define ZERO_HD_STEP 64                      // contracted elements of a stage
 #define ZERO_HD_STAGES 6
 #define ZERO_HD_SIDE 16384                   // bytes of a stage's operand in one SM
-#define ZERO_HD_ROWS 4096                    // bytes in which an output warp lays 32 rows of 64 columns
-#define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + 8 * ZERO_HD_ROWS + 1024)
+#define ZERO_HD_WRITERS 16                   // warps that read the accumulators
+#define ZERO_HD_THREADS (128 + 32 * ZERO_HD_WRITERS)    // warp 0 loads, 1 products, from 4 output
+#define ZERO_HD_ROWS 2048                    // bytes in which a writer lays 32 rows of 32 columns
+#define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + ZERO_HD_WRITERS * ZERO_HD_ROWS + 1024)
 #define ZERO_HD_PAIRS 80                     // most pairs that share a launch's work
 #define ZERO_HD_PART 8                       // least stages of a part of a cut tile
 #define ZERO_HD_RUN 12                       // stages an accumulator adds for the loss
@@ -38,11 +40,12 @@ namespace zero {
 
 enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT = 3, HEAD_PRODUCTS = 4 };
 
-// Warps that read the accumulators, each 32 rows of a column group of the tile.  Logits, whose runs are
-// added in registers, take 64 columns a warp (128 would spill: 6.4 against 4.96 ms without runs at 8192
-// x 128256 x 4096); the others 128.
-__host__ __device__ constexpr int head_writers(int pass) { return pass == HEAD_LOGITS ? 16 : 8; }
-__host__ __device__ constexpr int head_threads(int pass) { return 128 + 32 * head_writers(pass); }   // warp 0 loads, 1 products, from 4 output
+// How the writers share the work.  Logits, whose runs are added in registers: all read every tile,
+// 64 columns each (128 would spill: 6.4 against 4.4 ms at 8192 x 128256 x 4096).  The others: two groups of
+// eight take tiles in turn, one accumulator each, 128 columns a warp, so that one group's loads and
+// stores are under way while the other computes.
+__host__ __device__ constexpr int head_groups(int pass) { return pass == HEAD_LOGITS ? 1 : 2; }
+__host__ __device__ constexpr int head_columns(int pass) { return 4 * ZERO_HD_TILE * head_groups(pass) / ZERO_HD_WRITERS; }
 
 // What the passes over the rows leave for the rest, at the head of the workspace.
 struct HeadState {
@@ -50,6 +53,12 @@ struct HeadState {
     uint32_t ticket;
     int32_t rows;                            // counted rows
     int32_t top;                             // largest exponent of their gradients' scales
+};
+
+// A target of a row: its column and its weight, the teacher's share or the label's.
+struct __align__(8) HeadTarget {
+    int32_t column;
+    float weight;
 };
 
 // A counted row.  Gradients: dz = c1 2^(k1 z - l1) + c2 2^(k2 z - l2) - weight at the targets.
@@ -75,8 +84,8 @@ struct HeadArgs {
     int32_t *count, *most;                   // of a chunk of rows: how many; their largest exponent
     int32_t *map, *exponent;                 // counted row -> row, its scale's exponent
     HeadRow* info;                           // (forward: c1 is the loss's constant part, c2 the teacher's share)
-    int32_t* column;                         // targets of a counted row, ascending, and their weights
-    float *target, *found;                   // found: their logits
+    HeadTarget* target;                      // of a counted row, by columns
+    float* found;                            // their logits
     double* partial;
     float2* part;                            // [tiles of the vocabulary][npad]: maximum, sum
     float* part2;                            // the sum at the temperature
@@ -334,45 +343,66 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
     }
 }
 
-// The targets of a row, ascending and without repetitions: the teacher's entries and the label.
-// A warp's; `cols` and `vals` are its shared memory.  An entry leads if none before it has its
-// column, and takes the weights of all that have it; its place is the number of leaders of smaller columns.
-static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t at, int* cols, float* vals)
+// The targets of a row, the teacher's entries and the label, by columns (equal ones in their order; those that
+// are none come last).  A warp's; `cols` and `vals` are its shared memory, cols filled up with none to a multiple of 4.
+static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t at, const int* cols, const float* vals)
 {
-    const int lane = threadIdx.x & 31, n = a.slots;
-    uint32_t leads = 0;                                      // bit i: this lane's i-th entry
-    int leaders = 0;
-    for (int e = lane, i = 0; e < n; e += 32, i++) {
-        const int col = cols[e];
-        bool first = col != ZERO_HD_NONE;
-        for (int f = 0; f < e; f++) first = first && cols[f] != col;
-        leads |= (uint32_t)first << i;
-    }
-    __syncwarp();
-    for (int e = lane, i = 0; e < n; e += 32, i++) {
-        if (!(leads >> i & 1)) continue;
-        const int col = cols[e];
-        float w = 0.0f;
-        for (int f = e; f < n; f++)
-            if (cols[f] == col) w += vals[f];
-        vals[n + e] = w;
-    }
-    __syncwarp();
-    for (int e = lane, i = 0; e < n; e += 32, i++)
-        if (!(leads >> i & 1)) cols[e] = ZERO_HD_NONE;
-    __syncwarp();
-    for (int e = lane, i = 0; e < n; e += 32, i++) {
-        if (!(leads >> i & 1)) continue;
+    const int n = a.slots;
+    for (int e = threadIdx.x & 31; e < n; e += 32) {
         const int col = cols[e];
         int rank = 0;
-        for (int f = 0; f < n; f++) rank += cols[f] < col;
-        a.column[at + rank] = col;
-        a.target[at + rank] = vals[n + e];
+        for (int f = 0; f < n; f += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(cols + f);
+            rank += (q.x < col || (q.x == col && f < e)) + (q.y < col || (q.y == col && f + 1 < e)) +
+                    (q.z < col || (q.z == col && f + 2 < e)) + (q.w < col || (q.w == col && f + 3 < e));
+        }
+        a.target[at + rank] = {col, vals[e]};
     }
-    leaders = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)__popc(leads));
-    for (int e = leaders + lane; e < n; e += 32) {
-        a.column[at + e] = ZERO_HD_NONE;
-        a.target[at + e] = 0.0f;
+}
+
+// The `wide` columns of a row of `cols` as 16-byte vectors, zeros past its end, whatever the row's
+// alignment: put(o, v) gets vector o.  A warp's.  Rows that are not aligned are read in aligned vectors, each
+// lane's shifted together with the next lane's (of the vectors that reach over the row's ends only the
+// row's elements are read): 49 MB of 771 columns in 24 us element by element.
+template <class Put>
+static __device__ __forceinline__ void row_vectors(const uint16_t* from, int cols, int wide, Put put)
+{
+    const int lane = threadIdx.x & 31, s = (int)(reinterpret_cast<uintptr_t>(from) & 15) >> 1;
+    // elements [8 g - s, 8 g - s + 8) of the row: an aligned vector
+    auto load = [&](int g) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        const int e = 8 * g - s;
+        if (e >= 0 && e + 8 <= cols) return __ldg(reinterpret_cast<const uint4*>(from + e));
+        if (e < cols) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (e + i >= 0 && e + i < cols) w[i / 2] |= (uint32_t)__ldg(from + e + i) << 16 * (i & 1);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    if (s == 0) {
+#pragma unroll 4
+        for (int o = lane; o < wide / 8; o += 32) put(o, load(o));
+        return;
+    }
+#pragma unroll 4
+    for (int first = 0; first < wide / 8; first += 31) {
+        const uint4 q = load(first + lane);
+        uint32_t w[8] = {q.x, q.y, q.z, q.w, __shfl_down_sync(0xFFFFFFFFu, q.x, 1), __shfl_down_sync(0xFFFFFFFFu, q.y, 1),
+                         __shfl_down_sync(0xFFFFFFFFu, q.z, 1), __shfl_down_sync(0xFFFFFFFFu, q.w, 1)};
+        if (s & 4) {
+#pragma unroll
+            for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+        }
+        if (s & 2) {
+#pragma unroll
+            for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+        }
+        if (s & 1) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        if (lane < 31 && first + lane < wide / 8) put(first + lane, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
@@ -381,7 +411,7 @@ static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t at
 template <int DT>
 __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadArgs a)
 {
-    extern __shared__ int32_t entries_of[];                 // a warp's targets: columns, weights, added weights
+    extern __shared__ __align__(16) int32_t entries_of[];   // a warp's targets: columns, weights
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 8 + warp;
     let_next_begin();
@@ -426,7 +456,7 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         const int64_t end = all > 0 ? ((int64_t)all + 255) / 256 * 256 : 256;
         if (at >= end) return;
     }
-    // the row, eight columns a lane
+    // the row
     float up = 1.0f;
     int e = 0;
     float s = 0.0f, hard = 0.0f, soft = 0.0f;
@@ -437,62 +467,51 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         up = b - b == 0.0f ? power2(e - top) : 1.0f;
         if (!(b - b == 0.0f)) e = top;
     }
-    const uint16_t* from = a.x + row * a.ldx;
-    const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ldx % 8 == 0;
-#pragma unroll 4
-    for (int c = lane * 8; c < a.wide; c += 256) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (counted) {
-            if (vec && c + 8 <= a.cols) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4*>(from + c));
-                w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (c + i < a.cols) w[i / 2] |= (uint32_t)__ldg(from + c + i) << 16 * (i & 1);
-            }
-        }
-        *reinterpret_cast<uint4*>(a.xp + at * a.wide + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    row_vectors(a.x + (counted ? row : 0) * a.ldx, counted ? a.cols : 0, a.wide, [&](int o, uint4 q) {
+        reinterpret_cast<uint4*>(a.xp + at * a.wide)[o] = q;
         if (a.xs != a.xp) {
+            uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 float lo, hi;
                 widen2<DT>(w[i], lo, hi);
                 w[i] = narrow2<DT>(lo * up, hi * up);
             }
-            *reinterpret_cast<uint4*>(a.xs + at * a.wide + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(a.xs + at * a.wide)[o] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    }
+    });
     if (!counted) return;
     // its targets and coefficients
-    int* cols = entries_of + warp * 3 * a.slots;
-    float* vals = reinterpret_cast<float*>(cols + a.slots);
+    const int room = (a.slots + 3) & ~3;
+    int* cols = entries_of + warp * 2 * room;
+    float* vals = reinterpret_cast<float*>(cols + room);
     const float nan = __uint_as_float(0x7FC00000u);
     bool bad = false;
     float constant = 0.0f, share = 0.0f;
     const float fit = a.backward ? power2(ZERO_HD_SCALE - e) : 1.0f;
     if (a.index) {
-        float m = __uint_as_float(0xFF800000u), sum = 0.0f, cross = 0.0f;
-        for (int k = lane; k < a.top; k += 32)
-            if (has_entry(a, row, k)) {
-                const float t = teacher_logit(a, row, k);
-                m = fmaxf(m, t);
-                share = 1.0f;
-            }
+        const float low = __uint_as_float(0xFF800000u);
+        float m = low, sum = 0.0f, cross = 0.0f;
+        for (int k = lane; k < a.top; k += 32) {
+            const int col = __ldg(a.index + row * a.ldt + k);
+            float t = teacher_logit(a, row, k);
+            if (col < 0) t = low;                           // (a NaN there is not read)
+            cols[k] = t == low ? ZERO_HD_NONE : col;
+            vals[k] = t;
+            bad = bad || (t != low && col >= a.vocab);
+            m = fmaxf(m, t);
+            if (t != low) share = 1.0f;
+        }
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         share = __any_sync(0xFFFFFFFFu, share > 0.0f) ? 1.0f : 0.0f;
         for (int k = lane; k < a.top; k += 32) {
-            const int col = __ldg(a.index + row * a.ldt + k);
-            const bool has = has_entry(a, row, k);
-            float t = 0.0f, q = 0.0f;
-            if (has) {
-                t = (teacher_logit(a, row, k) - m) / a.temperature;
+            float q = 0.0f;
+            if (cols[k] != ZERO_HD_NONE) {
+                const float t = (vals[k] - m) / a.temperature;
                 q = expf(t);
                 sum += q;
                 cross += q > 0.0f ? q * t : q;              // (a NaN stays one)
-                bad = bad || col >= a.vocab;
             }
-            cols[k] = has ? col : ZERO_HD_NONE;
             vals[k] = q;
         }
         for (int o = 16; o > 0; o >>= 1) {
@@ -512,15 +531,9 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         vals[a.slots - 1] = (a.backward ? s * fit : 1.0f) * a.hard;
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane < room - a.slots) cols[a.slots + lane] = ZERO_HD_NONE;
     __syncwarp();
-    if (a.slots == 1) {
-        if (lane == 0) {
-            a.column[at] = cols[0];
-            a.target[at] = vals[0];
-        }
-    } else {
-        put_targets(a, at * a.slots, cols, vals);
-    }
+    put_targets(a, at * a.slots, cols, vals);
     if (lane == 0) {
         a.map[at] = (int32_t)row;
         HeadRow h;
@@ -550,20 +563,11 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
 // Rows of the weights that are not aligned to 16 bytes, a piece of them, to rows that are.
 static __global__ void __launch_bounds__(256) k_head_weights(const __grid_constant__ HeadArgs a)
 {
-    const int lane = threadIdx.x & 31;
     let_next_begin();
     after_previous();
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < a.count_v; r += (int64_t)gridDim.x * 8) {
-        const uint16_t* from = a.w + (a.v0 + r) * a.ldw;
-        uint16_t* to = a.wp + r * a.wide;
-#pragma unroll 8
-        for (int c = 2 * lane; c < a.wide; c += 64) {
-            uint32_t w = 0;
-            if (c < a.cols) w = __ldg(from + c);
-            if (c + 1 < a.cols) w |= (uint32_t)__ldg(from + c + 1) << 16;
-            *reinterpret_cast<uint32_t*>(to + c) = w;
-        }
-    }
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < a.count_v; r += (int64_t)gridDim.x * 8)
+        row_vectors(a.w + (a.v0 + r) * a.ldw, a.cols, a.wide,
+                    [&](int o, uint4 q) { reinterpret_cast<uint4*>(a.wp + r * a.wide)[o] = q; });
 }
 
 // ---- the pair's machinery ------------------------------------------------------------
@@ -687,15 +691,17 @@ static __device__ __forceinline__ void put_row(const HeadArgs& a, bool input, ui
         }
 }
 
-// 32 columns of a lane's row into the warp's 32 rows of 128 bytes, with the swizzle that TMA takes them
-// with (16-byte word q of row r at q ^ (r & 7)): its first or second half.
+// Where 16-byte word q of a lane's row lies in the warp's 32 rows of 64 bytes: at q ^ (row >> 1 & 3), TMA's
+// 64-byte swizzle, in which lanes that each take a row meet all banks.
+static __device__ __forceinline__ uint32_t word_of(uint32_t stage, int row, int q) { return stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4); }
+// 32 columns of a lane's row in 16 bits.
 template <int DT>
-static __device__ __forceinline__ void lay_half(uint32_t stage, int half, const float (&v)[32])
+static __device__ __forceinline__ void lay_row(uint32_t stage, const float (&v)[32])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int q = 0; q < 4; q++)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4)),
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(word_of(stage, lane, q)),
                      "r"(narrow2<DT>(v[8 * q], v[8 * q + 1])), "r"(narrow2<DT>(v[8 * q + 2], v[8 * q + 3])),
                      "r"(narrow2<DT>(v[8 * q + 4], v[8 * q + 5])), "r"(narrow2<DT>(v[8 * q + 6], v[8 * q + 7])) : "memory");
 }
@@ -714,76 +720,95 @@ static __device__ __forceinline__ void rows_sent()
     __syncwarp();
 }
 
-// put_row() for rows that are not aligned to vectors: 32 columns of the warp's rows through 2 KB of
-// shared memory, so that an access of the warp is a run of a row and not an element of each of 32
-// rows.  16-byte word q of row r lies at q ^ (r >> 1 & 3), so that lanes that each take a row meet all banks too.
+// put_row() for rows that are not aligned to vectors: 32 columns of the warp's rows through shared
+// memory, so that an access of the warp is a run of a row and not an element of each of 32 rows.
 template <int DT>
-static __device__ __forceinline__ void put_rows(const HeadArgs& a, bool input, uint16_t* to, float factor, int j, float (&v)[32], uint32_t stage)
+static __device__ __forceinline__ void put_rows(const HeadArgs& a, bool input, uint16_t* to, float factor, int j, float (&v)[32],
+                                                uint32_t stage)
 {
     const int lane = threadIdx.x & 31;
     if (j >= a.cols) return;                                 // all lanes
-    const bool add = !input && a.accumulate;
-    const uint32_t own = stage + lane * 64;
     const uint64_t mine = reinterpret_cast<uint64_t>(to);
-    if (add) {
+#pragma unroll
+    for (int e = 0; e < 32; e++) v[e] *= factor;
+    if (!input && a.accumulate) {
 #pragma unroll 8
         for (int r = 0; r < 32; r++) {
             const uint16_t* g = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, mine, r));
             const uint16_t x = g && j + lane < a.cols ? g[j + lane] : 0;
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + r * 64 + ((lane >> 3) ^ (r >> 1 & 3)) * 16 + (lane & 7) * 2),
-                         "h"(x) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(word_of(stage, r, lane >> 3) + (lane & 7) * 2), "h"(x) : "memory");
         }
         __syncwarp();
-    }
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-        const uint32_t word = own + (q ^ (lane >> 1 & 3)) * 16;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (add)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(word));
+        for (int q = 0; q < 4; q++) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(word_of(stage, lane, q)));
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            float lo = 0.0f, hi = 0.0f;
-            if (add) widen2<DT>(w[e], lo, hi);
-            w[e] = narrow2<DT>(v[8 * q + 2 * e] * factor + lo, v[8 * q + 2 * e + 1] * factor + hi);
+            for (int e = 0; e < 4; e++) {
+                float lo, hi;
+                widen2<DT>(w[e], lo, hi);
+                v[8 * q + 2 * e] += lo;
+                v[8 * q + 2 * e + 1] += hi;
+            }
         }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(word), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
     }
+    lay_row<DT>(stage, v);
     __syncwarp();
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < 32; r++) {
         uint16_t* g = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, mine, r));
-        if (g && j + lane < a.cols) {
-            uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x)
-                         : "r"(stage + r * 64 + ((lane >> 3) ^ (r >> 1 & 3)) * 16 + (lane & 7) * 2));
-            g[j + lane] = x;
-        }
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(word_of(stage, r, lane >> 3) + (lane & 7) * 2));
+        if (g && j + lane < a.cols) g[j + lane] = x;
     }
     __syncwarp();
 }
 
-// Where a counted row's targets from column c on begin.
-static __device__ __forceinline__ int first_target(const HeadArgs& a, const int32_t* columns, int c)
-{
-    int lo = 0, hi = a.slots;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(columns + mid) < c) lo = mid + 1;
-        else hi = mid;
+// A lane's next target of its row from column `from` on; AHEAD: the one after it is loaded ahead.
+template <bool AHEAD>
+struct HeadGoal {
+    const HeadTarget* at;
+    int next, from;
+    HeadTarget now, then;                                   // columns counted from `from`
+    __device__ __forceinline__ HeadTarget load(const HeadArgs& a, int e) const
+    {
+        if (e >= a.slots) return {ZERO_HD_NONE, 0.0f};
+        const int2 q = __ldg(reinterpret_cast<const int2*>(at) + e);
+        return {q.x == ZERO_HD_NONE ? q.x : q.x - from, __int_as_float(q.y)};
     }
-    return lo;
-}
+    __device__ __forceinline__ void begin(const HeadArgs& a, int64_t row, int c)
+    {
+        at = a.target + row * a.slots;
+        from = c;
+        int hi = a.slots;
+        next = 0;
+        while (next < hi) {                                  // the first whose column is not below
+            const int mid = (next + hi) >> 1;
+            if (__ldg(&at[mid].column) < c) next = mid + 1;
+            else hi = mid;
+        }
+        now = load(a, next);
+        if (AHEAD) then = load(a, next + 1);
+    }
+    __device__ __forceinline__ void none() { now = {ZERO_HD_NONE, 0.0f}; }
+    __device__ __forceinline__ void step(const HeadArgs& a)
+    {
+        next++;
+        now = AHEAD ? then : load(a, next);
+        if (AHEAD) then = load(a, next + 1);
+    }
+};
 
 // ---- the products --------------------------------------------------------------------
 // map_a, map_b: the operands of the logits or of dx; map_c, map_d: of dw; map_o: where the pass's
 // output goes by TMA (dz; dw where its rows are aligned).
 template <int DT, int PASS, bool TWO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
     k_head(const __grid_constant__ HeadArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
            const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_o)
 {
-    constexpr int WRITERS = head_writers(PASS), WIDE = 4 * ZERO_HD_TILE / WRITERS;      // columns of a writer
+    constexpr int GROUPS = head_groups(PASS), WIDE = head_columns(PASS);                // columns of a writer
     extern __shared__ unsigned char raw[];
     __shared__ HeadShared sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -798,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(smem_u32(&sh.sum_full[s]), 1);
-            mbar_init(smem_u32(&sh.sum_empty[s]), 2 * WRITERS);
+            mbar_init(smem_u32(&sh.sum_empty[s]), 2 * ZERO_HD_WRITERS / GROUPS);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.dead = 0;
@@ -929,7 +954,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
         }
     } else if (warp >= 4) {
         // ---- output: warp w reads rows 32 (w mod 4) + lane of this SM's half, WIDE columns ----
-        const int quad = warp & 3, side = (warp - 4) >> 2;
+        const int quad = warp & 3, side = ((warp - 4) >> 2) % (4 / GROUPS), group = (warp - 4) / (ZERO_HD_WRITERS / GROUPS);
         const float nan = __uint_as_float(0x7FC00000u), low = __uint_as_float(0xFF800000u);
         [[maybe_unused]] const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
         [[maybe_unused]] const int top = a.st->top;
@@ -938,7 +963,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
         // maxima and sums of a tile's column groups but the first: [group][which][lane] of this quad
         [[maybe_unused]] const auto merge = reinterpret_cast<float(*)[3][32]>(
             raw + (base - smem_u32(raw)) + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + quad * (9 * 32 * 4));
-        for (int i = 0; head_next<PASS>(a, shape, shape_w, inputs, pair, i, g); i++) {
+        for (int i = group; head_next<PASS>(a, shape, shape_w, inputs, pair, i, g); i += GROUPS) {
             const int acc = i & 1;
             uint32_t ti, tj;
             const bool dw = place(ti, tj);
@@ -948,18 +973,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
             // what does not depend on the sums, while they are made
             [[maybe_unused]] const int c0 = (int)tj * ZERO_HD_TILE + side * WIDE;     // first column, of the piece
             [[maybe_unused]] const int end = a.count_v - c0;                          // columns there are from it
-            [[maybe_unused]] int next = 0;
-            [[maybe_unused]] int goal = ZERO_HD_NONE;                                 // the next target's column, from c0
-            [[maybe_unused]] const int32_t* columns = nullptr;
+            [[maybe_unused]] HeadGoal<PASS == HEAD_GRADIENT> goal;
             [[maybe_unused]] HeadRow row{};
             [[maybe_unused]] uint16_t* to = nullptr;
             [[maybe_unused]] float factor = 0.0f;
             if (PASS <= HEAD_GRADIENT) {
+                goal.none();
                 if (live && g.last) {
-                    columns = a.column + r * a.slots;
-                    next = a.slots == 1 ? (__ldg(columns) < a.v0 + c0) : first_target(a, columns, a.v0 + c0);
-                    if (next < a.slots) goal = __ldg(columns + next) - a.v0 - c0;
                     if (PASS == HEAD_GRADIENT) row = a.info[r];
+                    goal.begin(a, r, a.v0 + c0);
                 }
             } else if (g.slot < 0 && (dw || a.last)) {
                 to = out_row(a, !dw, r, counted, top, common, factor);
@@ -969,7 +991,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
             if constexpr (PASS == HEAD_LOGITS) {
                 // z: the tile's sums, runs of it added in fp32.  Logits of targets in these columns: a
                 // lane's accumulators are read at a column of the warp's choice, where the added ones are put back
-                const bool sought = g.last && __any_sync(0xFFFFFFFFu, goal < WIDE);
+                const bool sought = g.last && __any_sync(0xFFFFFFFFu, goal.now.column < WIDE);
 #pragma unroll
                 for (int c = 0; c < WIDE; c += 16) {
                     float v[16];
@@ -984,13 +1006,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
                 }
                 if (sought) {
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal)) < WIDE;) {
+                    for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal.now.column)) < WIDE;) {
                         const float v = read_one(from + c);
-                        if (goal == c) {
-                            a.found[r * a.slots + next] = have ? v : nan;
-                            next++;
-                            goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
-                        }
+                        for (; goal.now.column == c; goal.step(a)) a.found[r * a.slots + goal.next] = have ? v : nan;
                         __syncwarp();
                     }
                 }
@@ -1048,42 +1066,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
             } else if constexpr (PASS == HEAD_GRADIENT) {
-                for (int c = 0; c < WIDE; c += 64) {
+                for (int c = 0; c < WIDE; c += 32) {
+                    float v[32];
+                    __syncwarp();
+                    read_accumulator(from + c, v);
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float v[32];
-                        __syncwarp();
-                        read_accumulator(from + c + 32 * h, v);
-#pragma unroll
-                        for (int e = 0; e < 32; e++) {
-                            float d = row.c1 * exp2_fast(__fmaf_rn(v[e], a.k1, -row.l1));
-                            if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v[e], a.k2, -row.l2)), d);
-                            v[e] = d;
-                        }
-                        if (!live || c + 32 * h + 32 > end) {
-#pragma unroll
-                            for (int e = 0; e < 32; e++)
-                                if (!live || c + 32 * h + e >= end) v[e] = 0.0f;
-                        }
-                        if (!have) {
-#pragma unroll
-                            for (int e = 0; e < 32; e++) v[e] = nan;
-                        }
-                        if (h == 0) rows_sent();
-                        lay_half<DT>(stage, h, v);
+                    for (int e = 0; e < 32; e++) {
+                        float d = row.c1 * exp2_fast(__fmaf_rn(v[e], a.k1, -row.l1));
+                        if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v[e], a.k2, -row.l2)), d);
+                        v[e] = d;
                     }
+                    if (!live || c + 32 > end) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (!live || c + e >= end) v[e] = 0.0f;
+                    }
+                    if (!have) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) v[e] = nan;
+                    }
+                    rows_sent();
+                    lay_row<DT>(stage, v);
                     // once more where the targets are
-                    for (int t; (t = __reduce_min_sync(0xFFFFFFFFu, goal)) < c + 64;) {
+                    for (int t; (t = __reduce_min_sync(0xFFFFFFFFu, goal.now.column)) < c + 32;) {
                         const float v = read_one(from + t);
-                        if (goal == t) {
-                            float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1));
+                        if (goal.now.column == t) {
+                            float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1)), w = 0.0f;
                             if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v, a.k2, -row.l2)), d);
-                            d = have ? d - __ldg(a.target + r * a.slots + next) : nan;
+                            for (; goal.now.column == t; goal.step(a)) w += goal.now.weight;
+                            d = have ? d - w : nan;
                             const int in = t - c;
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + lane * 128 + (((in >> 3) ^ (lane & 7)) << 4) + (in & 7) * 2),
-                                         "h"(narrow1<DT>(d)) : "memory");
-                            next++;
-                            goal = next < a.slots ? __ldg(columns + next) - a.v0 - c0 : ZERO_HD_NONE;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(word_of(stage, lane, in >> 3) + (in & 7) * 2), "h"(narrow1<DT>(d))
+                                         : "memory");
                         }
                         __syncwarp();
                     }
@@ -1125,9 +1139,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
                     } else if (sent) {
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] *= factor;
-                        if (!(c & 32)) rows_sent();
-                        lay_half<DT>(stage, c >> 5 & 1, v);
-                        if (c & 32) send_rows(stage, &map_o, j + c - 32, a.v0 + (int)(r - lane));
+                        rows_sent();
+                        lay_row<DT>(stage, v);
+                        send_rows(stage, &map_o, j + c, a.v0 + (int)(r - lane));
                     } else if (dw ? a.vec_w : a.vec_x) {
                         put_row<DT, 32>(a, !dw, to, factor, j + c, v);
                     } else {
@@ -1151,7 +1165,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(head_threads(PASS), 
 // Adds the parts of cut tiles of one pass in the contracted axis's order: a warp takes 32 rows and 16
 // columns of a tile.
 template <int DT, int PASS>
-static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& shape, uint32_t unit, int counted, int top, float common)
+static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& shape, uint32_t unit, int counted, int top, float common,
+                                            float (*turn)[17])
 {
     constexpr bool INPUT = PASS == HEAD_INPUT;
     const int lane = threadIdx.x & 31;
@@ -1201,11 +1216,29 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
     }
     float factor = 0.0f;
     uint16_t* to = out_row(a, INPUT, r, counted, top, common, factor);
-    put_row<DT, 16>(a, INPUT, to, factor, j, v);
+    if (INPUT ? a.vec_x : a.vec_w) {
+        put_row<DT, 16>(a, INPUT, to, factor, j, v);
+        return;
+    }
+    // two rows' runs of 16 columns an access
+#pragma unroll
+    for (int e = 0; e < 16; e++) turn[lane][e] = v[e] * factor;
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; e++) {
+        const int row = 2 * e + (lane >> 4), col = lane & 15;
+        uint16_t* g = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(to), row));
+        if (!g || j + col >= a.cols) continue;
+        float x = turn[row][col];
+        if (!INPUT && a.accumulate) x += widen1<DT>(g[j + col]);
+        g[j + col] = narrow1<DT>(x);
+    }
+    __syncwarp();
 }
 template <int DT>
 __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadArgs a)
 {
+    __shared__ float turn[8][32][17];
     let_next_begin();
     after_previous();
     const int counted = a.st->rows, top = a.st->top;
@@ -1213,18 +1246,19 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
     const uint32_t of_x = a.dx && x.rest_pairs > x.rest ? x.rest * 128 : 0, of_w = a.dw && w.rest_pairs > w.rest ? w.rest * 128 : 0;
     for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < of_x + of_w; unit += gridDim.x * 8) {
-        if (unit < of_x) join<DT, HEAD_INPUT>(a, x, unit, counted, top, common);
-        else join<DT, HEAD_WEIGHT>(a, w, unit - of_x, counted, top, common);
+        if (unit < of_x) join<DT, HEAD_INPUT>(a, x, unit, counted, top, common, turn[threadIdx.x >> 5]);
+        else join<DT, HEAD_WEIGHT>(a, w, unit - of_x, counted, top, common, turn[threadIdx.x >> 5]);
     }
 }
 
 // ---- the loss ------------------------------------------------------------------------
-// 32 counted rows a block, a lane a row; the 32 warps share the tiles' maxima and sums.  The
-// last block to finish adds the blocks' sums in order.
+// 32 counted rows a block: first a lane a row, the 32 warps sharing the tiles' maxima and sums, then a
+// warp a row.  The last block to finish adds the blocks' sums in order.
 static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
 {
-    __shared__ float ms[32][32], ss[32][32], ts[32][32], dots[32];
-    __shared__ int last;
+    __shared__ float ms[32][33], ss[32][33], ts[32][33];
+    __shared__ double losses[32];
+    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     let_next_begin();
     after_previous();
@@ -1233,17 +1267,28 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
     const float low = __uint_as_float(0xFF800000u), nan = __uint_as_float(0x7FC00000u);
     float m = low, s = 0.0f, t = 0.0f;
     if (r < counted) {
-#pragma unroll 4
-        for (int v = warp; v < tiles; v += 32) {
-            const float2 p = a.part[(int64_t)v * a.npad + r];
-            const float most = fmaxf(m, p.x);
-            if (most == low) {                              // (a NaN sum of a lowest maximum is kept)
-                s += p.y;
-                continue;
+        const float2* part = a.part + r;
+        const float* part2 = a.part2 + r;
+        for (int v = warp; v < tiles; v += 128) {           // four tiles at a time
+            float2 p[4];
+            float p2[4];
+            float most = m;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const bool in = v + 32 * e < tiles;
+                p[e] = in ? part[(v + 32 * e) * a.npad] : make_float2(low, 0.0f);
+                p2[e] = in && a.two ? part2[(v + 32 * e) * a.npad] : 0.0f;
             }
-            const float f = exp2_fast((m - most) * a.k1), h = exp2_fast((p.x - most) * a.k1);
-            s = s * f + p.y * h;
-            if (a.two) t = t * exp2_fast((m - most) * a.k2) + a.part2[(int64_t)v * a.npad + r] * exp2_fast((p.x - most) * a.k2);
+#pragma unroll
+            for (int e = 0; e < 4; e++) most = fmaxf(most, p[e].x);
+            const float base = most == low ? 0.0f : most;   // (a NaN sum of a lowest maximum is kept)
+            s *= exp2_fast((m - base) * a.k1);
+            if (a.two) t *= exp2_fast((m - base) * a.k2);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                s += p[e].y * exp2_fast((p[e].x - base) * a.k1);
+                if (a.two) t += p2[e] * exp2_fast((p[e].x - base) * a.k2);
+            }
             m = most;
         }
     }
@@ -1254,31 +1299,37 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
     const int64_t w = (int64_t)blockIdx.x * 32 + warp;
     float dot = 0.0f;
     if (w < counted)
-        for (int e = lane; e < a.slots; e += 32)
-            if (a.column[w * a.slots + e] < a.vocab) dot += a.target[w * a.slots + e] * a.found[w * a.slots + e];
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    if (lane == 0) dots[warp] = dot;
+        for (int e = lane; e < a.slots; e += 32) {
+            const HeadTarget g = a.target[w * a.slots + e];
+            if (g.column < a.vocab) dot += g.weight * a.found[w * a.slots + e];
+        }
     __syncthreads();
-    if (warp == 0) {
+    float most = m = ms[lane][warp];
+    s = ss[lane][warp];
+    t = ts[lane][warp];
+    for (int o = 16; o > 0; o >>= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    }
+    const float base = most == low ? 0.0f : most;
+    s *= exp2_fast((m - base) * a.k1);
+    t *= exp2_fast((m - base) * a.k2);
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    }
+    if (lane == 0) {
         double loss = 0.0;
-        if (r < counted) {
-            m = low;
-            for (int v = 0; v < 32; v++) m = fmaxf(m, ms[v][lane]);
-            s = t = 0.0f;
-            for (int v = 0; v < 32; v++) {
-                if (v >= tiles) break;
-                s += ss[v][lane] * exp2_fast((ms[v][lane] - m) * a.k1);
-                if (a.two) t += ts[v][lane] * exp2_fast((ms[v][lane] - m) * a.k2);
-            }
+        if (w < counted) {
             // k1 is 1/T only where there is no other log-sum-exp
-            const HeadRow h = a.info[r];
+            const HeadRow h = a.info[w];
             const float scale1 = a.labels ? 1.0f : 1.0f / a.temperature;
-            float l1 = m * scale1 + logf(s), l2 = a.two ? m / a.temperature + logf(t) : l1;
+            float l1 = base * scale1 + logf(s), l2 = a.two ? base / a.temperature + logf(t) : l1;
             if (h.c1 != h.c1) l1 = l2 = nan;
-            float x = h.c1 - dots[lane];
+            float x = h.c1 - dot;
             if (a.index) x = __fmaf_rn(h.c2 * a.soft * a.temperature * a.temperature, l2, x);
             if (a.labels) x = __fmaf_rn(a.hard, __fmaf_rn(a.z_loss * l1, l1, l1), x);
-            const int64_t row = a.map[r];
+            const int64_t row = a.map[w];
             a.loss[row] = x;
             if (a.index) {
                 a.lse[2 * row] = l2;
@@ -1288,23 +1339,28 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
             }
             loss = x;
         }
-        for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+        losses[warp] = loss;
+    }
+    __syncthreads();
+    if (warp > 0 || !a.sums) return;
+    double loss = losses[lane];
+    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+    if (gridDim.x > 1) {
         if (lane == 0) {
             __stcg(a.partial + blockIdx.x, loss);
             __threadfence();
             last = atomicAdd(&a.st->ticket, 1u) == gridDim.x - 1;
         }
         __syncwarp();
-        if (a.sums && last) {
-            __threadfence();
-            double all = 0.0;
-            for (unsigned b = lane; b < gridDim.x; b += 32) all += __ldcg(a.partial + b);
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            if (lane == 0) {
-                a.sums[0] = (float)all;
-                a.sums[1] = (float)counted;
-            }
-        }
+        if (!last) return;
+        __threadfence();
+        loss = 0.0;
+        for (unsigned b = lane; b < gridDim.x; b += 32) loss += __ldcg(a.partial + b);
+        for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+    }
+    if (lane == 0) {
+        a.sums[0] = (float)loss;
+        a.sums[1] = (float)counted;
     }
 }
 

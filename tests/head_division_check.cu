@@ -19,7 +19,10 @@ static int check(int counted, int cols, int columns, int pairs, int band)
     a.dx = &some;
     const HeadShape s = head_shape<PASS>(a, counted);
     const uint32_t tiles = s.tm * s.tn, places = head_band<PASS>(a);
-    std::vector<uint8_t> seen((size_t)tiles * s.steps, 0), place(tiles, 0), slots(2 * ZERO_HD_PAIRS, 0);
+    // places that the workspace has: of the largest call of these sizes
+    int64_t most = (int64_t)(tiles < ZERO_HD_PAIRS ? tiles : ZERO_HD_PAIRS) * (s.steps / ZERO_HD_PART);
+    if (most > ZERO_HD_ROUNDS * ZERO_HD_PAIRS) most = ZERO_HD_ROUNDS * ZERO_HD_PAIRS;
+    std::vector<uint8_t> seen((size_t)tiles * s.steps, 0), place(tiles, 0), slots(ZERO_HD_ROUNDS * ZERO_HD_PAIRS, 0);
     if (pairs > ZERO_HD_PAIRS || s.runs * s.run < s.steps || (PASS == HEAD_LOGITS && s.run > ZERO_HD_RUN)) return 1;
     for (uint32_t t = 0; t < tiles; t++) {
         uint32_t i, j;
@@ -39,13 +42,11 @@ static int check(int counted, int cols, int columns, int pairs, int band)
             const bool whole = g.first && g.last && g.s0 == 0 && g.s1 == (int)s.steps;
             if (PASS >= HEAD_INPUT && (g.slot < 0) != whole) return 6;
             if (PASS < HEAD_INPUT && g.slot >= 0) return 6;
-            if (g.slot >= 0 && (g.slot >= 2 * ZERO_HD_PAIRS || slots[g.slot]++)) return 7;
-            if (PASS >= HEAD_INPUT && g.tile >= s.waves * a.pairs) {
+            if (g.slot >= 0 && (g.slot >= most || slots[g.slot]++)) return 7;
+            if (g.slot >= 0) {                       // the join adds parts q, q + rest, ... of tile q in the axis's order
                 const uint32_t q = g.tile - s.waves * a.pairs;
-                const uint32_t p0 = head_owner(s, q * s.steps), p1 = head_owner(s, (q + 1) * s.steps - 1);
-                if ((uint32_t)p < p0 || (uint32_t)p > p1 || (p0 == p1) != whole) return 8;
-                const uint32_t second = head_share(s, p0) / s.steps < q;
-                if (!whole && g.slot != (int)(2 * p + ((uint32_t)p == p0 ? second : 0))) return 9;
+                if (g.tile < s.waves * a.pairs || g.slot % (int)s.rest != (int)q || g.slot / s.rest >= s.ranges) return 8;
+                if (g.s0 != (int)(g.slot / s.rest * s.steps / s.ranges)) return 9;
             }
         }
         if (within) return 10;
@@ -53,8 +54,8 @@ static int check(int counted, int cols, int columns, int pairs, int band)
     }
     for (uint8_t n : seen)
         if (n != 1) return 11;
-    // parts are cut only where the host launches the join: from 16 stages
-    if (PASS >= HEAD_INPUT && s.rest_pairs > s.rest && s.steps < 16) return 12;
+    // parts are cut only where the host launches the join
+    if (PASS >= HEAD_INPUT && s.ranges > 1 && s.steps < 2 * ZERO_HD_PART) return 12;
     return 0;
 }
 

@@ -73,7 +73,14 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     take(a.xs, a.npad * a.wide);              // backward
     take(a.dz, a.npad * a.pitch);
     take(a.acc, a.npad / ZERO_HD_TILE * up(h->cols, ZERO_HD_TILE) * ZERO_HD_SLOT);
-    take(a.parts, 4ll * ZERO_HD_PAIRS * ZERO_HD_SLOT);
+    // as many parts as the largest call has
+    auto parts = [&](int64_t tiles_, int64_t steps) {
+        const int64_t most = (tiles_ < ZERO_HD_PAIRS ? tiles_ : ZERO_HD_PAIRS) * (steps / ZERO_HD_PART);
+        return most < ZERO_HD_ROUNDS * ZERO_HD_PAIRS ? most : ZERO_HD_ROUNDS * ZERO_HD_PAIRS;
+    };
+    const int64_t wide = up(h->cols, ZERO_HD_TILE);
+    a.slots_x = (int)parts(a.npad / ZERO_HD_TILE * wide, up(a.pitch, ZERO_HD_STEP));
+    take(a.parts, (a.slots_x + parts(up(a.pitch, ZERO_HD_TILE) * wide, up(a.npad, ZERO_HD_STEP))) * ZERO_HD_SLOT);
     return (uint64_t)((at > forward ? at : forward) - begin);
 }
 
@@ -169,8 +176,11 @@ bool launch_next(const void* fn, dim3 grid, int threads, int smem, void** args, 
 bool run_rows(const HeadArgs& a, const HeadKernels& k, void* stream)
 {
     void* args[] = {const_cast<HeadArgs*>(&a)};
+    const dim3 grid((unsigned)up(a.rows + ZERO_HD_TILE, 8));
+    const int smem = 8 * 2 * ((a.slots + 3) & ~3) * 4;
+    if (a.rows <= ZERO_HD_CHUNK) return launch(k.pack, grid, 256, smem, args, stream);
     return launch((const void*)k_head_rows, dim3((unsigned)up(a.rows, ZERO_HD_CHUNK)), ZERO_HD_CHUNK, 0, args, stream) &&
-           launch_next(k.pack, dim3((unsigned)up(a.rows + ZERO_HD_TILE, 8)), 256, 8 * 2 * ((a.slots + 3) & ~3) * 4, args, stream);
+           launch_next(k.pack, grid, 256, smem, args, stream);
 }
 
 // Rows that leave from a writer's 32 rows of 32 columns.
@@ -287,9 +297,10 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
             !product(k.gradient[a.two], a, rows * up(a.count_v, ZERO_HD_TILE), pairs, {&mx, &mw, &mx, &mw, &mo}, stream) ||
             !product(k.products, a, pairs, pairs, {&mz, &mn, &mt, &ms, &md}, stream))
             return ZERO_ECUDA;
-        // tiles are cut where 16 stages or more are added
+        // tiles are cut from twice a part's stages on
         void* args[] = {&a};
-        if (((dx && a.count_v > 15 * ZERO_HD_STEP) || (dw && a.rows > 15 * ZERO_HD_STEP)) &&
+        const int64_t least = (2 * ZERO_HD_PART - 1) * ZERO_HD_STEP;
+        if (((dx && a.count_v > least) || (dw && a.rows > least)) &&
             !launch_next(k.join, dim3(4 * pairs), 256, 0, args, stream))
             return ZERO_ECUDA;
     }

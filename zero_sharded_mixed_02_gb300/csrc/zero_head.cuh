@@ -28,7 +28,8 @@ namespace zero {
 #define ZERO_HD_ROWS 2048                    // bytes in which a writer lays 32 rows of 32 columns
 #define ZERO_HD_SMEM (ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + ZERO_HD_WRITERS * ZERO_HD_ROWS + 1024)
 #define ZERO_HD_PAIRS 80                     // most pairs that share a launch's work
-#define ZERO_HD_PART 8                       // least stages of a part of a cut tile
+#define ZERO_HD_PART 16                      // least stages of a part of a cut tile,
+#define ZERO_HD_ROUNDS 4                     // and most parts of a pair
 #define ZERO_HD_RUN 12                       // stages an accumulator adds for the loss
 #define ZERO_HD_CHUNK 1024                   // rows whose counted ones are numbered by one block
 #define ZERO_HD_SLOT (ZERO_HD_TILE * ZERO_HD_TILE)      // floats of a tile's sums
@@ -96,12 +97,14 @@ struct HeadArgs {
     // this launch
     int pairs, v0, count_v, wy;              // first column of the piece, columns, its first row in the weights' map
     int first, last;                         // piece
+    int slots_x;                             // places of dx's parts
     int band;                                // row tiles that are taken together
 };
 
 // ---- the division of the work ------------------------------------------------------
 struct HeadShape {
-    uint32_t tm, tn, steps, runs, run, waves, rest, rest_pairs, share, extra;
+    uint32_t tm, tn, steps, runs, run, waves, rest;
+    uint32_t ranges;                         // parts that the rest's tiles are cut into
 };
 struct HeadSegment {
     uint32_t tile;
@@ -114,13 +117,15 @@ struct HeadSegment {
 static __host__ __device__ __forceinline__ uint32_t head_up(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
 // Tiles along the left operand's rows (tm) and the right one's (tn), and how `pairs` pairs share
-// them: whole waves, then the rest, whose tiles are cut along the contracted axis into equal parts
-// where that is long enough to pay for joining them (INPUT, WEIGHT).
+// them: whole waves, then the rest, whose tiles are cut along the contracted axis (INPUT, WEIGHT)
+// where that is long enough to pay for joining the parts.  All are cut at the same places, and the parts of a
+// range of the axis run at about the same time, so that they share their panels in L2: cut into equal shares of all
+// pairs instead, tiles of 2048 rows of 4096 x 64256 took 1260 us with their dw.
 template <int PASS>
 static __host__ __device__ __forceinline__ HeadShape head_shape(const HeadArgs& a, int counted)
 {
     HeadShape s;
-    const uint32_t n = counted > 0 ? counted : 1;
+    const uint32_t n = counted > 0 ? counted : 1, pairs = a.pairs;
     const uint32_t rows = head_up(n, ZERO_HD_TILE), words = head_up(a.count_v, ZERO_HD_TILE), wide = head_up(a.cols, ZERO_HD_TILE);
     s.tm = PASS == HEAD_WEIGHT ? words : rows;
     s.tn = PASS <= HEAD_GRADIENT ? words : wide;
@@ -129,31 +134,23 @@ static __host__ __device__ __forceinline__ HeadShape head_shape(const HeadArgs& 
     s.run = head_up(s.steps, s.runs);
     s.runs = head_up(s.steps, s.run);
     const uint32_t tiles = s.tm * s.tn;
-    s.waves = tiles / a.pairs;
-    s.rest = tiles % a.pairs;
-    s.rest_pairs = s.rest;
-    s.share = s.extra = 0;
-    if (s.rest > 0) {
-        const uint32_t units = s.rest * s.steps;
-        if (PASS >= HEAD_INPUT && s.steps >= 2 * ZERO_HD_PART) {
-            const uint32_t parts = units / ZERO_HD_PART;
-            s.rest_pairs = parts < s.rest ? s.rest : parts < (uint32_t)a.pairs ? parts : a.pairs;
+    s.waves = tiles / pairs;
+    s.rest = tiles % pairs;
+    s.ranges = 1;
+    if (PASS >= HEAD_INPUT && s.rest > 0) {
+        // as many parts as fill one to four rounds of all pairs: the least time, in stages, of the rounds,
+        // each with its output, and the join (about 20)
+        uint32_t best = s.steps + 8;
+        for (uint32_t k = 1; k <= ZERO_HD_ROUNDS; k++) {
+            const uint32_t fill = k * pairs / s.rest, most = s.steps / ZERO_HD_PART, r = fill < most ? fill : most;
+            const uint32_t time = k * (head_up(s.steps, r > 0 ? r : 1) + 8) + 20 + r;
+            if (r > 1 && time < best) {
+                best = time;
+                s.ranges = r;
+            }
         }
-        s.share = units / s.rest_pairs;
-        s.extra = units % s.rest_pairs;
     }
     return s;
-}
-
-// First unit (stage of a tile of the last wave) of a pair's share, and the pair that has a unit.
-static __host__ __device__ __forceinline__ uint32_t head_share(const HeadShape& s, uint32_t pair)
-{
-    return pair * s.share + (pair < s.extra ? pair : s.extra);
-}
-static __host__ __device__ __forceinline__ uint32_t head_owner(const HeadShape& s, uint32_t unit)
-{
-    const uint32_t large = s.extra * (s.share + 1);
-    return unit < large ? unit / (s.share + 1) : s.extra + (unit - large) / s.share;
 }
 
 // Segment i of a pair; false past its last.
@@ -172,9 +169,8 @@ static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, 
         return true;
     }
     i -= s.waves * s.runs;
-    if (pair >= s.rest_pairs) return false;
     if (PASS <= HEAD_GRADIENT) {             // whole tiles
-        if (i >= s.runs) return false;
+        if (pair >= s.rest || i >= s.runs) return false;
         g.tile = s.waves * a.pairs + pair;
         g.s0 = i * s.run;
         g.last = i + 1 == s.runs;
@@ -183,16 +179,14 @@ static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, 
         g.slot = -1;
         return true;
     }
-    const uint32_t u0 = head_share(s, pair), u1 = head_share(s, pair + 1), t = u0 / s.steps + i;
-    uint32_t b = t * s.steps, e = b + s.steps;
-    if (b >= u1) return false;               // a share lies in two tiles at most
-    b = b > u0 ? b : u0;
-    e = e < u1 ? e : u1;
-    g.tile = s.waves * a.pairs + t;
-    g.slot = e - b == s.steps ? -1 : (int)(2 * pair + i);
-    g.s0 = b - t * s.steps;
-    g.s1 = e - t * s.steps;
     g.first = g.last = true;
+    if (s.rest == 0) return false;
+    const uint32_t part = i * a.pairs + pair, range = part / s.rest;
+    if (range >= s.ranges) return false;
+    g.tile = s.waves * a.pairs + (part - range * s.rest);
+    g.s0 = range * s.steps / s.ranges;
+    g.s1 = (range + 1) * s.steps / s.ranges;
+    g.slot = s.ranges > 1 ? (int)part : -1;
     return true;
 }
 
@@ -200,9 +194,7 @@ static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, 
 static __host__ __device__ __forceinline__ uint32_t head_inputs(const HeadArgs& a, const HeadShape& s, uint32_t pair)
 {
     if (!a.dx) return 0;
-    if (pair >= s.rest_pairs) return s.waves;
-    const uint32_t u0 = head_share(s, pair), u1 = head_share(s, pair + 1);
-    return s.waves + (u1 - 1) / s.steps - u0 / s.steps + 1;
+    return s.waves + (s.ranges * s.rest + a.pairs - 1 - pair) / a.pairs;
 }
 template <int PASS>
 static __host__ __device__ __forceinline__ bool head_next(const HeadArgs& a, const HeadShape& s, const HeadShape& w, uint32_t inputs,
@@ -212,7 +204,7 @@ static __host__ __device__ __forceinline__ bool head_next(const HeadArgs& a, con
     g.input = i < inputs;
     if (g.input) return head_segment<HEAD_INPUT>(a, s, pair, i, g);
     if (!a.dw || !head_segment<HEAD_WEIGHT>(a, w, pair, i - inputs, g)) return false;
-    if (g.slot >= 0) g.slot += 2 * ZERO_HD_PAIRS;
+    if (g.slot >= 0) g.slot += a.slots_x;
     return true;
 }
 
@@ -299,8 +291,29 @@ static __device__ __forceinline__ int bound_exponent(float b)
 }
 
 // ---- the rows ------------------------------------------------------------------------
+// Whether a row is counted, and the exponent of its gradient's scale (-1000: none that is finite).
+static __device__ __forceinline__ bool row_counts(const HeadArgs& a, int64_t row, int& e)
+{
+    e = -1000;
+    if (row >= a.rows) return false;
+    if (a.labels) {
+        if (__ldg(a.labels + row) < 0) return false;
+    } else {                                 // rows of which the teacher has kept something
+        int k = 0;
+        while (k < a.top && !has_entry(a, row, k)) k++;
+        if (k == a.top) return false;
+    }
+    if (!a.backward) return true;
+    float s, hard, soft;
+    row_factors(a, row, s, hard, soft);
+    const float b = factors_bound(a, s, hard, soft);
+    if (b == 0.0f || common_factor(a) == 0.0f) return false;
+    if (b - b == 0.0f) e = bound_exponent(b);
+    return true;
+}
+
 // Which rows are counted, and their gradients' largest power of two: a block takes a chunk of
-// 1024 rows, a warp 32 of them.
+// 1024 rows.  (With one chunk k_head_pack's blocks find this out themselves.)
 static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant__ HeadArgs a)
 {
     __shared__ int32_t counts[32], tops[32];
@@ -311,21 +324,8 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
         a.st->err = 0;
         a.st->ticket = 0;
     }
-    bool in = row < a.rows;
-    if (a.labels) {
-        in = in && __ldg(a.labels + row) >= 0;
-    } else if (in) {                         // rows of which the teacher has kept something
-        in = false;
-        for (int k = 0; k < a.top && !in; k++) in = has_entry(a, row, k);
-    }
-    int e = -1000;
-    if (in && a.backward) {
-        float s, hard, soft;
-        row_factors(a, row, s, hard, soft);
-        const float b = factors_bound(a, s, hard, soft);
-        in = b != 0.0f && common_factor(a) != 0.0f;
-        if (in && b - b == 0.0f) e = bound_exponent(b);
-    }
+    int e;
+    const bool in = row_counts(a, row, e);
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
     e = __reduce_max_sync(0xFFFFFFFFu, e);
     if (lane == 0) {
@@ -414,29 +414,50 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     extern __shared__ __align__(16) int32_t entries_of[];   // a warp's targets: columns, weights
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 8 + warp;
-    let_next_begin();
-    after_previous();
     const int chunks = (int)((a.rows + ZERO_HD_CHUNK - 1) / ZERO_HD_CHUNK);
-    int mine = (int)(row < a.rows ? row >> 10 : chunks), before = 0, all = 0, top = -1000;
-    for (int c = lane; c < chunks; c += 32) {
-        const int n = a.count[c];
-        all += n;
-        if (c < mine) before += n;
-        top = max(top, a.most[c]);
-    }
-    before = __reduce_add_sync(0xFFFFFFFFu, before);
-    all = __reduce_add_sync(0xFFFFFFFFu, all);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        a.st->rows = all;
-        a.st->top = top == -1000 ? 0 : top;
+    int before = 0, all = 0, top = -1000;
+    __shared__ uint32_t masks[32];                          // the row's chunk's mask
+    __shared__ int32_t tops[8];
+    let_next_begin();
+    if (chunks == 1) {
+        for (int i = 0; i < 4; i++) {
+            int e;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, row_counts(a, i * 256 + threadIdx.x, e));
+            top = max(top, __reduce_max_sync(0xFFFFFFFFu, e));
+            if (lane == 0) masks[i * 8 + warp] = m;
+        }
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+        all = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)__popc(masks[lane]));
+        top = __reduce_max_sync(0xFFFFFFFFu, tops[lane & 7]);
+        if (row >= a.rows) before = all;
+    } else {
+        after_previous();
+        const int mine = (int)(row < a.rows ? row >> 10 : chunks);
+        for (int c = lane; c < chunks; c += 32) {
+            const int n = a.count[c];
+            all += n;
+            if (c < mine) before += n;
+            top = max(top, a.most[c]);
+        }
+        before = __reduce_add_sync(0xFFFFFFFFu, before);
+        all = __reduce_add_sync(0xFFFFFFFFu, all);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
     }
     if (top == -1000) top = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.st->rows = all;
+        a.st->top = top;
+        if (chunks == 1) {
+            a.st->err = 0;
+            a.st->ticket = 0;
+        }
+    }
     int64_t at;                                             // packed row
     bool counted = false;
     if (row < a.rows) {
         const int in = (int)(row & 1023), word = in >> 5;
-        const uint32_t w = lane <= word ? a.mask[(row >> 10 << 5) + lane] : 0;
+        const uint32_t w = lane > word ? 0 : chunks == 1 ? masks[lane] : a.mask[(row >> 10 << 5) + lane];
         const uint32_t below = lane < word ? w : w & ((1u << (in & 31)) - 1);
         at = before + __reduce_add_sync(0xFFFFFFFFu, (uint32_t)__popc(below));
         counted = __shfl_sync(0xFFFFFFFFu, w, word) >> (in & 31) & 1;
@@ -586,12 +607,6 @@ static __device__ __forceinline__ uint64_t operand_rows(uint32_t addr)
     return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)2 << 61;
 }
-static __device__ __forceinline__ float read_one(uint32_t at)
-{
-    uint32_t r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(at) : "memory");
-    return __uint_as_float(r);
-}
 static __device__ __forceinline__ void read16(uint32_t at, float (&v)[16])
 {
     uint32_t r[16];
@@ -604,17 +619,6 @@ static __device__ __forceinline__ void read16(uint32_t at, float (&v)[16])
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
-static __device__ __forceinline__ void write16(uint32_t at, const float* v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
-        ::"r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-          "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
-          "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-          "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
-          "r"(at) : "memory");
-}
-
 struct HeadShared {
     uint64_t full[ZERO_HD_STAGES];          // (first SM's) both SMs' operands of a stage have come
     uint64_t empty[ZERO_HD_STAGES];         // its products are done
@@ -989,33 +993,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
             const bool have = __all_sync(0xFFFFFFFFu, head_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, err));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if constexpr (PASS == HEAD_LOGITS) {
-                // z: the tile's sums, runs of it added in fp32.  Logits of targets in these columns: a
-                // lane's accumulators are read at a column of the warp's choice, where the added ones are put back
-                const bool sought = g.last && __any_sync(0xFFFFFFFFu, goal.now.column < WIDE);
+                // z: the tile's sums, runs of it added in fp32
 #pragma unroll
                 for (int c = 0; c < WIDE; c += 16) {
                     float v[16];
                     read16(from + c, v);
-                    if (!g.first) {
 #pragma unroll
-                        for (int e = 0; e < 16; e++) v[e] += z[c + e];
-                        if (sought) write16(from + c, v);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; e++) z[c + e] = v[e];
-                }
-                if (sought) {
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    for (int c; (c = __reduce_min_sync(0xFFFFFFFFu, goal.now.column)) < WIDE;) {
-                        const float v = read_one(from + c);
-                        for (; goal.now.column == c; goal.step(a)) a.found[r * a.slots + goal.next] = have ? v : nan;
-                        __syncwarp();
-                    }
+                    for (int e = 0; e < 16; e++) z[c + e] = v[e] + (g.first ? 0.0f : z[c + e]);
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_first(smem_u32(&sh.sum_empty[acc]));
                 if (!g.last) continue;
+                // logits of targets in these columns, every lane's next one at a time
+                while (__any_sync(0xFFFFFFFFu, goal.now.column < WIDE)) {
+                    float x = z[0];
+#pragma unroll
+                    for (int c = 1; c < WIDE; c++) x = goal.now.column == c ? z[c] : x;
+                    if (goal.now.column < WIDE) {
+                        a.found[r * a.slots + goal.next] = have ? x : nan;
+                        goal.step(a);
+                    }
+                }
                 if (end < WIDE) {
 #pragma unroll
                     for (int c = 0; c < WIDE; c++)
@@ -1066,6 +1065,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
             } else if constexpr (PASS == HEAD_GRADIENT) {
+                const int rows = counted > 0 ? (int)head_up(counted, ZERO_HD_STEP) * ZERO_HD_STEP : ZERO_HD_STEP;
                 for (int c = 0; c < WIDE; c += 32) {
                     float v[32];
                     __syncwarp();
@@ -1085,22 +1085,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] = nan;
                     }
+                    // less the targets' weights, every lane's next target at a time
+                    while (__any_sync(0xFFFFFFFFu, goal.now.column < c + 32)) {
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (goal.now.column == c + e) v[e] -= goal.now.weight;
+                        if (goal.now.column < c + 32) goal.step(a);
+                    }
+                    // rows past the last counted one are read up to a whole stage
+                    if (r - lane >= rows) continue;
                     rows_sent();
                     lay_row<DT>(stage, v);
-                    // once more where the targets are
-                    for (int t; (t = __reduce_min_sync(0xFFFFFFFFu, goal.now.column)) < c + 32;) {
-                        const float v = read_one(from + t);
-                        if (goal.now.column == t) {
-                            float d = row.c1 * exp2_fast(__fmaf_rn(v, a.k1, -row.l1)), w = 0.0f;
-                            if (TWO) d = __fmaf_rn(row.c2, exp2_fast(__fmaf_rn(v, a.k2, -row.l2)), d);
-                            for (; goal.now.column == t; goal.step(a)) w += goal.now.weight;
-                            d = have ? d - w : nan;
-                            const int in = t - c;
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(word_of(stage, lane, in >> 3) + (in & 7) * 2), "h"(narrow1<DT>(d))
-                                         : "memory");
-                        }
-                        __syncwarp();
-                    }
                     send_rows(stage, &map_o, c0 + c, (int)(r - lane));
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1172,20 +1167,18 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
     const int lane = threadIdx.x & 31;
     const uint32_t q = unit >> 7;
     const int strip = (unit >> 4) & 7, c = unit & 15;
-    const uint32_t p0 = head_owner(shape, q * shape.steps), p1 = head_owner(shape, (q + 1) * shape.steps - 1);
     uint32_t ti, tj;
     head_place(head_band<PASS>(a), shape, shape.waves * a.pairs + q, ti, tj);
     const int j = (int)tj * ZERO_HD_TILE + c * 16;
-    if (p0 == p1 || j >= a.cols) return;
-    const uint32_t second = head_share(shape, p0) / shape.steps < q;
-    const float* parts = a.parts + (INPUT ? 0 : 2ll * ZERO_HD_PAIRS * ZERO_HD_SLOT);
+    if (j >= a.cols) return;
+    const float* parts = a.parts + (INPUT ? 0 : (int64_t)a.slots_x * ZERO_HD_SLOT);
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; e++) v[e] = 0.0f;
     const int64_t own = (int64_t)(strip * 64 + c * 4) * 32 + lane;
 #pragma unroll 4
-    for (uint32_t p = p0; p <= p1; p++) {
-        const float4* s = reinterpret_cast<const float4*>(parts + (int64_t)(2 * p + (p == p0 ? second : 0)) * ZERO_HD_SLOT) + own;
+    for (uint32_t p = 0; p < shape.ranges; p++) {
+        const float4* s = reinterpret_cast<const float4*>(parts + (int64_t)(p * shape.rest + q) * ZERO_HD_SLOT) + own;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const float4 f = __ldcg(s + e * 32);
@@ -1244,7 +1237,7 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     const int counted = a.st->rows, top = a.st->top;
     const float common = common_factor(a);
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
-    const uint32_t of_x = a.dx && x.rest_pairs > x.rest ? x.rest * 128 : 0, of_w = a.dw && w.rest_pairs > w.rest ? w.rest * 128 : 0;
+    const uint32_t of_x = a.dx && x.ranges > 1 ? x.rest * 128 : 0, of_w = a.dw && w.ranges > 1 ? w.rest * 128 : 0;
     for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < of_x + of_w; unit += gridDim.x * 8) {
         if (unit < of_x) join<DT, HEAD_INPUT>(a, x, unit, counted, top, common, turn[threadIdx.x >> 5]);
         else join<DT, HEAD_WEIGHT>(a, w, unit - of_x, counted, top, common, turn[threadIdx.x >> 5]);
@@ -1254,7 +1247,7 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
 // ---- the loss ------------------------------------------------------------------------
 // 32 counted rows a block: first a lane a row, the 32 warps sharing the tiles' maxima and sums, then a
 // warp a row.  The last block to finish adds the blocks' sums in order.
-static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
+static __global__ void __launch_bounds__(1024, 2) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
 {
     __shared__ float ms[32][33], ss[32][33], ts[32][33];
     __shared__ double losses[32];
@@ -1269,23 +1262,23 @@ static __global__ void __launch_bounds__(1024) k_head_loss(const __grid_constant
     if (r < counted) {
         const float2* part = a.part + r;
         const float* part2 = a.part2 + r;
-        for (int v = warp; v < tiles; v += 128) {           // four tiles at a time
-            float2 p[4];
-            float p2[4];
+        for (int v = warp; v < tiles; v += 64) {            // two tiles at a time
+            float2 p[2];
+            float p2[2];
             float most = m;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
+            for (int e = 0; e < 2; e++) {
                 const bool in = v + 32 * e < tiles;
                 p[e] = in ? part[(v + 32 * e) * a.npad] : make_float2(low, 0.0f);
                 p2[e] = in && a.two ? part2[(v + 32 * e) * a.npad] : 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 4; e++) most = fmaxf(most, p[e].x);
+            for (int e = 0; e < 2; e++) most = fmaxf(most, p[e].x);
             const float base = most == low ? 0.0f : most;   // (a NaN sum of a lowest maximum is kept)
             s *= exp2_fast((m - base) * a.k1);
             if (a.two) t *= exp2_fast((m - base) * a.k2);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
+            for (int e = 0; e < 2; e++) {
                 s += p[e].y * exp2_fast((p[e].x - base) * a.k1);
                 if (a.two) t += p2[e] * exp2_fast((p[e].x - base) * a.k2);
             }

@@ -70,7 +70,9 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     take(a.part2, tiles * a.npad);
     char* const forward = at;
     at = rest;
-    take(a.xs, a.npad * a.wide);              // backward
+    take(a.heavy, rows * ZERO_HD_HEAVY);      // backward
+    take(a.heavies, rows);
+    take(a.xs, a.npad * a.wide);
     take(a.dz, a.npad * a.pitch);
     take(a.acc, a.npad / ZERO_HD_TILE * up(h->cols, ZERO_HD_TILE) * ZERO_HD_SLOT);
     // as many parts as the largest call has
@@ -278,6 +280,7 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     const bool copied = !aligned_to(w, 16) || ldw % 8 != 0;
     const int64_t rows = a.npad / ZERO_HD_TILE;
     CUtensorMap mx, ms, mz, mt, mo, md, mw, mn;
+    a.vec = !copied;
     a.vec_x = aligned_to(dx, 16) && lddx % 8 == 0;
     a.vec_w = aligned_to(dw, 16) && lddw % 8 == 0;
     if (!map16(&mx, a.xp, a.wide, a.npad, a.wide, 128) || !map16(&ms, a.xs, a.wide, a.npad, a.wide, 64) ||

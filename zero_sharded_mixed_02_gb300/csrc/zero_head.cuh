@@ -35,6 +35,7 @@ namespace zero {
 #define ZERO_HD_SLOT (ZERO_HD_TILE * ZERO_HD_TILE)      // floats of a tile's sums
 #define ZERO_HD_SCALE 14                     // dz is kept times 2^14 over its row's power of two
 #define ZERO_HD_NONE 0x7FFFFFFF              // column of no target
+#define ZERO_HD_HEAVY 8                      // targets of a row with an eighth of its targets' weight or more
 #ifndef ZERO_HD_WAIT_LIMIT                   // polls before a wait gives up
 #define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
 #endif
@@ -56,10 +57,17 @@ struct HeadState {
     int32_t top;                             // largest exponent of their gradients' scales
 };
 
-// A target of a row: its column and its weight, the teacher's share or the label's.
+// A target of a row: its column (24 bits; above them its place among the row's heavy ones, from 1) and its
+// weight, the teacher's share or the label's.
 struct __align__(8) HeadTarget {
     int32_t column;
     float weight;
+};
+
+// A target that has much of its row's weight: its column, and what rounding dz cut off there.
+struct __align__(8) HeadHeavy {
+    int32_t column;
+    float cut;
 };
 
 // A counted row.  Gradients: dz = c1 2^(k1 z - l1) + c2 2^(k2 z - l2) - weight at the targets.
@@ -78,7 +86,7 @@ struct HeadArgs {
     const float *weight, *divisor, *kept;    // the backward pass's row weights, divisor, log-sum-exps
     float *loss, *lse, *sums;
     uint16_t *dx, *dw;
-    int accumulate, vec_x, vec_w;
+    int accumulate, vec, vec_x, vec_w;       // aligned rows: of w, dx, dw
     // workspace
     HeadState* st;
     uint32_t* mask;                          // counted rows, a bit each
@@ -87,6 +95,8 @@ struct HeadArgs {
     HeadRow* info;                           // (forward: c1 is the loss's constant part, c2 the teacher's share)
     HeadTarget* target;                      // of a counted row, by columns
     float* found;                            // their logits
+    HeadHeavy* heavy;                        // [ZERO_HD_HEAVY] of a counted row, and their number
+    int32_t* heavies;
     double* partial;
     float2* part;                            // [tiles of the vocabulary][npad]: maximum, sum
     float* part2;                            // the sum at the temperature
@@ -345,19 +355,33 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
 
 // The targets of a row, the teacher's entries and the label, by columns (equal ones in their order; those that
 // are none come last).  A warp's; `cols` and `vals` are its shared memory, cols filled up with none to a multiple of 4.
-static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t at, const int* cols, const float* vals)
+static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t row, const int* cols, const float* vals)
 {
-    const int n = a.slots;
-    for (int e = threadIdx.x & 31; e < n; e += 32) {
-        const int col = cols[e];
-        int rank = 0;
-        for (int f = 0; f < n; f += 4) {
-            const int4 q = *reinterpret_cast<const int4*>(cols + f);
-            rank += (q.x < col || (q.x == col && f < e)) + (q.y < col || (q.y == col && f + 1 < e)) +
-                    (q.z < col || (q.z == col && f + 2 < e)) + (q.w < col || (q.w == col && f + 3 < e));
+    const int n = a.slots, lane = threadIdx.x & 31;
+    float total = 0.0f;
+    for (int e = lane; e < n; e += 32) total += fabsf(vals[e]);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    int heavies = 0;
+    for (int e = lane; e < n + lane; e += 32) {              // all lanes the same number of turns
+        bool heavy = false;
+        int rank = 0, col = ZERO_HD_NONE;
+        if (e < n) {
+            col = cols[e];
+            for (int f = 0; f < n; f += 4) {
+                const int4 q = *reinterpret_cast<const int4*>(cols + f);
+                rank += (q.x < col || (q.x == col && f < e)) + (q.y < col || (q.y == col && f + 1 < e)) +
+                        (q.z < col || (q.z == col && f + 2 < e)) + (q.w < col || (q.w == col && f + 3 < e));
+            }
+            heavy = a.backward && col != ZERO_HD_NONE && fabsf(vals[e]) >= total * (1.0f / ZERO_HD_HEAVY);
         }
-        a.target[at + rank] = {col, vals[e]};
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, heavy);
+        const int at = heavies + __popc(m & ((1u << lane) - 1));
+        heavy = heavy && at < ZERO_HD_HEAVY;
+        if (heavy) a.heavy[row * ZERO_HD_HEAVY + at] = {col, 0.0f};
+        if (e < n) a.target[row * n + rank] = {heavy ? col | (at + 1) << 24 : col, vals[e]};
+        heavies += __popc(m);
     }
+    if (a.backward && lane == 0) a.heavies[row] = heavies < ZERO_HD_HEAVY ? heavies : ZERO_HD_HEAVY;
 }
 
 // The `wide` columns of a row of `cols` as 16-byte vectors, zeros past its end, whatever the row's
@@ -517,9 +541,10 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
             const int col = __ldg(a.index + row * a.ldt + k);
             float t = teacher_logit(a, row, k);
             if (col < 0) t = low;                           // (a NaN there is not read)
-            cols[k] = t == low ? ZERO_HD_NONE : col;
+            const bool past = t != low && col >= a.vocab;
+            cols[k] = t == low ? ZERO_HD_NONE : past ? 0 : col;
             vals[k] = t;
-            bad = bad || (t != low && col >= a.vocab);
+            bad = bad || past;
             m = fmaxf(m, t);
             if (t != low) share = 1.0f;
         }
@@ -548,13 +573,13 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     if (a.labels && lane == 0) {
         const int label = __ldg(a.labels + row);
         bad = bad || label >= a.vocab;
-        cols[a.slots - 1] = label;
+        cols[a.slots - 1] = label < a.vocab ? label : 0;
         vals[a.slots - 1] = (a.backward ? s * fit : 1.0f) * a.hard;
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
     if (lane < room - a.slots) cols[a.slots + lane] = ZERO_HD_NONE;
     __syncwarp();
-    put_targets(a, at * a.slots, cols, vals);
+    put_targets(a, at, cols, vals);
     if (lane == 0) {
         a.map[at] = (int32_t)row;
         HeadRow h;
@@ -698,6 +723,50 @@ static __device__ __forceinline__ void put_row(const HeadArgs& a, bool input, ui
 // Where 16-byte word q of a lane's row lies in the warp's 32 rows of 64 bytes: at q ^ (row >> 1 & 3), TMA's
 // 64-byte swizzle, in which lanes that each take a row meet all banks.
 static __device__ __forceinline__ uint32_t word_of(uint32_t stage, int row, int q) { return stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4); }
+// What rounding dz cut off at a row's heavy targets, which is most of what dx would be off by (a row's dz
+// is often little else than a label's p - 1): the number of them and the first two, and the addition of all
+// times their weights to N columns from j of dx's sums.
+struct HeadCuts {
+    int n = 0;
+    int4 two;
+    __device__ __forceinline__ void begin(const HeadArgs& a, int64_t row)
+    {
+        n = __ldg(a.heavies + row);
+        two = __ldg(reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY));
+    }
+    template <int DT, int N>
+    __device__ __forceinline__ void add_one(const HeadArgs& a, int2 h, int j, float (&v)[N]) const
+    {
+        const float cut = __int_as_float(h.y);
+        const uint16_t* w = a.w + h.x * a.ldw + j;
+        if (a.vec && j + N <= a.cols) {
+#pragma unroll
+            for (int c = 0; c < N; c += 8) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + c));
+                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    float lo, hi;
+                    widen2<DT>(u[e], lo, hi);
+                    v[c + 2 * e] = __fmaf_rn(cut, lo, v[c + 2 * e]);
+                    v[c + 2 * e + 1] = __fmaf_rn(cut, hi, v[c + 2 * e + 1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; c++)
+                if (j + c < a.cols) v[c] = __fmaf_rn(cut, widen1<DT>(__ldg(w + c)), v[c]);
+        }
+    }
+    template <int DT, int N>
+    __device__ __forceinline__ void add(const HeadArgs& a, int64_t row, int j, float (&v)[N]) const
+    {
+        if (n > 0) add_one<DT>(a, make_int2(two.x, two.y), j, v);
+        if (n > 1) add_one<DT>(a, make_int2(two.z, two.w), j, v);
+        for (int i = 2; i < n; i++) add_one<DT>(a, __ldg(reinterpret_cast<const int2*>(a.heavy + row * ZERO_HD_HEAVY + i)), j, v);
+    }
+};
+
 // 32 columns of a lane's row in 16 bits.
 template <int DT>
 static __device__ __forceinline__ void lay_row(uint32_t stage, const float (&v)[32])
@@ -773,13 +842,19 @@ static __device__ __forceinline__ void put_rows(const HeadArgs& a, bool input, u
 template <bool AHEAD>
 struct HeadGoal {
     const HeadTarget* at;
-    int next, from;
-    HeadTarget now, then;                                   // columns counted from `from`
+    int next, from, heavy;                                  // heavy: this one's place, or 0
+    HeadTarget now, then;                                   // then as it is stored; now's column counted from `from`
     __device__ __forceinline__ HeadTarget load(const HeadArgs& a, int e) const
     {
         if (e >= a.slots) return {ZERO_HD_NONE, 0.0f};
         const int2 q = __ldg(reinterpret_cast<const int2*>(at) + e);
-        return {q.x == ZERO_HD_NONE ? q.x : q.x - from, __int_as_float(q.y)};
+        return {q.x, __int_as_float(q.y)};
+    }
+    __device__ __forceinline__ int place(int column) const { return column == ZERO_HD_NONE ? column : (column & 0xFFFFFF) - from; }
+    __device__ __forceinline__ void take(const HeadTarget& t)
+    {
+        heavy = t.column == ZERO_HD_NONE ? 0 : t.column >> 24;
+        now = {place(t.column), t.weight};
     }
     __device__ __forceinline__ void begin(const HeadArgs& a, int64_t row, int c)
     {
@@ -789,17 +864,17 @@ struct HeadGoal {
         next = 0;
         while (next < hi) {                                  // the first whose column is not below
             const int mid = (next + hi) >> 1;
-            if (__ldg(&at[mid].column) < c) next = mid + 1;
+            if ((__ldg(&at[mid].column) & 0xFFFFFF) < c) next = mid + 1;
             else hi = mid;
         }
-        now = load(a, next);
+        take(load(a, next));
         if (AHEAD) then = load(a, next + 1);
     }
     __device__ __forceinline__ void none() { now = {ZERO_HD_NONE, 0.0f}; }
     __device__ __forceinline__ void step(const HeadArgs& a)
     {
         next++;
-        now = AHEAD ? then : load(a, next);
+        take(AHEAD ? then : load(a, next));
         if (AHEAD) then = load(a, next + 1);
     }
 };
@@ -980,6 +1055,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
             [[maybe_unused]] HeadGoal<PASS == HEAD_GRADIENT> goal;
             [[maybe_unused]] HeadRow row{};
             [[maybe_unused]] uint16_t* to = nullptr;
+            [[maybe_unused]] HeadCuts cuts;
             [[maybe_unused]] float factor = 0.0f;
             if (PASS <= HEAD_GRADIENT) {
                 goal.none();
@@ -989,6 +1065,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                 }
             } else if (g.slot < 0 && (dw || a.last)) {
                 to = out_row(a, !dw, r, counted, top, common, factor);
+                if (!dw && to) cuts.begin(a, r);
             }
             const bool have = __all_sync(0xFFFFFFFFu, head_wait(smem_u32(&sh.sum_full[acc]), (uint32_t)(i >> 1) & 1u, dead, err));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1087,10 +1164,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     }
                     // less the targets' weights, every lane's next target at a time
                     while (__any_sync(0xFFFFFFFFu, goal.now.column < c + 32)) {
+                        float x = 0.0f;
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            if (goal.now.column == c + e) v[e] -= goal.now.weight;
-                        if (goal.now.column < c + 32) goal.step(a);
+                            if (goal.now.column == c + e) x = v[e] -= goal.now.weight;
+                        if (goal.now.column < c + 32) {
+                            // of targets in one column the last has it all
+                            if (goal.heavy && goal.place(goal.then.column) != goal.now.column)
+                                a.heavy[r * ZERO_HD_HEAVY + goal.heavy - 1].cut = x - widen1<DT>(narrow1<DT>(x));
+                            goal.step(a);
+                        }
                     }
                     // rows past the last counted one are read up to a whole stage
                     if (r - lane >= rows) continue;
@@ -1131,7 +1214,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 8; e++)
                             o[(c / 4 + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    } else if (sent) {
+                        continue;
+                    }
+                    if (!dw && to) cuts.add<DT>(a, r, j + c, v);
+                    if (sent) {
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] *= factor;
                         rows_sent();
@@ -1172,6 +1258,11 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
     const int j = (int)tj * ZERO_HD_TILE + c * 16;
     if (j >= a.cols) return;
     const float* parts = a.parts + (INPUT ? 0 : (int64_t)a.slots_x * ZERO_HD_SLOT);
+    const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
+    float factor = 0.0f;
+    uint16_t* to = !INPUT || a.last ? out_row(a, INPUT, r, counted, top, common, factor) : nullptr;
+    HeadCuts cuts;
+    if (INPUT && to) cuts.begin(a, r);
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; e++) v[e] = 0.0f;
@@ -1188,7 +1279,6 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
             v[4 * e + 3] += f.w;
         }
     }
-    const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
     if (INPUT) {
         float4* kept = reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
         if (!a.first) {
@@ -1207,8 +1297,7 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
             return;
         }
     }
-    float factor = 0.0f;
-    uint16_t* to = out_row(a, INPUT, r, counted, top, common, factor);
+    if (INPUT && to) cuts.add<DT>(a, r, j, v);
     if (INPUT ? a.vec_x : a.vec_w) {
         put_row<DT, 16>(a, INPUT, to, factor, j, v);
         return;

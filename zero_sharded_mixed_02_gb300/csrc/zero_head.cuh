@@ -306,6 +306,8 @@ static __device__ __forceinline__ bool row_counts(const HeadArgs& a, int64_t row
 {
     e = -1000;
     if (row >= a.rows) return false;
+    float s = 0.0f, hard = 0.0f, soft = 0.0f;
+    if (a.backward) row_factors(a, row, s, hard, soft);      // (their loads with the label's)
     if (a.labels) {
         if (__ldg(a.labels + row) < 0) return false;
     } else {                                 // rows of which the teacher has kept something
@@ -314,8 +316,6 @@ static __device__ __forceinline__ bool row_counts(const HeadArgs& a, int64_t row
         if (k == a.top) return false;
     }
     if (!a.backward) return true;
-    float s, hard, soft;
-    row_factors(a, row, s, hard, soft);
     const float b = factors_bound(a, s, hard, soft);
     if (b == 0.0f || common_factor(a) == 0.0f) return false;
     if (b - b == 0.0f) e = bound_exponent(b);
@@ -1191,7 +1191,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                 float4* part = g.slot < 0 ? nullptr : reinterpret_cast<float4*>(a.parts + (int64_t)g.slot * ZERO_HD_SLOT) + own;
                 float4* kept = dw ? nullptr : reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
                 const bool sent = dw && !part && a.vec_w && !a.accumulate;
-                for (int c = side * WIDE; c < (side + 1) * WIDE && c < width; c += 32) {
+                // (dx: rows past the last counted one are neither kept nor joined)
+                for (int c = side * WIDE; (dw || r - lane < counted) && c < (side + 1) * WIDE && c < width; c += 32) {
                     float v[32];
                     __syncwarp();
                     read_accumulator(tmem + acc * ZERO_HD_TILE + c + ((uint32_t)quad << 21), v);
@@ -1244,19 +1245,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
 }
 
 // Adds the parts of cut tiles of one pass in the contracted axis's order: a warp takes 32 rows and 16
-// columns of a tile.
-template <int DT, int PASS>
+// columns of a tile, or (DEEP) the eight warps of a block share their parts, add them and the eight sums
+// in order: for tiles of many parts (16 rows of 768 x 50257, 25 parts a tile: 29 us by a warp alone).
+template <int DT, int PASS, bool DEEP>
 static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& shape, uint32_t unit, int counted, int top, float common,
-                                            float (*turn)[17])
+                                            float (*turns)[32][17])
 {
     constexpr bool INPUT = PASS == HEAD_INPUT;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float (*const turn)[17] = turns[warp];
     const uint32_t q = unit >> 7;
     const int strip = (unit >> 4) & 7, c = unit & 15;
     uint32_t ti, tj;
     head_place(head_band<PASS>(a), shape, shape.waves * a.pairs + q, ti, tj);
     const int j = (int)tj * ZERO_HD_TILE + c * 16;
-    if (j >= a.cols) return;
+    if (j >= a.cols || (INPUT && (int)ti * ZERO_HD_TILE + strip * 32 >= counted)) return;     // (of a block, all warps)
     const float* parts = a.parts + (INPUT ? 0 : (int64_t)a.slots_x * ZERO_HD_SLOT);
     const int64_t r = (int64_t)ti * ZERO_HD_TILE + strip * 32 + lane;
     float factor = 0.0f;
@@ -1268,7 +1271,7 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
     for (int e = 0; e < 16; e++) v[e] = 0.0f;
     const int64_t own = (int64_t)(strip * 64 + c * 4) * 32 + lane;
 #pragma unroll 4
-    for (uint32_t p = 0; p < shape.ranges; p++) {
+    for (uint32_t p = DEEP ? warp : 0; p < shape.ranges; p += DEEP ? 8 : 1) {
         const float4* s = reinterpret_cast<const float4*>(parts + (int64_t)(p * shape.rest + q) * ZERO_HD_SLOT) + own;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -1278,6 +1281,20 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
             v[4 * e + 2] += f.z;
             v[4 * e + 3] += f.w;
         }
+    }
+    if (DEEP) {
+        __syncthreads();                                     // (the sums of the unit before have been read)
+#pragma unroll
+        for (int e = 0; e < 16; e++) turn[lane][e] = v[e];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            v[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; w++) v[e] += turns[w][lane][e];
+        }
+        __syncwarp();
     }
     if (INPUT) {
         float4* kept = reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
@@ -1327,9 +1344,17 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     const float common = common_factor(a);
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
     const uint32_t of_x = a.dx && x.ranges > 1 ? x.rest * 128 : 0, of_w = a.dw && w.ranges > 1 ? w.rest * 128 : 0;
+    // by blocks if there are too few units for warps
+    if (of_x + of_w <= 2 * gridDim.x) {
+        for (uint32_t unit = blockIdx.x; unit < of_x + of_w; unit += gridDim.x) {
+            if (unit < of_x) join<DT, HEAD_INPUT, true>(a, x, unit, counted, top, common, turn);
+            else join<DT, HEAD_WEIGHT, true>(a, w, unit - of_x, counted, top, common, turn);
+        }
+        return;
+    }
     for (uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < of_x + of_w; unit += gridDim.x * 8) {
-        if (unit < of_x) join<DT, HEAD_INPUT>(a, x, unit, counted, top, common, turn[threadIdx.x >> 5]);
-        else join<DT, HEAD_WEIGHT>(a, w, unit - of_x, counted, top, common, turn[threadIdx.x >> 5]);
+        if (unit < of_x) join<DT, HEAD_INPUT, false>(a, x, unit, counted, top, common, turn);
+        else join<DT, HEAD_WEIGHT, false>(a, w, unit - of_x, counted, top, common, turn);
     }
 }
 

@@ -651,10 +651,19 @@ struct HeadShared {
     uint64_t drain;
     uint32_t tmem;
     int dead;
+    uint32_t issued;                        // stages this SM has loaded, and the bytes of the last ones
+    uint32_t bytes[ZERO_HD_STAGES];
     uint32_t inputs;                        // (products) a pair's segments of dx
     HeadShape shape, shape_w;
 };
 
+// A word of the second SM's shared memory, at this SM's address of it.
+static __device__ __forceinline__ uint32_t of_second(uint32_t at)
+{
+    uint32_t r;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, 1;\n ld.shared::cluster.u32 %0, [a];\n}" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
 static __device__ __forceinline__ bool head_wait(uint32_t bar, uint32_t parity, volatile int* dead, int32_t* err)
 {
     return pair_wait<ZERO_HD_WAIT_LIMIT>(bar, parity, dead, err);
@@ -906,6 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.dead = 0;
+        sh.issued = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -957,6 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     const uint32_t bar = smem_u32(&sh.full[s]), at = base + s * 2 * ZERO_HD_SIDE, bt = at + ZERO_HD_SIDE;
                     const int k = t * ZERO_HD_STEP;
                     if (rank == 0) mbar_expect_tx(bar, bytes);
+                    else sh.bytes[s] = bytes / 2;
                     if (dw) {
                         box_for_first(at, &map_c, ra, k, bar);
                         box_for_first(at + 8192, &map_c, ra + 64, k, bar);
@@ -974,6 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                     if (++s == ZERO_HD_STAGES) { s = 0; ph ^= 1u; }
                 }
             }
+            sh.issued = n;
             // before this SM's shared memory is given back: both SMs' copies have landed (the
             // first SM knows), and the last products are done
             for (uint32_t q = n > ZERO_HD_STAGES ? n - ZERO_HD_STAGES : 0; q < n; q++) {
@@ -1239,6 +1251,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
         if (PASS != HEAD_LOGITS && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     cluster_sync();
+    // after a wait that gave up, the second SM may have loaded stages that the first has not: those land too
+    if (rank == 0 && threadIdx.x == 0) {
+        const uint32_t mine = sh.issued, other = of_second(smem_u32(&sh.issued));
+        for (uint32_t q = mine; q < other; q++) {
+            const uint32_t bar = smem_u32(&sh.full[q % ZERO_HD_STAGES]);
+            mbar_expect_tx(bar, of_second(smem_u32(&sh.bytes[q % ZERO_HD_STAGES])));
+            for (uint32_t it = 0; it < ZERO_TMA_WAIT_LIMIT && !mbar_try_wait(bar, q / ZERO_HD_STAGES & 1); it++) {
+            }
+        }
+    }
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     cluster_sync();

@@ -664,9 +664,10 @@ uint64_t zero_norm_workspace(const zero_norm_t* norm);
  *                gradient of at a time (2 rows piece bytes of workspace), rounded up
  *                to 256, at most 65536; 0: the library's choice (up to 1 GB).
  *   z_loss       weight of the squared log-sum-exp (0: none).
- *   top, top_dtype, temperature, hard, soft   zero_distill_* only: the teacher's
- *                entries of a row, the type of its logits (fp16, bf16, fp32), the
- *                temperature (> 0) and the weights of the two parts of the loss. */
+ *   top, top_dtype, temperature, hard, soft   zero_distill_* only (others do not look at
+ *                them, but top is counted in the workspace): the teacher's entries of a row,
+ *                the type of its logits (fp16, bf16, fp32), the temperature (> 0) and the
+ *                weights of the two parts of the loss. */
 typedef struct {
     int32_t dtype, top, top_dtype;
     float   temperature, hard, soft, z_loss;
@@ -690,10 +691,10 @@ typedef struct {
  * in a fixed order: equal inputs give equal bits.  Asynchronous.  rows = 0 is accepted
  * (sums are 0).  A bounded device wait that gives up (none should) sets the first
  * int32 of `work` to ZERO_ETIMEOUT and gives NaN.
- * Errors: ZERO_EINVAL (description: types; rows in [0, ZERO_HEAD_MAX_ROWS], cols in [1,
+ * Errors: ZERO_EINVAL (description: type; rows in [0, ZERO_HEAD_MAX_ROWS], cols in [1,
  * ZERO_HEAD_MAX_COLS], vocab in [1, ZERO_HEAD_MAX_VOCAB], piece >= 0, top in [0,
- * ZERO_HEAD_MAX_TOP]; weights that are not finite, temperature not > 0; strides below cols
- * or above 2^31; null or misaligned pointer), ZERO_ECUDA. */
+ * ZERO_HEAD_MAX_TOP], z_loss not finite; strides below cols or above 2^31; null or
+ * misaligned pointer), ZERO_ECUDA. */
 zero_status_t zero_ce_forward(const zero_head_t* head, const void* x, int64_t ldx, const void* w,
                               int64_t ldw, const int32_t* labels, float* loss, float* lse,
                               float* sums, void* work, void* stream);
@@ -704,13 +705,13 @@ zero_status_t zero_ce_forward(const zero_head_t* head, const void* x, int64_t ld
  *   dx_i  = sum_j dz_ij w_j,   dw_j = sum_i dz_ij x_i.
  * lse is what the forward pass wrote.  Rows that take no part, and rows with g_i = 0,
  * have dx = 0 and are not read.  dz is rounded once to dtype, relative to its row's own power of
- * two (so neither a loss scale nor small weights cost bits), all sums are fp32, and dx
- * and dw are rounded once.
+ * two (so neither a loss scale nor small weights cost bits), and dx gets back what that
+ * cut off at the row's heaviest targets; all sums are fp32, and dx and dw are rounded once.
  *   dx, dw      rows lddx, lddw apart, aligned to their element (16-byte aligned rows are
  *               written fastest); either may be NULL: not wanted.  dx may be x itself
  *               (lddx = ldx).
  *   accumulate  1: dw is added to what it holds (one rounding); 0: overwritten.
- * rows = 0 is accepted (dw is 0, or nothing is added).  The rest as zero_ce_forward. */
+ * Results overlap no input but as said.  rows = 0 is accepted (dw is 0, or nothing is added).  The rest as zero_ce_forward. */
 zero_status_t zero_ce_backward(const zero_head_t* head, const void* x, int64_t ldx, const void* w,
                                int64_t ldw, const int32_t* labels, const float* lse,
                                const float* row_grad, float scale, const float* divisor, void* dx,
@@ -728,7 +729,8 @@ zero_status_t zero_ce_backward(const zero_head_t* head, const void* x, int64_t l
  * labels may be NULL: no second part, and a row without an entry takes no part.  With
  * labels a row with a negative label takes no part, and one without an entry has no first
  * part.  An index >= vocab of an entry gives NaN as such a label does.  The rest as zero_ce_forward
- * and zero_ce_backward; also ZERO_EINVAL: head->top < 1, ldt < head->top. */
+ * and zero_ce_backward; also ZERO_EINVAL: head->top < 1, ldt < head->top, its type, weights
+ * that are not finite, a temperature that is not > 0 (or whose inverse is not finite). */
 zero_status_t zero_distill_forward(const zero_head_t* head, const void* x, int64_t ldx,
                                    const void* w, int64_t ldw, const int32_t* top_index,
                                    const void* top_logit, int64_t ldt, const int32_t* labels,

@@ -79,6 +79,16 @@ class Case:
         size = (scale * (1 + lse.abs() + soft_lse.abs() + z.abs().max(1).values))
         return loss, out, torch.stack([loss.sum(), keep.sum().double()]), scale * off + size * 2.0 ** -18
 
+    def lse_bound(self):
+        """A log-sum-exp moves by no more than its logits do (by the softmax's mean of it), at a temperature T by 1/T of
+        that; its sums, exponentials and logarithm add 2^-18 of 1 and itself."""
+        x, z = self.logits()
+        t = self.temperature
+        off = self.logit_error(x, z, run=48)
+        soft = off / t + 2.0 ** -18 * (1 + torch.logsumexp(z / t, 1).abs())
+        hard = off + 2.0 ** -18 * (1 + torch.logsumexp(z, 1).abs())
+        return torch.stack([soft, hard], 1) if self.distill else hard
+
     def logit_error(self, x, z, run):
         top = (x.abs() @ self.w.double().abs().T).max(1).values
         steps = min(run, -(-x.shape[1] // 16)) + x.shape[1] / 768

@@ -112,7 +112,7 @@ class Head:
         loss, lse, sums = self.forward()
         want, want_lse, want_sums, bound = self.case().forward()
         R.close(loss, want, bound, "loss")
-        R.close(lse, want_lse, bound[:, None].expand_as(want_lse) if self.top else bound, "lse")
+        R.close(lse, want_lse, self.case().lse_bound(), "lse")
         if not bool(torch.isnan(want).any()):
             # the losses themselves are added exactly enough: their bounds, and the result's rounding
             assert abs(float(sums[0]) - float(want_sums[0])) <= float(bound.sum()) + 2.0 ** -22 * float(want.abs().sum()) + 1e-30
@@ -481,3 +481,62 @@ def test_gradients_go_into_a_step(z):
     z.zero_step(plan, grads, master, m, v, params, step_work, s)
     assert z.zero_step_result(plan)["skipped"] == 0 and not torch.equal(before, params)
     z.zero_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("top", [0, 6])
+def test_precision_of_the_gradients(z, dtype, top):
+    """In the 2-norm over many rows: a result's own rounding (e0), and of dz's (its relative error is spread over at most
+    half a step, eps / sqrt(3) in the mean square) for dw all of it, for dx what the heavy targets leave, whose
+    share of dz's square is 1 - rho; rows of w and x are independent, so squares add.  A tenth for chance."""
+    kw = dict(top=top, temperature=1.0, hard=0.5, soft=0.5) if top else {}
+    h = Head(z, 600, 512, 2000, dtype, spread=3.0, **kw)
+    lse = h.check_forward()
+    dx, dw = h.backward(lse, scale=64.0)
+    c = h.case()
+    want_x, want_w, _, _ = c.gradient(lse, None, 64.0)
+    x, logits = c.logits()
+    heavy = torch.zeros_like(logits)
+    weight = heavy.clone()
+    if top:
+        q, at, _ = c.teacher()
+        weight.scatter_add_(1, at, 0.5 * q)
+        dz = 0.5 * (logits - lse[:, :1].double()).exp() + 0.5 * (logits - lse[:, 1:].double()).exp()
+    else:
+        dz = (logits - lse[:, None].double()).exp()
+    weight.scatter_add_(1, h.labels.long()[:, None], torch.full_like(logits[:, :1], 0.5 if top else 1.0))
+    dz = dz - weight
+    heavy = weight >= weight.sum(1, keepdim=True) / 8
+    rho = float((dz * ~heavy).square().sum() / dz.square().sum())
+    assert 0.001 < rho < 0.9
+    eps = R.EPS[KIND[dtype]]
+    off = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+    for got, want, share in ((dx, want_x, rho), (dw, want_w, 1.0)):
+        e0 = off(want.to(KIND[dtype]), want)
+        assert off(got, want) < 1.1 * math.sqrt(e0 ** 2 + share * eps ** 2 / 3)
+
+
+def test_teachers_entries_with_a_stride(z):
+    h = Head(z, 70, 64, 500, BF16, top=5, labels=False)
+    loss, lse, _ = h.forward()
+    wide_i, wide_l = torch.full((70, 9), 499, dtype=torch.int32, device="cuda"), torch.full((70, 9), math.nan, device="cuda")
+    wide_i[:, :5], wide_l[:, :5] = h.index, h.logit
+    out, out_lse = torch.empty(70, device="cuda"), torch.empty(70, 2, device="cuda")
+    z.zero_distill_forward(h.head, h.x, 64, h.w, 64, wide_i, wide_l, 9, None, out, out_lse, None, h.work, stream())
+    assert torch.equal(out, loss) and torch.equal(out_lse, lse)
+
+
+def test_weights_of_the_parts(z):
+    """Either part switched off, and negative weights."""
+    for hard, soft in ((0.0, 1.0), (1.0, 0.0), (0.0, 0.0), (-0.5, 0.7), (2.0, 30.0)):
+        h = Head(z, 130, 72, 400, BF16, top=4, temperature=1.5, hard=hard, soft=soft)
+        h.check()
+
+
+def test_largest_sizes_of_one_kind(z):
+    """A row of 16384 columns, a vocabulary of 200003 in many pieces, 65536 rows."""
+    Head(z, 3, 16384, 70, BF16).check()
+    Head(z, 5, 16, 200003, BF16, piece=3000).check()
+    h = Head(z, 65536, 16, 40, BF16, ignored=range(0, 65536, 3))
+    lse = h.check_forward()
+    h.check_backward(lse, row_grad=torch.rand(65536, device="cuda"))

@@ -51,14 +51,24 @@ def both(z, head, forward, backward, teacher):
 
 @pytest.mark.parametrize("bad", [
     dict(dtype=2), dict(dtype=-1), dict(rows=-1), dict(rows=65537), dict(cols=0), dict(cols=16385), dict(vocab=0),
-    dict(vocab=(1 << 24) + 1), dict(piece=-1), dict(top=-1), dict(top=257), dict(top_dtype=3), dict(top_dtype=-1),
-    dict(z_loss=math.nan), dict(z_loss=math.inf), dict(hard=math.nan), dict(soft=math.inf), dict(temperature=0.0),
-    dict(temperature=-1.0), dict(temperature=math.nan), dict(temperature=math.inf), dict(temperature=1e-39)])
+    dict(vocab=(1 << 24) + 1), dict(piece=-1), dict(top=-1), dict(top=257), dict(z_loss=math.nan), dict(z_loss=math.inf)])
 def test_descriptions_refused(z, bad):
     h = description(z, **bad)
     both(z, h, {**FORWARD, "ldx": 1 << 16, "ldw": 1 << 16},
          {**BACKWARD, "ldx": 1 << 16, "ldw": 1 << 16, "lddx": 1 << 16, "lddw": 1 << 16}, {**TEACHER, "ldt": 300})
     assert z.zero_head_workspace(h) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(top_dtype=3), dict(top_dtype=-1), dict(hard=math.nan), dict(soft=math.inf), dict(temperature=0.0),
+    dict(temperature=-1.0), dict(temperature=math.nan), dict(temperature=math.inf), dict(temperature=1e-39), dict(top=0)])
+def test_descriptions_that_only_distillation_refuses(z, bad):
+    h = description(z, **bad)
+    refused(z, z.zero_distill_forward, h, **FORWARD, **TEACHER)
+    refused(z, z.zero_distill_backward, h, **BACKWARD, **TEACHER)
+    assert z.zero_head_workspace(h) > 0
+    refused(z, z.zero_ce_forward, h, **{**FORWARD, "x": None})       # (for its x, not for the description)
+    z.zero_ce_forward(description(z, rows=0, **bad), **{**FORWARD, "sums": None})
 
 
 @pytest.mark.parametrize("bad", [

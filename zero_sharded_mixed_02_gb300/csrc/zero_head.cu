@@ -18,8 +18,11 @@ bool described(const zero_head_t* h)
 {
     return h && (h->dtype == ZERO_FP16 || h->dtype == ZERO_BF16) && h->rows >= 0 && h->rows <= ZERO_HEAD_MAX_ROWS &&
            h->cols >= 1 && h->cols <= ZERO_HEAD_MAX_COLS && h->vocab >= 1 && h->vocab <= ZERO_HEAD_MAX_VOCAB &&
-           h->piece >= 0 && h->top >= 0 && h->top <= ZERO_HEAD_MAX_TOP && h->top_dtype >= ZERO_FP16 &&
-           h->top_dtype <= ZERO_FP32 && isfinite(h->z_loss) && isfinite(h->hard) && isfinite(h->soft) &&
+           h->piece >= 0 && h->top >= 0 && h->top <= ZERO_HEAD_MAX_TOP && isfinite(h->z_loss);
+}
+bool distill_described(const zero_head_t* h)
+{
+    return h->top >= 1 && h->top_dtype >= ZERO_FP16 && h->top_dtype <= ZERO_FP32 && isfinite(h->hard) && isfinite(h->soft) &&
            isfinite(h->temperature) && h->temperature > 0.0f && isfinite(1.4426950408889634f / h->temperature);
 }
 
@@ -121,8 +124,8 @@ bool inputs_ok(const zero_head_t* h, const void* x, int64_t ldx, const void* w, 
                const void* logit, int64_t ldt, const void* labels, const void* work)
 {
     if (!work || !aligned_to(work, 16) || !w || !aligned_to(w, 2) || ldw < h->cols || ldw > (1ll << 31)) return false;
-    if (distill && (h->top < 1 || ldt < h->top || ldt > (1ll << 31))) return false;
-    if (!aligned_to(labels, 4) || !aligned_to(index, 4) || !aligned_to(logit, h->top_dtype == ZERO_FP32 ? 4 : 2)) return false;
+    if (distill && (!distill_described(h) || ldt < h->top || ldt > (1ll << 31))) return false;
+    if (!aligned_to(labels, 4) || !aligned_to(index, 4) || !aligned_to(logit, distill && h->top_dtype == ZERO_FP32 ? 4 : 2)) return false;
     if (h->rows == 0) return true;
     if (!x || !aligned_to(x, 2) || ldx < h->cols || ldx > (1ll << 31)) return false;
     return distill ? index && logit : labels != nullptr;

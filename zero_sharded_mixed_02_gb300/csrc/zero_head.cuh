@@ -238,7 +238,8 @@ static __device__ __forceinline__ int head_width(const HeadArgs& a, uint32_t j)
     return PASS <= HEAD_GRADIENT || a.cols - (int)j * ZERO_HD_TILE > ZERO_HD_TILE / 2 ? ZERO_HD_TILE : ZERO_HD_TILE / 2;
 }
 
-// Whether the kernel's launch may begin before the one before it has ended: this waits for that one's results.
+// A call's kernels begin before the one before has ended; this waits for that one's results.  What a kernel of
+// the call has written is not read through the non-coherent path (__ldg): it may change while this kernel lives.
 static __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 static __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -740,8 +741,8 @@ struct HeadCuts {
     int4 two;
     __device__ __forceinline__ void begin(const HeadArgs& a, int64_t row)
     {
-        n = __ldg(a.heavies + row);
-        two = __ldg(reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY));
+        n = a.heavies[row];
+        two = *reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY);
     }
     template <int DT, int N>
     __device__ __forceinline__ void add_one(const HeadArgs& a, int2 h, int j, float (&v)[N]) const
@@ -772,7 +773,7 @@ struct HeadCuts {
     {
         if (n > 0) add_one<DT>(a, make_int2(two.x, two.y), j, v);
         if (n > 1) add_one<DT>(a, make_int2(two.z, two.w), j, v);
-        for (int i = 2; i < n; i++) add_one<DT>(a, __ldg(reinterpret_cast<const int2*>(a.heavy + row * ZERO_HD_HEAVY + i)), j, v);
+        for (int i = 2; i < n; i++) add_one<DT>(a, *reinterpret_cast<const int2*>(a.heavy + row * ZERO_HD_HEAVY + i), j, v);
     }
 };
 
@@ -856,7 +857,7 @@ struct HeadGoal {
     __device__ __forceinline__ HeadTarget load(const HeadArgs& a, int e) const
     {
         if (e >= a.slots) return {ZERO_HD_NONE, 0.0f};
-        const int2 q = __ldg(reinterpret_cast<const int2*>(at) + e);
+        const int2 q = reinterpret_cast<const int2*>(at)[e];
         return {q.x, __int_as_float(q.y)};
     }
     __device__ __forceinline__ int place(int column) const { return column == ZERO_HD_NONE ? column : (column & 0xFFFFFF) - from; }
@@ -873,7 +874,7 @@ struct HeadGoal {
         next = 0;
         while (next < hi) {                                  // the first whose column is not below
             const int mid = (next + hi) >> 1;
-            if ((__ldg(&at[mid].column) & 0xFFFFFF) < c) next = mid + 1;
+            if ((at[mid].column & 0xFFFFFF) < c) next = mid + 1;
             else hi = mid;
         }
         take(load(a, next));

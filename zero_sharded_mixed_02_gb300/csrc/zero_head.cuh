@@ -200,7 +200,8 @@ static __host__ __device__ __forceinline__ bool head_segment(const HeadArgs& a, 
     return true;
 }
 
-// The products' segments: dx's, then dw's.  `inputs`: how many a pair has of the first.
+// The products' segments: dx's, then dw's, whose tiles are dealt to the pairs from the last one on, so that
+// incomplete rounds of the two fall on different pairs.  `inputs`: how many a pair has of the first.
 static __host__ __device__ __forceinline__ uint32_t head_inputs(const HeadArgs& a, const HeadShape& s, uint32_t pair)
 {
     if (!a.dx) return 0;
@@ -213,7 +214,7 @@ static __host__ __device__ __forceinline__ bool head_next(const HeadArgs& a, con
     if (PASS != HEAD_PRODUCTS) return head_segment<PASS>(a, s, pair, i, g);
     g.input = i < inputs;
     if (g.input) return head_segment<HEAD_INPUT>(a, s, pair, i, g);
-    if (!a.dw || !head_segment<HEAD_WEIGHT>(a, w, pair, i - inputs, g)) return false;
+    if (!a.dw || !head_segment<HEAD_WEIGHT>(a, w, a.pairs - 1 - pair, i - inputs, g)) return false;
     if (g.slot >= 0) g.slot += a.slots_x;
     return true;
 }

@@ -9,6 +9,12 @@
 // Rows that take no part are left out before the first product: a pass over the rows packs the
 // others (aligned, padded with zeros to a whole stage), so what their x holds is not read, and
 // every product's rows are the counted ones.
+//
+// From a thousand rows on the products are bound by the tensor cores, whose memory is busy in 96 % of an
+// SM's active cycles (2048 x 4096 x 32000, bf16: logits 283 us = 1896 TFLOP/s, gradient 293, both products 572);
+// fewer rows by reading the weights (once forward, twice backward) and writing dw, and by about 7 us that a
+// launch of k_head takes to begin and end.  A call's kernels follow each other by programmatic launches,
+// which takes 33 -> 29 us for 64 x 256 x 1000 backward and 109 -> 98 us for 1999 x 771 x 32003 forward.
 #pragma once
 
 #include <cuda.h>
@@ -21,7 +27,7 @@ namespace zero {
 
 #define ZERO_HD_TILE 256                     // rows and columns of a pair's tile
 #define ZERO_HD_STEP 64                      // contracted elements of a stage
-#define ZERO_HD_STAGES 6
+#define ZERO_HD_STAGES 6                     // (five, for twice the rows on their way out: 1 to 3 % slower)
 #define ZERO_HD_SIDE 16384                   // bytes of a stage's operand in one SM
 #define ZERO_HD_WRITERS 16                   // warps that read the accumulators
 #define ZERO_HD_THREADS (128 + 32 * ZERO_HD_WRITERS)    // warp 0 loads, 1 products, from 4 output
@@ -48,6 +54,13 @@ enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT 
 // stores are under way while the other computes.
 __host__ __device__ constexpr int head_groups(int pass) { return pass == HEAD_LOGITS ? 1 : 2; }
 __host__ __device__ constexpr int head_columns(int pass) { return 4 * ZERO_HD_TILE * head_groups(pass) / ZERO_HD_WRITERS; }
+
+// The tensor cores cut each sum off rather than round it, so an accumulator's relative error grows by
+// about 1.6e-8 a step of 16 columns.  The loss is fp32 and would show it: its logits are added in runs of 12
+// stages (48 steps) and the runs in fp32.  8192 x 4096 x 128256: runs of 12 stages are off by 3.5e-7 in the
+// 2-norm, of 24 by 7.4e-7, of 40 by 1.2e-6 (fp32 products without tensor cores: 6e-7), all within 2 % of the same
+// time.  dz is rounded to 16 bits, 2^-9 or 2^-12 in the mean, and needs none; dx's accumulators add at
+// most 65536 columns and dw's 65536 rows (4096 steps: 6.6e-5).
 
 // What the passes over the rows leave for the rest, at the head of the workspace.
 struct HeadState {
@@ -130,7 +143,7 @@ static __host__ __device__ __forceinline__ uint32_t head_up(uint32_t a, uint32_t
 // them: whole waves, then the rest, whose tiles are cut along the contracted axis (INPUT, WEIGHT)
 // where that is long enough to pay for joining the parts.  All are cut at the same places, and the parts of a
 // range of the axis run at about the same time, so that they share their panels in L2: cut into equal shares of all
-// pairs instead, tiles of 2048 rows of 4096 x 64256 took 1260 us with their dw.
+// pairs instead, 1843 rows of 4096 x 64256 took 1260 us with their dw, and take 1036.
 template <int PASS>
 static __host__ __device__ __forceinline__ HeadShape head_shape(const HeadArgs& a, int counted)
 {
@@ -389,7 +402,8 @@ static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t ro
 // The `wide` columns of a row of `cols` as 16-byte vectors, zeros past its end, whatever the row's
 // alignment: put(o, v) gets vector o.  A warp's.  Rows that are not aligned are read in aligned vectors, each
 // lane's shifted together with the next lane's (of the vectors that reach over the row's ends only the
-// row's elements are read): 49 MB of 771 columns in 24 us element by element.
+// row's elements are read): 49 MB of 771 columns in 22 us, 24 element by element (reading and writing them at the
+// rate of HBM takes 15).
 template <class Put>
 static __device__ __forceinline__ void row_vectors(const uint16_t* from, int cols, int wide, Put put)
 {
@@ -433,7 +447,8 @@ static __device__ __forceinline__ void row_vectors(const uint16_t* from, int col
 }
 
 // Packs the counted rows and what belongs to them: a warp a row, eight rows a block; rows past the
-// last counted one are zeros up to a whole tile.
+// last counted one are zeros up to a whole tile.  8192 rows of 4096: 26 us, at HBM's rate 20; a few rows 5 to 7 us,
+// the latency of the label, what depends on it, and the row.
 template <int DT>
 __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadArgs a)
 {
@@ -891,6 +906,15 @@ struct HeadGoal {
 };
 
 // ---- the products --------------------------------------------------------------------
+// A pair's two SMs hold 128 rows each of a tile and half of the other operand; one thread loads an SM's
+// halves of a stage by TMA (both SMs' bytes count on the first one's barrier), one thread of the pair issues
+// the products, and sixteen warps of each SM read the two accumulators in turn:
+//   logits: a thread its row's 64 columns, in registers: runs added, targets picked out, maximum, sum of
+//     exponentials; the four column groups meet in shared memory and leave one pair of numbers a row.
+//   gradient: dz of 32 columns at a time, less the targets' weights, out by TMA through 2 KB a warp (written
+//     by the lanes that have the rows, 32 sectors an access, a piece of 6144 x 25344 x 1600 took 287 us, now 246).
+//   products: dw out the same way (rows that are not aligned, dx and sums that are added: by the warp or its
+//     lanes), parts of cut tiles and dx's sums so far in fp32, four columns of 32 rows a run.
 // map_a, map_b: the operands of the logits or of dx; map_c, map_d: of dw; map_o: where the pass's
 // output goes by TMA (dz; dw where its rows are aligned).
 template <int DT, int PASS, bool TWO>
@@ -1270,7 +1294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
 
 // Adds the parts of cut tiles of one pass in the contracted axis's order: a warp takes 32 rows and 16
 // columns of a tile, or (DEEP) the eight warps of a block share their parts, add them and the eight sums
-// in order: for tiles of many parts (16 rows of 768 x 50257, 25 parts a tile: 29 us by a warp alone).
+// in order: for few tiles, of many parts (16 rows of 768 x 50257, 25 parts a tile: 29 us by warps, 9 by blocks).
 template <int DT, int PASS, bool DEEP>
 static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& shape, uint32_t unit, int counted, int top, float common,
                                             float (*turns)[32][17])
@@ -1384,7 +1408,8 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
 
 // ---- the loss ------------------------------------------------------------------------
 // 32 counted rows a block: first a lane a row, the 32 warps sharing the tiles' maxima and sums, then a
-// warp a row.  The last block to finish adds the blocks' sums in order.
+// warp a row.  The last block to finish adds the blocks' sums in order.  Bound by latency: 7 us for 16 rows of 197
+// tiles, 15 for 8192 of 501 (33 MB).
 static __global__ void __launch_bounds__(1024, 2) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
 {
     __shared__ float ms[32][33], ss[32][33], ts[32][33];

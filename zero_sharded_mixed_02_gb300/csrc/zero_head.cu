@@ -96,12 +96,13 @@ int device_pairs(const HeadKernels& k)
 {
     static std::mutex lock;
     static int pairs[64] = {};
-    for (const void* fn : {k.logits[0], k.logits[1], k.gradient[0], k.gradient[1], k.products})
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ZERO_HD_SMEM) != cudaSuccess) return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::lock_guard<std::mutex> hold(lock);
     if (pairs[dev] == 0) {
+        for (const HeadKernels& of : {head_kernels_fp16(), head_kernels_bf16()})
+            for (const void* fn : {of.logits[0], of.logits[1], of.gradient[0], of.gradient[1], of.products})
+                if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ZERO_HD_SMEM) != cudaSuccess) return 0;
         cudaLaunchConfig_t c{};
         c.gridDim = dim3(2 * ZERO_HD_PAIRS);
         c.blockDim = dim3(ZERO_HD_THREADS);
@@ -249,7 +250,9 @@ zero_status_t forward(const zero_head_t* h, const void* x, int64_t ldx, const vo
     }
     int tiles = (int)up(h->vocab, ZERO_HD_TILE);
     void* args[] = {&a, &tiles};
-    return launch_next((const void*)k_head_loss, dim3((unsigned)up(a.rows, 32)), 1024, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
+    const int64_t blocks = up(a.rows, 32);
+    const void* loss_kernel = blocks <= 2 * pairs ? (const void*)k_head_loss<1> : (const void*)k_head_loss<2>;
+    return launch_next(loss_kernel, dim3((unsigned)blocks), 1024, 0, args, stream) ? ZERO_OK : ZERO_ECUDA;
 }
 
 zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const void* w, int64_t ldw, bool distill,

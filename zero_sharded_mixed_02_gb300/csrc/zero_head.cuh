@@ -953,16 +953,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
     let_next_begin();
-    after_previous();
-    const int counted = a.st->rows;
-    // kept in shared memory: the writers' registers hold sums
-    if (threadIdx.x == 0) {
-        sh.shape = head_shape<PASS == HEAD_PRODUCTS ? HEAD_INPUT : PASS>(a, counted);
+    // kept in shared memory: the writers' registers hold sums.  Of all rows before their number is known, and
+    // once more where not all count
+    auto divide = [&](int rows) {
+        sh.shape = head_shape<PASS == HEAD_PRODUCTS ? HEAD_INPUT : PASS>(a, rows);
         if (PASS == HEAD_PRODUCTS) {
-            sh.shape_w = head_shape<HEAD_WEIGHT>(a, counted);
+            sh.shape_w = head_shape<HEAD_WEIGHT>(a, rows);
             sh.inputs = head_inputs(a, sh.shape, pair);
         }
-    }
+    };
+    if (threadIdx.x == 0) divide((int)a.rows);
+    after_previous();
+    const int counted = a.st->rows;
+    if (threadIdx.x == 0 && counted != (int)a.rows) divide(counted);
     __syncthreads();
     const HeadShape &shape = sh.shape, &shape_w = sh.shape_w;
     const uint32_t& inputs = sh.inputs;
@@ -1410,8 +1413,11 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
 // 32 counted rows a block: first a lane a row, the 32 warps sharing the tiles' maxima and sums, then a
 // warp a row.  The last block to finish adds the blocks' sums in order.  Bound by latency: 7 us for 16 rows of 197
 // tiles, 15 for 8192 of 501 (33 MB).
-static __global__ void __launch_bounds__(1024, 2) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
+// Blocks that have an SM to themselves take eight tiles at a time, others two.
+template <int BLOCKS>
+static __global__ void __launch_bounds__(1024, BLOCKS) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
 {
+    constexpr int EACH = BLOCKS > 1 ? 2 : 8;
     __shared__ float ms[32][33], ss[32][33], ts[32][33];
     __shared__ double losses[32];
     __shared__ bool last;
@@ -1425,23 +1431,23 @@ static __global__ void __launch_bounds__(1024, 2) k_head_loss(const __grid_const
     if (r < counted) {
         const float2* part = a.part + r;
         const float* part2 = a.part2 + r;
-        for (int v = warp; v < tiles; v += 64) {            // two tiles at a time
-            float2 p[2];
-            float p2[2];
+        for (int v = warp; v < tiles; v += 32 * EACH) {
+            float2 p[EACH];
+            float p2[EACH];
             float most = m;
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
+            for (int e = 0; e < EACH; e++) {
                 const bool in = v + 32 * e < tiles;
                 p[e] = in ? part[(v + 32 * e) * a.npad] : make_float2(low, 0.0f);
                 p2[e] = in && a.two ? part2[(v + 32 * e) * a.npad] : 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 2; e++) most = fmaxf(most, p[e].x);
+            for (int e = 0; e < EACH; e++) most = fmaxf(most, p[e].x);
             const float base = most == low ? 0.0f : most;   // (a NaN sum of a lowest maximum is kept)
             s *= exp2_fast((m - base) * a.k1);
             if (a.two) t *= exp2_fast((m - base) * a.k2);
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
+            for (int e = 0; e < EACH; e++) {
                 s += p[e].y * exp2_fast((p[e].x - base) * a.k1);
                 if (a.two) t += p2[e] * exp2_fast((p[e].x - base) * a.k2);
             }

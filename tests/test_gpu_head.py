@@ -159,6 +159,19 @@ def test_strides_and_alignment(z, pad, shift, out, dtype):
     Head(z, 130, 200, 600, dtype, pad=pad, shift=shift).check(scale=64.0, pad=out[0], shift=out[1])
 
 
+@pytest.mark.parametrize("cols", [1, 31, 193, 196, 199, 1479])
+@pytest.mark.parametrize("rows", [64, 1100])
+def test_columns_that_end_inside_a_vector(z, cols, rows):
+    """Aligned rows whose last 16 bytes hold more than the row: what is there is neither used nor written."""
+    pad = -cols % 8
+    h = Head(z, rows, cols, 300, BF16, pad=pad, top=3, hard=0.5, soft=0.5)
+    for buf, n in ((h.x_buf, rows), (h.w_buf, 300)):
+        buf[:n * h.ld].view(n, h.ld)[:, cols:] = math.nan
+    h.check(pad=pad)
+    before = torch.randn(300, cols, device="cuda").bfloat16()
+    h.check_backward(h.forward()[1], pad=pad, accumulate=before)
+
+
 @pytest.mark.parametrize("piece", [1, 256, 512, 700, 1 << 20])
 @pytest.mark.parametrize("shift", [0, 1])
 @pytest.mark.parametrize("top", [0, 7])

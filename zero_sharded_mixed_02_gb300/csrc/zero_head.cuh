@@ -1231,7 +1231,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                 const int64_t own = (int64_t)((rank * 4 + quad) * 64) * 32 + lane;
                 float4* part = g.slot < 0 ? nullptr : reinterpret_cast<float4*>(a.parts + (int64_t)g.slot * ZERO_HD_SLOT) + own;
                 float4* kept = dw ? nullptr : reinterpret_cast<float4*>(a.acc + (int64_t)(ti * shape.tn + tj) * ZERO_HD_SLOT) + own;
-                const bool sent = dw && !part && a.vec_w && !a.accumulate;
+                // (TMA writes whole 16-byte vectors past a matrix's right edge)
+                const int sent = dw && !part && a.vec_w && !a.accumulate ? (a.cols % 8 == 0 ? 1 << 30 : a.cols) : 0;
                 // (dx: rows past the last counted one are neither kept nor joined)
                 for (int c = side * WIDE; (dw || r - lane < counted) && c < (side + 1) * WIDE && c < width; c += 32) {
                     float v[32];
@@ -1259,7 +1260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                         continue;
                     }
                     if (!dw && to) cuts.add<DT>(a, r, j + c, v);
-                    if (sent) {
+                    if (j + c + 32 <= sent) {
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] *= factor;
                         rows_sent();

@@ -131,6 +131,8 @@ class Case:
         each = half * dz.abs() + size * off[:, None]
         if self.x.dtype == torch.float16:
             each = each + 2.0 ** -37 * size.sum(1, keepdim=True)
+        # probabilities below fp32's normal numbers (2^-126) are 0
+        each = each + 2.0 ** -126 * size.sum(1, keepdim=True)
         steps_x, steps_w = -(-z.shape[1] // 16), -(-z.shape[0] // 16)
         dx, dw = dz @ w, dz.T @ x
         a, b = dz.abs() @ w.abs(), dz.abs().T @ x.abs()

@@ -208,7 +208,7 @@ bool weights(HeadArgs& a, int box_rows, bool copied, CUtensorMap* m)
 bool copy_weights(const HeadArgs& a, int pairs, void* stream)
 {
     void* args[] = {const_cast<HeadArgs*>(&a)};
-    const int64_t most = 16ll * pairs, want = up(a.count_v, 8);
+    const int64_t most = 32ll * pairs, want = up(a.count_v, 8);
     return launch_next((const void*)k_head_weights, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream);
 }
 bool product(const void* fn, HeadArgs& a, int64_t tiles, int pairs, CUtensorMap* const (&maps)[5], void* stream)

@@ -262,7 +262,7 @@ static __device__ __forceinline__ float power2(int e)       // 2^e, 0 below the 
 {
     return e < -126 ? 0.0f : __uint_as_float((uint32_t)(e + 127) << 23);
 }
-static __device__ __forceinline__ float exp2_fast(float x)  // within 2 ulp
+static __device__ __forceinline__ float exp2_fast(float x)  // within 2 ulp; 0 below 2^-126
 {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -402,7 +402,7 @@ static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t ro
 // The `wide` columns of a row of `cols` as 16-byte vectors, zeros past its end, whatever the row's
 // alignment: put(o, v) gets vector o.  A warp's.  Rows that are not aligned are read in aligned vectors, each
 // lane's shifted together with the next lane's (of the vectors that reach over the row's ends only the
-// row's elements are read): 49 MB of 771 columns in 22 us, 24 element by element (reading and writing them at the
+// row's elements are read): 49 MB of 771 columns in 19 us, 24 element by element (reading and writing them at the
 // rate of HBM takes 15).
 template <class Put>
 static __device__ __forceinline__ void row_vectors(const uint16_t* from, int cols, int wide, Put put)
@@ -623,8 +623,9 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     }
 }
 
-// Rows of the weights that are not aligned to 16 bytes, a piece of them, to rows that are.
-static __global__ void __launch_bounds__(256) k_head_weights(const __grid_constant__ HeadArgs a)
+// Rows of the weights that are not aligned to 16 bytes, a piece of them, to rows that are.  Eight blocks an SM, two
+// rounds of them (five in 48 registers: 3 us more for 49 MB).
+static __global__ void __launch_bounds__(256, 8) k_head_weights(const __grid_constant__ HeadArgs a)
 {
     let_next_begin();
     after_previous();

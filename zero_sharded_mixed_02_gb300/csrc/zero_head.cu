@@ -162,7 +162,9 @@ HeadArgs arguments(const zero_head_t* h, const void* x, int64_t ldx, const void*
 }
 
 // A launch that may begin while the kernel before it ends (which it waits for before it reads or
-// writes anything): a call's kernels follow each other without the launches' latency.
+// writes anything): a call's kernels follow each other without the launches' latency, and with few rows the
+// first one a kernel before the call that lets it (16 rows of 768 x 50257, call after call: 29.4 -> 28.1 us; blocks of
+// more rows are in each other's way: 777 x 520 x 32003 backward 116 -> 118 us).
 bool launch_next(const void* fn, dim3 grid, int threads, int smem, void** args, void* stream)
 {
     cudaLaunchConfig_t c{};
@@ -184,6 +186,7 @@ bool run_rows(const HeadArgs& a, const HeadKernels& k, void* stream)
     void* args[] = {const_cast<HeadArgs*>(&a)};
     const dim3 grid((unsigned)up(a.rows + ZERO_HD_TILE, 8));
     const int smem = 8 * 2 * ((a.slots + 3) & ~3) * 4;
+    if (a.rows <= ZERO_HD_TILE) return launch_next(k.pack, grid, 256, smem, args, stream);
     if (a.rows <= ZERO_HD_CHUNK) return launch(k.pack, grid, 256, smem, args, stream);
     return launch((const void*)k_head_rows, dim3((unsigned)up(a.rows, ZERO_HD_CHUNK)), ZERO_HD_CHUNK, 0, args, stream) &&
            launch_next(k.pack, grid, 256, smem, args, stream);

@@ -14,7 +14,7 @@
 // SM's active cycles (2048 x 4096 x 32000, bf16: logits 283 us = 1896 TFLOP/s, gradient 293, both products 572);
 // fewer rows by reading the weights (once forward, twice backward) and writing dw, and by about 7 us that a
 // launch of k_head takes to begin and end.  A call's kernels follow each other by programmatic launches,
-// which takes 33 -> 29 us for 64 x 256 x 1000 backward and 109 -> 98 us for 1999 x 771 x 32003 forward.
+// which took 33 -> 29 us for 64 x 256 x 1000 backward and 109 -> 98 us for 1999 x 771 x 32003 forward.
 #pragma once
 
 #include <cuda.h>
@@ -41,7 +41,7 @@ namespace zero {
 #define ZERO_HD_SLOT (ZERO_HD_TILE * ZERO_HD_TILE)      // floats of a tile's sums
 #define ZERO_HD_SCALE 14                     // dz is kept times 2^14 over its row's power of two
 #define ZERO_HD_NONE 0x7FFFFFFF              // column of no target
-#define ZERO_HD_HEAVY 8                      // targets of a row with an eighth of its targets' weight or more
+#define ZERO_HD_HEAVY 4                      // targets of a row with a quarter of its targets' weight or more
 #ifndef ZERO_HD_WAIT_LIMIT                   // polls before a wait gives up
 #define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
 #endif
@@ -316,22 +316,38 @@ static __device__ __forceinline__ int bound_exponent(float b)
 }
 
 // ---- the rows ------------------------------------------------------------------------
+// What decides whether a row is counted, loaded at once (of a teacher's entries the first, mostly enough).
+struct RowFirst {
+    int label, index;
+    float logit, s, hard, soft;
+};
+static __device__ __forceinline__ RowFirst row_first(const HeadArgs& a, int64_t row)
+{
+    RowFirst f{-1, -1, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (row >= a.rows) return f;
+    if (a.labels) {
+        f.label = __ldg(a.labels + row);
+    } else {
+        f.index = __ldg(a.index + row * a.ldt);
+        f.logit = teacher_logit(a, row, 0);
+    }
+    if (a.backward) row_factors(a, row, f.s, f.hard, f.soft);
+    return f;
+}
 // Whether a row is counted, and the exponent of its gradient's scale (-1000: none that is finite).
-static __device__ __forceinline__ bool row_counts(const HeadArgs& a, int64_t row, int& e)
+static __device__ __forceinline__ bool row_counts(const HeadArgs& a, int64_t row, const RowFirst& f, int& e)
 {
     e = -1000;
     if (row >= a.rows) return false;
-    float s = 0.0f, hard = 0.0f, soft = 0.0f;
-    if (a.backward) row_factors(a, row, s, hard, soft);      // (their loads with the label's)
     if (a.labels) {
-        if (__ldg(a.labels + row) < 0) return false;
-    } else {                                 // rows of which the teacher has kept something
-        int k = 0;
+        if (f.label < 0) return false;
+    } else if (f.index < 0 || f.logit == __uint_as_float(0xFF800000u)) {     // rows of which the teacher has kept something
+        int k = 1;
         while (k < a.top && !has_entry(a, row, k)) k++;
-        if (k == a.top) return false;
+        if (k >= a.top) return false;
     }
     if (!a.backward) return true;
-    const float b = factors_bound(a, s, hard, soft);
+    const float b = factors_bound(a, f.s, f.hard, f.soft);
     if (b == 0.0f || common_factor(a) == 0.0f) return false;
     if (b - b == 0.0f) e = bound_exponent(b);
     return true;
@@ -345,12 +361,13 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * ZERO_HD_CHUNK + threadIdx.x;
     let_next_begin();
+    after_previous();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.st->err = 0;
         a.st->ticket = 0;
     }
     int e;
-    const bool in = row_counts(a, row, e);
+    const bool in = row_counts(a, row, row_first(a, row), e);
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
     e = __reduce_max_sync(0xFFFFFFFFu, e);
     if (lane == 0) {
@@ -447,8 +464,9 @@ static __device__ __forceinline__ void row_vectors(const uint16_t* from, int col
 }
 
 // Packs the counted rows and what belongs to them: a warp a row, eight rows a block; rows past the
-// last counted one are zeros up to a whole tile.  8192 rows of 4096: 26 us, at HBM's rate 20; a few rows 5 to 7 us,
-// the latency of the label, what depends on it, and the row.
+// last counted one are zeros up to a whole tile.  8192 rows of 4096: 26 us, at HBM's rate 20; a few rows 5 us, the
+// latency of the label (for 777 rows of a teacher without labels 12 us until all that decides was loaded at once), of
+// what depends on it, and of the row.
 template <int DT>
 __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadArgs a)
 {
@@ -460,10 +478,15 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     __shared__ uint32_t masks[32];                          // the row's chunk's mask
     __shared__ int32_t tops[8];
     let_next_begin();
+    after_previous();
     if (chunks == 1) {
+        RowFirst f[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = row_first(a, i * 256 + threadIdx.x);
+#pragma unroll
         for (int i = 0; i < 4; i++) {
             int e;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, row_counts(a, i * 256 + threadIdx.x, e));
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, row_counts(a, i * 256 + threadIdx.x, f[i], e));
             top = max(top, __reduce_max_sync(0xFFFFFFFFu, e));
             if (lane == 0) masks[i * 8 + warp] = m;
         }
@@ -473,7 +496,6 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         top = __reduce_max_sync(0xFFFFFFFFu, tops[lane & 7]);
         if (row >= a.rows) before = all;
     } else {
-        after_previous();
         const int mine = (int)(row < a.rows ? row >> 10 : chunks);
         for (int c = lane; c < chunks; c += 32) {
             const int n = a.count[c];
@@ -751,15 +773,16 @@ static __device__ __forceinline__ void put_row(const HeadArgs& a, bool input, ui
 // 64-byte swizzle, in which lanes that each take a row meet all banks.
 static __device__ __forceinline__ uint32_t word_of(uint32_t stage, int row, int q) { return stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4); }
 // What rounding dz cut off at a row's heavy targets, which is most of what dx would be off by (a row's dz
-// is often little else than a label's p - 1): the number of them and the first two, and the addition of all
-// times their weights to N columns from j of dx's sums.
+// is often little else than a label's p - 1): the number of them, and their addition, times their weights, to
+// N columns from j of dx's sums.
 struct HeadCuts {
     int n = 0;
-    int4 two;
+    int4 two, four;
     __device__ __forceinline__ void begin(const HeadArgs& a, int64_t row)
     {
         n = a.heavies[row];
-        two = *reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY);
+        two = reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY)[0];
+        four = reinterpret_cast<const int4*>(a.heavy + row * ZERO_HD_HEAVY)[1];
     }
     template <int DT, int N>
     __device__ __forceinline__ void add_one(const HeadArgs& a, int2 h, int j, float (&v)[N]) const
@@ -786,11 +809,12 @@ struct HeadCuts {
         }
     }
     template <int DT, int N>
-    __device__ __forceinline__ void add(const HeadArgs& a, int64_t row, int j, float (&v)[N]) const
+    __device__ __forceinline__ void add(const HeadArgs& a, int j, float (&v)[N]) const
     {
         if (n > 0) add_one<DT>(a, make_int2(two.x, two.y), j, v);
         if (n > 1) add_one<DT>(a, make_int2(two.z, two.w), j, v);
-        for (int i = 2; i < n; i++) add_one<DT>(a, *reinterpret_cast<const int2*>(a.heavy + row * ZERO_HD_HEAVY + i), j, v);
+        if (n > 2) add_one<DT>(a, make_int2(four.x, four.y), j, v);
+        if (n > 3) add_one<DT>(a, make_int2(four.z, four.w), j, v);
     }
 };
 
@@ -1260,7 +1284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                             o[(c / 4 + e) * 32] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                         continue;
                     }
-                    if (!dw && to) cuts.add<DT>(a, r, j + c, v);
+                    if (!dw && to) cuts.add<DT>(a, j + c, v);
                     if (j + c + 32 <= sent) {
 #pragma unroll
                         for (int e = 0; e < 32; e++) v[e] *= factor;
@@ -1367,7 +1391,7 @@ static __device__ __forceinline__ void join(const HeadArgs& a, const HeadShape& 
             return;
         }
     }
-    if (INPUT && to) cuts.add<DT>(a, r, j, v);
+    if (INPUT && to) cuts.add<DT>(a, j, v);
     if (INPUT ? a.vec_x : a.vec_w) {
         put_row<DT, 16>(a, INPUT, to, factor, j, v);
         return;

@@ -252,8 +252,10 @@ static __device__ __forceinline__ int head_width(const HeadArgs& a, uint32_t j)
     return PASS <= HEAD_GRADIENT || a.cols - (int)j * ZERO_HD_TILE > ZERO_HD_TILE / 2 ? ZERO_HD_TILE : ZERO_HD_TILE / 2;
 }
 
-// A call's kernels begin before the one before has ended; this waits for that one's results.  What a kernel of
-// the call has written is not read through the non-coherent path (__ldg): it may change while this kernel lives.
+// A call's kernels begin before the one before has ended; this waits for that one's results.  Nothing is read
+// through the non-coherent path (__ldg), which is for what does not change while a kernel lives.
+template <class T>
+static __device__ __forceinline__ T fetch(const T* p) { return *p; }
 static __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 static __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -271,13 +273,13 @@ static __device__ __forceinline__ float exp2_fast(float x)  // within 2 ulp; 0 b
 static __device__ __forceinline__ float teacher_logit(const HeadArgs& a, int64_t row, int k)
 {
     const int64_t i = row * a.ldt + k;
-    if (a.top_dtype == 2) return __ldg(static_cast<const float*>(a.logit) + i);
-    const uint16_t u = __ldg(static_cast<const uint16_t*>(a.logit) + i);
+    if (a.top_dtype == 2) return fetch(static_cast<const float*>(a.logit) + i);
+    const uint16_t u = fetch(static_cast<const uint16_t*>(a.logit) + i);
     return a.top_dtype == 0 ? widen1<0>(u) : widen1<1>(u);
 }
 static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row, int k)
 {
-    return __ldg(a.index + row * a.ldt + k) >= 0 && teacher_logit(a, row, k) != __uint_as_float(0xFF800000u);
+    return fetch(a.index + row * a.ldt + k) >= 0 && teacher_logit(a, row, k) != __uint_as_float(0xFF800000u);
 }
 
 // What all rows' gradients are multiplied with after the products: scale / divisor (0 where the divisor is), over
@@ -286,12 +288,12 @@ static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row,
 // (which is most of dz's rounding) costs least: 0.7 of a rounding at random, in all rows.
 static __device__ __forceinline__ float common_factor(const HeadArgs& a)
 {
-    const float d = a.divisor ? __ldg(a.divisor) : 1.0f;
+    const float d = a.divisor ? fetch(a.divisor) : 1.0f;
     return d == 0.0f ? 0.0f : a.scale / a.unit / d;
 }
 static __device__ __forceinline__ float row_scale(const HeadArgs& a, int64_t row)
 {
-    return a.weight ? __ldg(a.weight + row) : a.unit;
+    return a.weight ? fetch(a.weight + row) : a.unit;
 }
 // Factors of the two softmaxes in a row's gradient before the row's power of two, and a bound of |dz|.
 static __device__ __forceinline__ void row_factors(const HeadArgs& a, int64_t row, float& s, float& hard, float& soft)
@@ -299,7 +301,7 @@ static __device__ __forceinline__ void row_factors(const HeadArgs& a, int64_t ro
     s = row_scale(a, row);
     hard = 0.0f;
     if (a.labels) {
-        const float l = a.index ? __ldg(a.kept + 2 * row + 1) : __ldg(a.kept + row);
+        const float l = a.index ? fetch(a.kept + 2 * row + 1) : fetch(a.kept + row);
         hard = s * a.hard * (1.0f + 2.0f * a.z_loss * l);
     }
     soft = a.index ? s * a.soft * a.temperature : 0.0f;
@@ -326,9 +328,9 @@ static __device__ __forceinline__ RowFirst row_first(const HeadArgs& a, int64_t 
     RowFirst f{-1, -1, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row >= a.rows) return f;
     if (a.labels) {
-        f.label = __ldg(a.labels + row);
+        f.label = fetch(a.labels + row);
     } else {
-        f.index = __ldg(a.index + row * a.ldt);
+        f.index = fetch(a.index + row * a.ldt);
         f.logit = teacher_logit(a, row, 0);
     }
     if (a.backward) row_factors(a, row, f.s, f.hard, f.soft);
@@ -429,11 +431,11 @@ static __device__ __forceinline__ void row_vectors(const uint16_t* from, int col
     auto load = [&](int g) {
         uint32_t w[4] = {0, 0, 0, 0};
         const int e = 8 * g - s;
-        if (e >= 0 && e + 8 <= cols) return __ldg(reinterpret_cast<const uint4*>(from + e));
+        if (e >= 0 && e + 8 <= cols) return fetch(reinterpret_cast<const uint4*>(from + e));
         if (e < cols) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                if (e + i >= 0 && e + i < cols) w[i / 2] |= (uint32_t)__ldg(from + e + i) << 16 * (i & 1);
+                if (e + i >= 0 && e + i < cols) w[i / 2] |= (uint32_t)fetch(from + e + i) << 16 * (i & 1);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         const float low = __uint_as_float(0xFF800000u);
         float m = low, sum = 0.0f, cross = 0.0f;
         for (int k = lane; k < a.top; k += 32) {
-            const int col = __ldg(a.index + row * a.ldt + k);
+            const int col = fetch(a.index + row * a.ldt + k);
             float t = teacher_logit(a, row, k);
             if (col < 0) t = low;                           // (a NaN there is not read)
             const bool past = t != low && col >= a.vocab;
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         else soft = 0.0f;
     }
     if (a.labels && lane == 0) {
-        const int label = __ldg(a.labels + row);
+        const int label = fetch(a.labels + row);
         bad = bad || label >= a.vocab;
         cols[a.slots - 1] = label < a.vocab ? label : 0;
         vals[a.slots - 1] = (a.backward ? s * fit : 1.0f) * a.hard;
@@ -625,8 +627,8 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         if (a.backward) {
             a.exponent[at] = e;
             const float log2e = 1.4426950408889634f;
-            const float soft_l = a.index ? __ldg(a.kept + 2 * row) : 0.0f;
-            const float hard_l = !a.labels ? 0.0f : a.index ? __ldg(a.kept + 2 * row + 1) : __ldg(a.kept + row);
+            const float soft_l = a.index ? fetch(a.kept + 2 * row) : 0.0f;
+            const float hard_l = !a.labels ? 0.0f : a.index ? fetch(a.kept + 2 * row + 1) : fetch(a.kept + row);
             h.c1 = hard * fit;
             h.l1 = hard_l * log2e;
             h.c2 = soft * fit;
@@ -792,7 +794,7 @@ struct HeadCuts {
         if (a.vec && j + N <= a.cols) {
 #pragma unroll
             for (int c = 0; c < N; c += 8) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + c));
+                const uint4 q = fetch(reinterpret_cast<const uint4*>(w + c));
                 const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
@@ -805,7 +807,7 @@ struct HeadCuts {
         } else {
 #pragma unroll
             for (int c = 0; c < N; c++)
-                if (j + c < a.cols) v[c] = __fmaf_rn(cut, widen1<DT>(__ldg(w + c)), v[c]);
+                if (j + c < a.cols) v[c] = __fmaf_rn(cut, widen1<DT>(fetch(w + c)), v[c]);
         }
     }
     template <int DT, int N>

@@ -295,14 +295,15 @@ static __device__ __forceinline__ float row_scale(const HeadArgs& a, int64_t row
 {
     return a.weight ? fetch(a.weight + row) : a.unit;
 }
-// Factors of the two softmaxes in a row's gradient before the row's power of two, and a bound of |dz|.
+// Factors of the two softmaxes in a row's gradient before the row's power of two, and a bound of |dz|.  A row of weight
+// 0 has none whatever its log-sum-exp is (0 times inf or NaN would be NaN), and without z_loss that is no factor.
 static __device__ __forceinline__ void row_factors(const HeadArgs& a, int64_t row, float& s, float& hard, float& soft)
 {
     s = row_scale(a, row);
     hard = 0.0f;
     if (a.labels) {
         const float l = a.index ? fetch(a.kept + 2 * row + 1) : fetch(a.kept + row);
-        hard = s * a.hard * (1.0f + 2.0f * a.z_loss * l);
+        hard = s == 0.0f ? 0.0f : s * a.hard * (a.z_loss == 0.0f ? 1.0f : 1.0f + 2.0f * a.z_loss * l);
     }
     soft = a.index ? s * a.soft * a.temperature : 0.0f;
 }

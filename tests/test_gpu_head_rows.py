@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import head_reference as R  # noqa: E402
-from test_gpu_head import BF16, Head, z  # noqa: E402, F401
+from test_gpu_head import BF16, FP16, Head, stream, z  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,41 @@ def test_rows_of_no_weight_whose_loss_is_not_finite(z, rows, top, labels, z_loss
     assert bool((dx[10:33] == 0).all())
     R.close(dx, want_x, bound_x, "dx")
     R.close(dw, want_w, bound_w, "dw")
+
+
+# ---- no row that counts -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale,divisor", [(math.inf, 1.0), (math.nan, 1.0), (1.0, math.nan), (1.0, 0.0), (1e38, 1e-30)])
+@pytest.mark.parametrize("rows", [40, 2100])                 # 2100: where rows count, tiles are cut along them
+def test_no_row_counts_and_the_factor_is_not_finite(z, scale, divisor, rows):  # noqa: F811
+    """A sum over no rows is 0 whatever it is multiplied with."""
+    h = Head(z, rows, 72, 3000, FP16, ignored=range(rows))
+    lse = torch.zeros(rows, device="cuda")
+    d = torch.tensor([divisor], device="cuda")
+    dx, dw = h.backward(lse, None, scale, d)
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
+    before = torch.randn(3000, 72, device="cuda").half()
+    assert torch.equal(h.backward(lse, None, scale, d, accumulate=before)[1], before)
+
+
+@pytest.mark.parametrize("lddw", [1 << 30, 1 << 31])
+def test_no_rows_and_rows_of_the_gradient_far_apart(z, lddw):  # noqa: F811
+    h = z.head(BF16, 0, 64, 2)
+    work = torch.empty(z.zero_head_workspace(h), dtype=torch.uint8, device="cuda")
+    dw = torch.full((lddw + 72,), 3.0, dtype=torch.bfloat16, device="cuda")
+    z.zero_ce_backward(h, None, 64, dw, 64, None, None, None, 1.0, None, None, 64, dw, lddw, 0, work, stream())
+    for at in (0, lddw):
+        assert bool((dw[at:at + 64] == 0).all())
+    assert bool((dw[64:72] == 3.0).all()) and bool((dw[lddw - 8:lddw] == 3.0).all()) and bool((dw[lddw + 64:] == 3.0).all())
+
+
+def test_no_rows_and_odd_places(z):  # noqa: F811
+    for cols, ld, shift in ((1, 1, 0), (5, 9, 1), (8, 8, 0), (771, 773, 3), (4096, 4104, 0)):
+        h = z.head(FP16, 0, cols, 1003)
+        work = torch.empty(z.zero_head_workspace(h), dtype=torch.uint8, device="cuda")
+        dw = torch.full((1003 * ld + shift + 8,), 3.0, dtype=torch.float16, device="cuda")
+        z.zero_ce_backward(h, None, cols, dw, cols, None, None, None, 1.0, None, None, cols, dw[shift:], ld, 0, work, stream())
+        inner = dw[shift:shift + 1003 * ld].view(1003, ld)
+        assert bool((inner[:, :cols] == 0).all())
+        inner[:, :cols] = 3.0
+        assert bool((dw == 3.0).all())

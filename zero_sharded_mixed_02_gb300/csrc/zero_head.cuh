@@ -283,7 +283,7 @@ static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row,
 }
 
 // What all rows' gradients are multiplied with after the products: scale / divisor (0 where the divisor is), over
-// `unit`.  A row's dz is kept times its weight, or where rows have none times `unit`, one over the sum of the
+// `unit`; sums over no rows are 0 whatever that is.  A row's dz is kept times its weight, or where rows have none times `unit`, one over the sum of the
 // parts' weights: a label's coefficient p - 1 then lies just below a power of two, where rounding it
 // (which is most of dz's rounding) costs least: 0.7 of a rounding at random, in all rows.
 static __device__ __forceinline__ float common_factor(const HeadArgs& a)
@@ -1106,7 +1106,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
         const float nan = __uint_as_float(0x7FC00000u), low = __uint_as_float(0xFF800000u);
         [[maybe_unused]] const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
         [[maybe_unused]] const int top = a.st->top;
-        [[maybe_unused]] const float common = PASS == HEAD_PRODUCTS ? common_factor(a) : 0.0f;
+        [[maybe_unused]] const float common = PASS == HEAD_PRODUCTS && counted > 0 ? common_factor(a) : 0.0f;
         [[maybe_unused]] float z[PASS == HEAD_LOGITS ? WIDE : 1];
         // maxima and sums of a tile's column groups but the first: [group][which][lane] of this quad
         [[maybe_unused]] const auto merge = reinterpret_cast<float(*)[3][32]>(
@@ -1421,7 +1421,7 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     let_next_begin();
     after_previous();
     const int counted = a.st->rows, top = a.st->top;
-    const float common = common_factor(a);
+    const float common = counted > 0 ? common_factor(a) : 0.0f;
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
     const uint32_t of_x = a.dx && x.ranges > 1 ? x.rest * 128 : 0, of_w = a.dw && w.ranges > 1 ? w.rest * 128 : 0;
     // by blocks if there are too few units for warps

@@ -704,9 +704,13 @@ zero_status_t zero_ce_forward(const zero_head_t* head, const void* x, int64_t ld
  *   dz_ij = g_i (p_ij (1 + 2 z_loss l_i) - [j = y_i]),   p_ij = exp(z_ij - lse[i])
  *   dx_i  = sum_j dz_ij w_j,   dw_j = sum_i dz_ij x_i.
  * lse is what the forward pass wrote.  Rows that take no part, and rows with g_i = 0,
- * have dx = 0 and are not read.  dz is rounded once to dtype, relative to its row's own power of
- * two (so neither a loss scale nor small weights cost bits), and dx gets back what that
+ * have dx = 0 and are not read, whatever their lse.  dz is rounded once to dtype, relative to its row's
+ * own power of two (so neither a loss scale nor small weights cost bits), and dx gets back what that
  * cut off at the row's heaviest targets; all sums are fp32, and dx and dw are rounded once.
+ * dw adds rows times their powers of two.  Where these differ (row_grad or z_loss), fp16's short exponent
+ * moves a row's part of a dw by up to 2^-39 of the largest |g_i x_ik| of all rows (times hard + soft T and
+ * 1 + 2 z_loss l): two of fp16's smallest numbers at most while that is within its range.  bf16 keeps rows whose
+ * scale is 2^-100 of the largest.
  *   dx, dw      rows lddx, lddw apart, aligned to their element (16-byte aligned rows are
  *               written fastest); either may be NULL: not wanted.  dx may be x itself
  *               (lddx = ldx).

@@ -1,11 +1,11 @@
-"""Rows of the losses over the vocabulary that take no part, against 64 bits (head_reference.py)."""
+"""Rows of the losses over the vocabulary that take no part, rows whose weights lie far apart, against 64 bits (head_reference.py)."""
 import math
 
 import pytest
 
 torch = pytest.importorskip("torch")
 import head_reference as R  # noqa: E402
-from test_gpu_head import BF16, FP16, Head, stream, z  # noqa: E402, F401
+from test_gpu_head import BF16, FP16, KIND, Head, stream, z  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,96 @@ def test_no_rows_and_odd_places(z):  # noqa: F811
         assert bool((inner[:, :cols] == 0).all())
         inner[:, :cols] = 3.0
         assert bool((dw == 3.0).all())
+
+
+# ---- weights far apart ------------------------------------------------------------------------------
+
+def apart(z, dtype, groups, times, kw, size=1.0):  # noqa: F811
+    """Rows and tokens in groups that have nothing to do with each other's softmax: token j of group k has 12 in column k, and
+    so have the group's rows, so that another group's logits lie 144 lower."""
+    tokens, each = 8, 4 * times
+    h = Head(z, groups * each, 32 + groups, groups * tokens, dtype, **kw)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    of_row, of_token = (torch.arange(groups, device="cuda").repeat_interleave(n) for n in (each, tokens))
+    h.w.copy_(torch.randn(h.w.shape, generator=gen, device="cuda") * 0.2)
+    h.w[:, :groups] = 12.0 / size * torch.nn.functional.one_hot(of_token, groups).to(KIND[dtype])
+    h.x.copy_(torch.randn(h.x.shape, generator=gen, device="cuda") * size)
+    h.x[:, :groups] = 12.0 * size * torch.nn.functional.one_hot(of_row, groups).to(KIND[dtype])
+    if h.labels is not None:
+        h.labels.copy_(of_row * tokens + torch.randint(tokens, of_row.shape, generator=gen, device="cuda"))
+    if h.top:
+        h.index.copy_(of_row[:, None] * tokens + torch.randint(tokens, h.index.shape, generator=gen, device="cuda"))
+    return h, of_row, of_token
+
+
+@pytest.mark.parametrize("times", [1, 30])                   # up to 1024 rows, more
+@pytest.mark.parametrize("kw", [{}, dict(top=3, temperature=2.0, hard=0.5, soft=0.25)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -9, 2.0 ** 10])    # of x
+def test_fp16_weights_far_apart(z, times, kw, size):  # noqa: F811
+    """Weights of 1 to 2^-24, a group of tokens each, whose gradients are all fp16's numbers or far from overflow.  Per
+    element of dw, before its own rounding: dz's rounding (half a step, and half of its smallest number, 2^-39 of its row's
+    power of two), what its logits' errors change of the probabilities, 2^-20 of the targets' weights, and the sums
+    (2^-22 a step of 16 rows, 2^-20 for what follows).  And x's: where B_i is the bound of row i's dz (2 g_i of a cross
+    entropy) and 2^R the largest power of two of a B_i times that of the largest |x_ik|, x times its row's power of two
+    2^e <= B_i is kept below 2^16 in steps of 2^-24 at most, so that dz x is off by no more than |dz_ij| 2^(R - 40 - e)."""
+    groups = 13
+    h, of_row, _ = apart(z, FP16, groups, times, kw, size)
+    lse = h.check_forward()
+    g = torch.exp2(-2.0 * of_row.float())
+    scale = 2.0 ** 9 / size / times
+    _, dw = h.backward(lse, g, scale)
+    _, want, _, _ = h.case().gradient(lse, g, scale)
+    assert float(want.abs().max()) < 65504.0
+    c, kept, eps = h.case(), lse.double(), R.EPS[torch.float16]
+    (x, logits), t = c.logits(), c.temperature
+    p = c.hard * (logits - (kept[:, 1:] if h.top else kept[:, None])).exp()
+    weight = torch.zeros_like(p).scatter_add(1, h.labels.long()[:, None], torch.full_like(p[:, :1], c.hard))
+    if h.top:
+        q, at, _ = c.teacher()
+        p = p + c.soft * t * (logits / t - kept[:, :1]).exp()
+        weight.scatter_add_(1, at, c.soft * t * q)
+    gd = g.double()[:, None]
+    most = 2.0 * (c.hard + (c.soft * t if h.top else 0.0)) * gd                     # B
+    e = torch.floor(torch.log2(most))
+    reach = (e[:, 0] + torch.floor(torch.log2(x.abs().max(1).values))).max()
+    dz = gd * (p - weight)
+    off = c.logit_error(x, logits, run=1 << 30)[:, None] * 2 / min(t, 1.0)
+    each = eps * dz.abs() + torch.exp2(e - 39) + gd * (p * off + 2.0 ** -20 * weight)
+    sums = -(-h.rows // 16) * 2.0 ** -22 + 2.0 ** -20
+    bound = each.T @ x.abs() + sums * (dz.abs().T @ x.abs()) + (dz.abs() * torch.exp2(reach - 40 - e)).sum(0)[:, None]
+    R.close(dw, want, scale * bound, "dw")
+
+
+def test_fp16_one_row_far_above_the_others(z):  # noqa: F811
+    """Of 300 rows one has 2^20 times the others' weight and almost no loss: the others' tokens keep their gradients."""
+    h, of_row, of_token = apart(z, FP16, 2, 75, {})
+    h.labels[0] = 0
+    h.w[0] *= 2.0                                            # token 0 is certain for group 0
+    lse = h.check_forward()
+    g = torch.ones(h.rows, device="cuda")
+    g[0] = 2.0 ** 20
+    g[1:h.rows // 2] = 0.0
+    dx, dw = h.backward(lse, g, 16.0)
+    want_x, want_w, bound_x, _ = h.case().gradient(lse, g, 16.0)
+    R.close(dx, want_x, bound_x, "dx")
+    mine = of_token == 1
+    off = float((dw.double() - want_w)[mine].norm() / want_w[mine].norm())
+    assert off < 2.0 ** -10, off
+
+
+def test_fp16_rows_of_zeros_and_of_one_element(z):  # noqa: F811
+    """The largest weight belongs to a row of zeros; other rows hold fp16's smallest and largest numbers alone."""
+    h = Head(z, 70, 40, 60, FP16)
+    h.x[3] = 0.0
+    h.x[5], h.x[6] = 0.0, 0.0
+    h.x[5, 7], h.x[6, 9] = 2.0 ** -24, 65504.0
+    lse = h.check_forward()
+    g = torch.full((70,), 2.0 ** -20, device="cuda")
+    g[3] = 2.0 ** 100
+    g[6] = 2.0 ** -30
+    dx, dw = h.backward(lse, g, 16.0)
+    keep = g.clone()
+    keep[3] = 2.0 ** -20                                     # its x is 0 and so is its part of dw
+    _, want_w, _, bound_w = h.case().gradient(lse, keep, 16.0)
+    R.close(dw, want_w, bound_w, "dw")
+    assert bool((dw[:, 9] != 0).any())

@@ -75,6 +75,7 @@ uint64_t lay_out(const zero_head_t* h, HeadArgs& a, char* at)
     at = rest;
     take(a.heavy, rows * ZERO_HD_HEAVY);      // backward
     take(a.heavies, rows);
+    take(a.reach, a.npad);
     take(a.xs, a.npad * a.wide);
     take(a.dz, a.npad * a.pitch);
     take(a.acc, a.npad / ZERO_HD_TILE * up(h->cols, ZERO_HD_TILE) * ZERO_HD_SLOT);
@@ -286,6 +287,11 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     const HeadKernels k = kernels_of(h->dtype);
     const int pairs = device_pairs(k);
     if (pairs == 0 || !encode() || !run_rows(a, k, stream)) return ZERO_ECUDA;
+    if (h->dtype == ZERO_FP16 && a.xs != a.xp && dw) {
+        void* args[] = {&a};
+        const int64_t most = 16ll * pairs, want = up(a.npad, 8);
+        if (!launch_next((const void*)k_head_lift, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream)) return ZERO_ECUDA;
+    }
     const bool copied = !aligned_to(w, 16) || ldw % 8 != 0;
     const int64_t rows = a.npad / ZERO_HD_TILE;
     CUtensorMap mx, ms, mz, mt, mo, md, mw, mn;

@@ -41,6 +41,7 @@ namespace zero {
 #define ZERO_HD_SLOT (ZERO_HD_TILE * ZERO_HD_TILE)      // floats of a tile's sums
 #define ZERO_HD_SCALE 14                     // dz is kept times 2^14 over its row's power of two
 #define ZERO_HD_NONE 0x7FFFFFFF              // column of no target
+#define ZERO_HD_NO_REACH (-100000)           // exponent of a row that has none
 #define ZERO_HD_HEAVY 4                      // targets of a row with a quarter of its targets' weight or more
 #ifndef ZERO_HD_WAIT_LIMIT                   // polls before a wait gives up
 #define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
@@ -68,6 +69,7 @@ struct HeadState {
     uint32_t ticket;
     int32_t rows;                            // counted rows
     int32_t top;                             // largest exponent of their gradients' scales
+    int32_t lift;                            // of the packed rows for dw: 2^lift times what their own scales would make them
 };
 
 // A target of a row: its column (24 bits; above them its place among the row's heavy ones, from 1) and its
@@ -105,6 +107,7 @@ struct HeadArgs {
     uint32_t* mask;                          // counted rows, a bit each
     int32_t *count, *most;                   // of a chunk of rows: how many; their largest exponent
     int32_t *map, *exponent;                 // counted row -> row, its scale's exponent
+    int32_t* reach;                          // (backward, fp16) the exponent of its scale times its largest x
     HeadRow* info;                           // (forward: c1 is the loss's constant part, c2 the teacher's share)
     HeadTarget* target;                      // of a counted row, by columns
     float* found;                            // their logits
@@ -113,7 +116,7 @@ struct HeadArgs {
     double* partial;
     float2* part;                            // [tiles of the vocabulary][npad]: maximum, sum
     float* part2;                            // the sum at the temperature
-    uint16_t *xp, *xs, *wp, *dz;             // packed rows, the same scaled, weights where repacked, dz
+    uint16_t *xp, *xs, *wp, *dz;             // packed rows, the same scaled for dw, weights where repacked, dz
     float *acc, *parts;
     int64_t npad, pitch;                     // packed rows, columns of dz
     int wide;                                // columns of packed rows
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.st->rows = all;
         a.st->top = top;
+        a.st->lift = 0;
         if (chunks == 1) {
             a.st->err = 0;
             a.st->ticket = 0;
@@ -546,17 +550,22 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     // the row
     float up = 1.0f;
     int e = 0;
+    [[maybe_unused]] bool finite = true;
     float s = 0.0f, hard = 0.0f, soft = 0.0f;
     if (counted && a.backward) {
         row_factors(a, row, s, hard, soft);
         const float b = factors_bound(a, s, hard, soft);
         e = bound_exponent(b);
-        up = b - b == 0.0f ? power2(e - top) : 1.0f;
-        if (!(b - b == 0.0f)) e = top;
+        finite = b - b == 0.0f;
+        up = finite ? power2(e - top) : 1.0f;
+        if (!finite) e = top;
     }
+    uint32_t large = 0;                                     // (fp16) largest |x| of even and odd columns
     row_vectors(a.x + (counted ? row : 0) * a.ldx, counted ? a.cols : 0, a.wide, [&](int o, uint4 q) {
         reinterpret_cast<uint4*>(a.xp + at * a.wide)[o] = q;
-        if (a.xs != a.xp) {
+        if (DT == 0) {
+            large = __vmaxu2(large, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+        } else if (a.xs != a.xp) {
             uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -568,6 +577,12 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
         }
     });
     if (!counted) return;
+    if (DT == 0 && a.xs != a.xp) {
+        // (a row that is 0 decides nothing, nor does one without a finite scale, whose dw is not finite either)
+        large = __reduce_max_sync(0xFFFFFFFFu, max(large & 0xFFFFu, large >> 16));
+        const int most = (int)(__float_as_uint(widen1<0>((uint16_t)large)) >> 23) - 127;
+        if (lane == 0) a.reach[at] = large == 0 || !finite ? ZERO_HD_NO_REACH : e + min(most, 15);
+    }
     // its targets and coefficients
     const int room = (a.slots + 3) & ~3;
     int* cols = entries_of + warp * 2 * room;
@@ -645,6 +660,47 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
             h.l1 = h.l2 = 0.0f;
         }
         a.info[at] = h;
+    }
+}
+
+// The packed rows for dw of fp16 gradients whose rows have scales of their own: a row times its power of two over the
+// largest row's, as k_head_pack multiplies bf16's, would fall below fp16's normal numbers (2^-14) for a row of small
+// weight.  All are lifted by one power of two, so that the largest element ends in [2^15, 2^16): rounding a row then moves its
+// part of dw by at most 2^-39 of the largest |g x| of all rows, two of fp16's smallest numbers where that is its largest.
+// Every block finds the power by itself; a warp a row.  A launch of its own, since the power needs all packed rows: 64 x 256 x
+// 1000 with row weights 27 -> 30 us, 1023 x 771 x 32003 182 -> 186.
+static __global__ void __launch_bounds__(256) k_head_lift(const __grid_constant__ HeadArgs a)
+{
+    __shared__ int32_t tops[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    let_next_begin();
+    after_previous();
+    const int counted = a.st->rows, top = a.st->top;
+    int reach = ZERO_HD_NO_REACH;
+    for (int r = threadIdx.x; r < counted; r += 256) reach = max(reach, a.reach[r]);
+    reach = __reduce_max_sync(0xFFFFFFFFu, reach);
+    if (lane == 0) tops[warp] = reach;
+    __syncthreads();
+    reach = __reduce_max_sync(0xFFFFFFFFu, tops[lane & 7]);
+    const int lift = reach == ZERO_HD_NO_REACH ? 0 : 15 - (reach - top);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.st->lift = lift;
+    const int end = counted > 0 ? (int)head_up(counted, ZERO_HD_TILE) * ZERO_HD_TILE : ZERO_HD_TILE;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + warp; r < end; r += (int64_t)gridDim.x * 8) {
+        // (above 2^15 times 2^24 only a row of zeros is lifted)
+        const int k = r < counted ? a.exponent[r] - top + lift : 0;
+        const float up = power2(k < 127 ? k : 127);
+#pragma unroll 4
+        for (int o = lane; o < a.wide / 8; o += 32) {
+            const uint4 q = reinterpret_cast<const uint4*>(a.xp + r * a.wide)[o];
+            uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float lo, hi;
+                widen2<0>(w[i], lo, hi);
+                w[i] = narrow2<0>(lo * up, hi * up);
+            }
+            reinterpret_cast<uint4*>(a.xs + r * a.wide)[o] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
@@ -747,7 +803,9 @@ static __device__ __forceinline__ uint16_t* out_row(const HeadArgs& a, bool inpu
         return a.dx + a.map[i] * a.lddx;
     }
     if (i >= a.count_v) return nullptr;
-    factor = power2(top - ZERO_HD_SCALE) * common;
+    // (in two steps: one alone may lie below fp32's normal numbers)
+    const int k = top - ZERO_HD_SCALE, half = k / 2;
+    factor = power2(half) * common * power2(k - half);
     return a.dw + (a.v0 + i) * a.lddw;
 }
 
@@ -1105,7 +1163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
         const int quad = warp & 3, side = ((warp - 4) >> 2) % (4 / GROUPS), group = (warp - 4) / (ZERO_HD_WRITERS / GROUPS);
         const float nan = __uint_as_float(0x7FC00000u), low = __uint_as_float(0xFF800000u);
         [[maybe_unused]] const uint32_t stage = base + ZERO_HD_STAGES * 2 * ZERO_HD_SIDE + (warp - 4) * ZERO_HD_ROWS;
-        [[maybe_unused]] const int top = a.st->top;
+        [[maybe_unused]] const int top = a.st->top - a.st->lift;
         [[maybe_unused]] const float common = PASS == HEAD_PRODUCTS && counted > 0 ? common_factor(a) : 0.0f;
         [[maybe_unused]] float z[PASS == HEAD_LOGITS ? WIDE : 1];
         // maxima and sums of a tile's column groups but the first: [group][which][lane] of this quad
@@ -1420,7 +1478,7 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     __shared__ float turn[8][32][17];
     let_next_begin();
     after_previous();
-    const int counted = a.st->rows, top = a.st->top;
+    const int counted = a.st->rows, top = a.st->top - a.st->lift;
     const float common = counted > 0 ? common_factor(a) : 0.0f;
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
     const uint32_t of_x = a.dx && x.ranges > 1 ? x.rest * 128 : 0, of_w = a.dw && w.ranges > 1 ? w.rest * 128 : 0;

@@ -175,3 +175,14 @@ def test_fp16_rows_of_zeros_and_of_one_element(z):  # noqa: F811
     _, want_w, _, bound_w = h.case().gradient(lse, keep, 16.0)
     R.close(dw, want_w, bound_w, "dw")
     assert bool((dw[:, 9] != 0).any())
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+def test_rows_of_which_the_teacher_kept_nothing(z, dtype):  # noqa: F811
+    """All of their weight is the label's; others have some absent entries."""
+    h = Head(z, 600, 512, 2000, dtype, spread=1.0, top=6, temperature=2.0, hard=0.5, soft=0.5)
+    h.index[:300] = -1
+    h.index[300:400, 3:] = -1
+    h.logit[:300], h.logit[300:400, 3:] = math.nan, -math.inf
+    lse = h.check_forward()
+    gradient_of_inputs(h, lse, slice(0, 300))

@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
             cross += __shfl_xor_sync(0xFFFFFFFFu, cross, o);
         }
         const float each = (a.backward ? s * fit : 1.0f) * a.soft * a.temperature;
-        for (int k = lane; k < a.top; k += 32) vals[k] = vals[k] / sum * each;
+        // (none of them: sum is 0)
+        for (int k = lane; k < a.top; k += 32) vals[k] = cols[k] == ZERO_HD_NONE ? 0.0f : vals[k] / sum * each;
         // sum q log q = sum q t - log(sum)
         if (share > 0.0f) constant = a.soft * a.temperature * a.temperature * (cross / sum - logf(sum));
         else soft = 0.0f;

@@ -177,6 +177,34 @@ def test_fp16_rows_of_zeros_and_of_one_element(z):  # noqa: F811
     assert bool((dw[:, 9] != 0).any())
 
 
+# ---- what dx gets back of dz's rounding ------------------------------------------------------------
+
+def gradient_of_inputs(h, lse, rows):
+    """dx of these rows in the 2-norm: its own rounding, and of dz's what the heavy columns leave (those with a quarter of
+    the row's weight or more), eps / sqrt(3) of it in the mean square.  A tenth for chance.  The rows' weights put what the
+    targets get of dz, some -1, just above a power of two, where rounding it costs most."""
+    g = 1.02 + 0.2 * torch.rand(h.rows, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    dx, _ = h.backward(lse, g, 64.0)
+    c = h.case()
+    want, _, _, _ = c.gradient(lse, g, 64.0)
+    (x, logits), t = c.logits(), c.temperature
+    kept, weight = lse.double(), torch.zeros_like(logits)
+    dz = torch.zeros_like(logits)
+    q, at, has = c.teacher()
+    weight.scatter_add_(1, at, c.soft * t * q)
+    dz += c.soft * t * (logits / t - kept[:, :1]).exp() * has[:, None]
+    if h.labels is not None:
+        weight.scatter_add_(1, h.labels.long()[:, None], torch.full_like(logits[:, :1], c.hard))
+        dz += c.hard * (logits - kept[:, 1:]).exp()
+    dz = (dz - weight) * g.double()[:, None]
+    heavy = weight >= weight.sum(1, keepdim=True) * 0.25
+    rho = float((dz * ~heavy)[rows].square().sum() / dz[rows].square().sum())
+    off = lambda got: float((got.double() - want)[rows].norm() / want[rows].norm())  # noqa: E731
+    assert rho < 0.3
+    eps = R.EPS[KIND[h.dtype]]
+    assert off(dx) < 1.1 * math.sqrt(off(want.to(KIND[h.dtype])) ** 2 + rho * eps ** 2 / 3), (off(dx), rho)
+
+
 @pytest.mark.parametrize("dtype", [FP16, BF16])
 def test_rows_of_which_the_teacher_kept_nothing(z, dtype):  # noqa: F811
     """All of their weight is the label's; others have some absent entries."""

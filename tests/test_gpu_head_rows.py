@@ -1,4 +1,5 @@
-"""Rows of the losses over the vocabulary that take no part, rows whose weights lie far apart, against 64 bits (head_reference.py)."""
+"""Rows of the losses over the vocabulary that take no part, rows whose weights lie far apart, and targets that
+share a column, against 64 bits (head_reference.py)."""
 import math
 
 import pytest
@@ -214,3 +215,20 @@ def test_rows_of_which_the_teacher_kept_nothing(z, dtype):  # noqa: F811
     h.logit[:300], h.logit[300:400, 3:] = math.nan, -math.inf
     lse = h.check_forward()
     gradient_of_inputs(h, lse, slice(0, 300))
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+def test_a_light_label_on_a_heavy_entry(z, dtype):  # noqa: F811
+    h = Head(z, 600, 512, 2000, dtype, spread=1.0, top=6, temperature=2.0, hard=0.1, soft=0.45)
+    h.logit[:, 2] += 12.0
+    h.labels.copy_(h.index[:, 2])
+    gradient_of_inputs(h, h.check_forward(), slice(None))
+
+
+@pytest.mark.parametrize("labels", [False, True])
+def test_entries_of_one_column_that_are_light_alone(z, labels):  # noqa: F811
+    """Of nine equal entries five are one column, which has more than half of the weight; the others none has a quarter of."""
+    h = Head(z, 600, 512, 2000, BF16, spread=1.0, top=9, temperature=1.0, labels=labels, hard=0.1, soft=1.0)
+    h.logit[:] = 4.0
+    h.index[:, 4:9] = h.index[:, 4:5]
+    gradient_of_inputs(h, h.check_forward(), slice(None))

@@ -392,7 +392,8 @@ static __global__ void __launch_bounds__(1024) k_head_rows(const __grid_constant
 }
 
 // The targets of a row, the teacher's entries and the label, by columns (equal ones in their order; those that
-// are none come last).  A warp's; `cols` and `vals` are its shared memory, cols filled up with none to a multiple of 4.
+// are none come last).  Whether targets are heavy goes by their column's weight, and the last of them stands for it.  A
+// warp's; `cols` and `vals` are its shared memory, cols filled up with none to a multiple of 4.
 static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t row, const int* cols, const float* vals)
 {
     const int n = a.slots, lane = threadIdx.x & 31;
@@ -402,15 +403,26 @@ static __device__ __forceinline__ void put_targets(const HeadArgs& a, int64_t ro
     int heavies = 0;
     for (int e = lane; e < n + lane; e += 32) {              // all lanes the same number of turns
         bool heavy = false;
-        int rank = 0, col = ZERO_HD_NONE;
+        int rank = 0, same = 0, col = ZERO_HD_NONE;
         if (e < n) {
             col = cols[e];
             for (int f = 0; f < n; f += 4) {
                 const int4 q = *reinterpret_cast<const int4*>(cols + f);
                 rank += (q.x < col || (q.x == col && f < e)) + (q.y < col || (q.y == col && f + 1 < e)) +
                         (q.z < col || (q.z == col && f + 2 < e)) + (q.w < col || (q.w == col && f + 3 < e));
+                same += (q.x == col) + (q.y == col) + (q.z == col) + (q.w == col);
             }
-            heavy = a.backward && col != ZERO_HD_NONE && fabsf(vals[e]) >= total * (1.0f / ZERO_HD_HEAVY);
+            if (a.backward && col != ZERO_HD_NONE) {
+                float weight = vals[e];
+                bool last = true;
+                if (same > 1)
+                    for (int f = 0; f < n; f++)
+                        if (f != e && cols[f] == col) {
+                            weight += vals[f];
+                            last = last && f < e;
+                        }
+                heavy = last && fabsf(weight) >= total * (1.0f / ZERO_HD_HEAVY);
+            }
         }
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, heavy);
         const int at = heavies + __popc(m & ((1u << lane) - 1));
@@ -1297,8 +1309,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ZERO_HD_THREADS, 1)
                         for (int e = 0; e < 32; e++)
                             if (goal.now.column == c + e) x = v[e] -= goal.now.weight;
                         if (goal.now.column < c + 32) {
-                            // of targets in one column the last has it all
-                            if (goal.heavy && goal.place(goal.then.column) != goal.now.column)
+                            // (of targets in one column that is the last, which has it all)
+                            if (goal.heavy)
                                 a.heavy[r * ZERO_HD_HEAVY + goal.heavy - 1].cut = x - widen1<DT>(narrow1<DT>(x));
                             goal.step(a);
                         }

@@ -232,3 +232,50 @@ def test_entries_of_one_column_that_are_light_alone(z, labels):  # noqa: F811
     h.logit[:] = 4.0
     h.index[:, 4:9] = h.index[:, 4:5]
     gradient_of_inputs(h, h.check_forward(), slice(None))
+
+
+# ---- captured after work that is not a kernel of the same stream --------------------------------------
+
+@pytest.mark.parametrize("rows", [16, 300, 1300])
+@pytest.mark.parametrize("before", ["nothing", "copy", "clear", "two streams"])
+def test_captured_behind_other_work(z, rows, before):  # noqa: F811
+    """The first kernel of few rows' calls may begin early; behind whatever a graph holds it waits for all of it."""
+    h = Head(z, rows, 136, 1500, BF16)
+    source = h.x.clone()
+    want_loss, want_lse, _ = h.forward()
+    want = h.backward(want_lse)
+    loss, lse = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    dx, dw = torch.zeros_like(h.x), torch.zeros_like(h.w)
+    other = torch.cuda.Stream()
+    big = torch.zeros(1 << 26, device="cuda")
+
+    def step():
+        if before == "copy":
+            h.x.copy_(source)
+        elif before == "clear":
+            big.add_(1.0)
+            h.x.zero_()
+            h.x.add_(source)
+            loss.zero_()
+        elif before == "two streams":
+            mine = torch.cuda.current_stream()
+            other.wait_stream(mine)
+            h.x.zero_()
+            with torch.cuda.stream(other):
+                big.add_(1.0)
+                h.w.mul_(1.0)
+            h.x.add_(source)
+            mine.wait_stream(other)
+        z.zero_ce_forward(h.head, h.x, 136, h.w, 136, h.labels, loss, lse, None, h.work, stream())
+        z.zero_ce_backward(h.head, h.x, 136, h.w, 136, h.labels, lse, None, 1.0, None, dx, 136, dw, 136, 0, h.work, stream())
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (loss, lse, dx, dw):
+            t.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((loss, lse, dx, dw), (want_loss, want_lse, *want)):
+            assert torch.equal(a, b)

@@ -662,7 +662,10 @@ uint64_t zero_norm_workspace(const zero_norm_t* norm);
  *   dtype        fp16 or bf16: x, w, dx, dw.
  *   piece        columns of the vocabulary that the backward pass keeps the logits'
  *                gradient of at a time (2 rows piece bytes of workspace), rounded up
- *                to 256, at most 65536; 0: the library's choice (up to 1 GB).
+ *                to 256, at most 65536; 0: the library's choice (up to 1 GB, the fastest).
+ *                The workspace also has room for a copy of unaligned rows of w (up to
+ *                256 MB, less with a smaller piece): with few rows it is larger than their logits
+ *                would be.
  *   z_loss       weight of the squared log-sum-exp (0: none).
  *   top, top_dtype, temperature, hard, soft   zero_distill_* only (others do not look at
  *                them, but top is counted in the workspace): the teacher's entries of a row,

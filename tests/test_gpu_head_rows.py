@@ -178,6 +178,30 @@ def test_fp16_rows_of_zeros_and_of_one_element(z):  # noqa: F811
     assert bool((dw[:, 9] != 0).any())
 
 
+@pytest.mark.parametrize("rows", [60, 1500])
+def test_fp16_weights_equal_bits_and_captured(z, rows):  # noqa: F811
+    """Whatever the workspace holds, and in a graph; dw alone, and dx alone, whose rows are not lifted."""
+    h = Head(z, rows, 136, 3000, FP16, ignored=range(0, rows, 5), piece=1024)
+    lse = h.check_forward()
+    g = torch.exp2(-20.0 * torch.rand(rows, device="cuda"))
+    first = h.check_backward(lse, row_grad=g, scale=64.0)
+    for _ in range(5):
+        h.space[:h.work.numel()].random_(0, 256)
+        assert all(torch.equal(a, b) for a, b in zip(first, h.backward(lse, g, 64.0)))
+    for want in ((True, False), (False, True)):
+        h.space[:h.work.numel()].random_(0, 256)
+        one = h.backward(lse, g, 64.0, want=want)
+        assert all(torch.equal(a, b) for a, b, w in zip(first, one, want) if w)
+    dx, dw = torch.zeros_like(h.x), torch.zeros_like(h.w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z.zero_ce_backward(h.head, h.x, 136, h.w, 136, h.labels, lse, g, 64.0, None, dx, 136, dw, 136, 0, h.work, stream())
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx, first[0]) and torch.equal(dw, first[1])
+
+
 # ---- what dx gets back of dz's rounding ------------------------------------------------------------
 
 def gradient_of_inputs(h, lse, rows):

@@ -287,7 +287,7 @@ zero_status_t backward(const zero_head_t* h, const void* x, int64_t ldx, const v
     const HeadKernels k = kernels_of(h->dtype);
     const int pairs = device_pairs(k);
     if (pairs == 0 || !encode() || !run_rows(a, k, stream)) return ZERO_ECUDA;
-    if (h->dtype == ZERO_FP16 && a.xs != a.xp && dw) {
+    if (h->dtype == ZERO_FP16 && a.xs != a.xp && dw) {       // xs, which k_head_pack writes itself for bf16
         void* args[] = {&a};
         const int64_t most = 16ll * pairs, want = up(a.npad, 8);
         if (!launch_next((const void*)k_head_lift, dim3((unsigned)(want < most ? want : most)), 256, 0, args, stream)) return ZERO_ECUDA;

@@ -11,10 +11,11 @@
 // every product's rows are the counted ones.
 //
 // From a thousand rows on the products are bound by the tensor cores, whose memory is busy in 96 % of an
-// SM's active cycles (2048 x 4096 x 32000, bf16: logits 283 us = 1896 TFLOP/s, gradient 293, both products 572);
-// fewer rows by reading the weights (once forward, twice backward) and writing dw, and by about 7 us that a
-// launch of k_head takes to begin and end.  A call's kernels follow each other by programmatic launches,
-// which took 33 -> 29 us for 64 x 256 x 1000 backward and 109 -> 98 us for 1999 x 771 x 32003 forward.
+// SM's active cycles (4096 x 4096 x 128256, bf16, settled under the power limit: forward 2395 us = 1797 TFLOP/s,
+// backward 7463 = 1730; a library product 1882 at first and 1698 sustained); fewer rows by reading the weights (once
+// forward, twice backward) and writing dw, and by about 7 us that a launch of k_head takes to begin and end.  A call's
+// kernels follow each other by programmatic launches, which took 33 -> 29 us for 64 x 256 x 1000 backward and 109 -> 98
+// us for 1999 x 771 x 32003 forward.
 #pragma once
 
 #include <cuda.h>
@@ -42,7 +43,7 @@ namespace zero {
 #define ZERO_HD_SCALE 14                     // dz is kept times 2^14 over its row's power of two
 #define ZERO_HD_NONE 0x7FFFFFFF              // column of no target
 #define ZERO_HD_NO_REACH (-100000)           // exponent of a row that has none
-#define ZERO_HD_HEAVY 4                      // targets of a row with a quarter of its targets' weight or more
+#define ZERO_HD_HEAVY 4                      // columns of a row with a quarter of its targets' weight or more
 #ifndef ZERO_HD_WAIT_LIMIT                   // polls before a wait gives up
 #define ZERO_HD_WAIT_LIMIT ZERO_TMA_WAIT_LIMIT
 #endif
@@ -50,9 +51,9 @@ namespace zero {
 enum HeadPass { HEAD_LOGITS = 0, HEAD_GRADIENT = 1, HEAD_INPUT = 2, HEAD_WEIGHT = 3, HEAD_PRODUCTS = 4 };
 
 // How the writers share the work.  Logits, whose runs are added in registers: all read every tile,
-// 64 columns each (128 would spill: 6.4 against 4.4 ms at 8192 x 128256 x 4096).  The others: two groups of
-// eight take tiles in turn, one accumulator each, 128 columns a warp, so that one group's loads and
-// stores are under way while the other computes.
+// 64 columns each (128 would spill: 6.4 against 4.4 ms at 8192 x 128256 x 4096; 64 at two temperatures spill 4 bytes).
+// The others: two groups of eight take tiles in turn, one accumulator each, 128 columns a warp, so that one group's
+// loads and stores are under way while the other computes.
 __host__ __device__ constexpr int head_groups(int pass) { return pass == HEAD_LOGITS ? 1 : 2; }
 __host__ __device__ constexpr int head_columns(int pass) { return 4 * ZERO_HD_TILE * head_groups(pass) / ZERO_HD_WRITERS; }
 
@@ -60,8 +61,8 @@ __host__ __device__ constexpr int head_columns(int pass) { return 4 * ZERO_HD_TI
 // about 1.6e-8 a step of 16 columns.  The loss is fp32 and would show it: its logits are added in runs of 12
 // stages (48 steps) and the runs in fp32.  8192 x 4096 x 128256: runs of 12 stages are off by 3.5e-7 in the
 // 2-norm, of 24 by 7.4e-7, of 40 by 1.2e-6 (fp32 products without tensor cores: 6e-7), all within 2 % of the same
-// time.  dz is rounded to 16 bits, 2^-9 or 2^-12 in the mean, and needs none; dx's accumulators add at
-// most 65536 columns and dw's 65536 rows (4096 steps: 6.6e-5).
+// time.  (At 768 columns, one run, by 6e-7, fp32 products by 2.5e-7.)  dz is rounded to 16 bits, 2^-9 or 2^-12 in the
+// mean, and needs none; dx's accumulators add at most 65536 columns and dw's 65536 rows (4096 steps: 6.6e-5).
 
 // What the passes over the rows leave for the rest, at the head of the workspace.
 struct HeadState {
@@ -286,9 +287,9 @@ static __device__ __forceinline__ bool has_entry(const HeadArgs& a, int64_t row,
 }
 
 // What all rows' gradients are multiplied with after the products: scale / divisor (0 where the divisor is), over
-// `unit`; sums over no rows are 0 whatever that is.  A row's dz is kept times its weight, or where rows have none times `unit`, one over the sum of the
-// parts' weights: a label's coefficient p - 1 then lies just below a power of two, where rounding it
-// (which is most of dz's rounding) costs least: 0.7 of a rounding at random, in all rows.
+// `unit`; sums over no rows are 0 whatever that is.  A row's dz is kept times its weight, or where rows have none times
+// `unit`, one over the sum of the parts' weights: a label's coefficient p - 1 then lies just below a power of two,
+// where rounding it (which is most of dz's rounding) costs least: 0.7 of a rounding at random, in all rows.
 static __device__ __forceinline__ float common_factor(const HeadArgs& a)
 {
     const float d = a.divisor ? fetch(a.divisor) : 1.0f;
@@ -575,9 +576,11 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
     uint32_t large = 0;                                     // (fp16) largest |x| of even and odd columns
     row_vectors(a.x + (counted ? row : 0) * a.ldx, counted ? a.cols : 0, a.wide, [&](int o, uint4 q) {
         reinterpret_cast<uint4*>(a.xp + at * a.wide)[o] = q;
+        if (a.xs == a.xp) return;
+        const uint32_t m = 0x7FFF7FFFu;
         if (DT == 0) {
-            large = __vmaxu2(large, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
-        } else if (a.xs != a.xp) {
+            large = __vmaxu2(large, __vmaxu2(__vmaxu2(q.x & m, q.y & m), __vmaxu2(q.z & m, q.w & m)));
+        } else {
             uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -678,10 +681,10 @@ __global__ void __launch_bounds__(256) k_head_pack(const __grid_constant__ HeadA
 
 // The packed rows for dw of fp16 gradients whose rows have scales of their own: a row times its power of two over the
 // largest row's, as k_head_pack multiplies bf16's, would fall below fp16's normal numbers (2^-14) for a row of small
-// weight.  All are lifted by one power of two, so that the largest element ends in [2^15, 2^16): rounding a row then moves its
-// part of dw by at most 2^-39 of the largest |g x| of all rows, two of fp16's smallest numbers where that is its largest.
-// Every block finds the power by itself; a warp a row.  A launch of its own, since the power needs all packed rows: 64 x 256 x
-// 1000 with row weights 27 -> 30 us, 1023 x 771 x 32003 182 -> 186.
+// weight.  All are lifted by one power of two, so that the largest element ends in [2^15, 2^16): rounding a row then
+// moves its part of dw by at most 2^-39 of the largest |g x| of all rows, two of fp16's smallest numbers where that is
+// its largest.  Every block finds the power by itself; a warp a row.  A launch of its own, since the power needs all
+// packed rows: 64 x 256 x 1000 with row weights 27 -> 30 us, 1023 x 771 x 32003 182 -> 186.
 static __global__ void __launch_bounds__(256) k_head_lift(const __grid_constant__ HeadArgs a)
 {
     __shared__ int32_t tops[8];
@@ -718,7 +721,7 @@ static __global__ void __launch_bounds__(256) k_head_lift(const __grid_constant_
 }
 
 // Rows of the weights that are not aligned to 16 bytes, a piece of them, to rows that are.  Eight blocks an SM, two
-// rounds of them (five in 48 registers: 3 us more for 49 MB).
+// rounds of them, in 32 registers, which spills 28 bytes (five in 48 registers: 3 us more for 49 MB).
 static __global__ void __launch_bounds__(256, 8) k_head_weights(const __grid_constant__ HeadArgs a)
 {
     let_next_begin();
@@ -1495,7 +1498,9 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
     const float common = counted > 0 ? common_factor(a) : 0.0f;
     const HeadShape x = head_shape<HEAD_INPUT>(a, counted), w = head_shape<HEAD_WEIGHT>(a, counted);
     const uint32_t of_x = a.dx && x.ranges > 1 ? x.rest * 128 : 0, of_w = a.dw && w.ranges > 1 ? w.rest * 128 : 0;
-    // by blocks if there are too few units for warps
+    // by blocks if there are too few units for warps, two a block at most.  dw of 4096 rows of 64, whole calls: 4 tiles
+    // of 256 tokens 35.4 us by blocks and 36.2 by warps, 6 tiles 37.0 and 36.9, 8 tiles 38.9 and 37.2; dx of 16 rows
+    // over 50257 tokens, where seven units of eight have no rows: 4 tiles 66 and 72, 8 tiles 100 and 102.
     if (of_x + of_w <= 2 * gridDim.x) {
         for (uint32_t unit = blockIdx.x; unit < of_x + of_w; unit += gridDim.x) {
             if (unit < of_x) join<DT, HEAD_INPUT, true>(a, x, unit, counted, top, common, turn);
@@ -1513,7 +1518,8 @@ __global__ void __launch_bounds__(256) k_head_join(const __grid_constant__ HeadA
 // 32 counted rows a block: first a lane a row, the 32 warps sharing the tiles' maxima and sums, then a
 // warp a row.  The last block to finish adds the blocks' sums in order.  Bound by latency: 7 us for 16 rows of 197
 // tiles, 15 for 8192 of 501 (33 MB).
-// Blocks that have an SM to themselves take eight tiles at a time, others two.
+// Blocks that have an SM to themselves take eight tiles at a time, others two (two blocks an SM have 32 registers a
+// thread, and that spills 56 bytes).
 template <int BLOCKS>
 static __global__ void __launch_bounds__(1024, BLOCKS) k_head_loss(const __grid_constant__ HeadArgs a, int tiles)
 {
